@@ -1,0 +1,191 @@
+"""GPU tests of the mixture-of-experts layer against the float64 oracle, whose bound on what
+the fp32 sums and the 16-bit hidden values can do is derived in ``mx4_oracle.moe_layer``;
+the output's own rounding is half a step of its type."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from int8_mixed_precision_col_amd import binding, moe, mx4
+from oracle import mx4_oracle as ref
+from tests.gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+F16, B16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def prepared(w, fmt):
+    """(prepared pair, float64 values) of weight rows w."""
+    if fmt == "mx4":
+        return mx4.prepare_weight(w, 1), ref.mx4_round(f64(w))
+    Wq, aw = binding.prepare_weight(w.half().contiguous(), 1)
+    q, a = oracle.prepare_weight(w.half().cpu().numpy().T.copy())
+    assert np.array_equal(binding.untile_weight(Wq, w.shape[1]).cpu().numpy(), q)
+    return (Wq, aw), oracle.dequantize(q, a[:, None])
+
+
+def case(T, D, I, E, dtype, fmt, seed, scale=0.05):
+    g = torch.Generator().manual_seed(seed)
+    X = torch.randn((T, D), generator=g).to(dtype).cuda()
+    logits = torch.randn((T, E), generator=g) * 2
+    w13 = (torch.randn((E * 2 * I, D), generator=g) * scale).to(dtype).cuda()
+    w2 = (torch.randn((E * D, I), generator=g) * scale).to(dtype).cuda()
+    p13, v13 = prepared(w13, fmt)
+    p2, v2 = prepared(w2, fmt)
+    return X, logits, (p13, p2), (v13.reshape(E, 2 * I, D), v2.reshape(E, D, I))
+
+
+def check(X, logits, pairs, values, k, renorm, **kw):
+    dtype = X.dtype
+    y, ids, w = moe.moe_layer(X, logits.cuda(), *pairs, k, renormalize=renorm, **kw)
+    Y, want_ids, want_w, bound = ref.moe_layer(f64(X), f64(logits), *values, k, renorm)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    assert np.abs(f64(w) - want_w).max() <= 1e-6
+    tiny = 2.0 ** -25 if dtype == F16 else 2.0 ** -134
+    bound = bound + (np.abs(Y) + bound) * torch.finfo(dtype).eps / 2 + tiny
+    err = np.abs(f64(y) - Y)
+    assert np.isfinite(err).all() and (err <= bound).all(), (err / bound).max()
+    return y
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mx4"])
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("T,D,I,E,k,renorm", [
+    (1, 16, 16, 1, 1, True), (1, 512, 256, 8, 2, True), (5, 528, 144, 10, 3, False), (16, 1040, 528, 4, 4, True),
+    (16, 256, 128, 70, 8, False), (9, 144, 48, 500, 16, True), (2, 2064, 32, 3, 1, False), (16, 128, 1040, 2, 2, False),
+    (13, 640, 272, 64, 6, True),
+])
+def test_layer(T, D, I, E, k, renorm, dtype, fmt):
+    announce(f"moe T={T} D={D} I={I} E={E} k={k} {dtype} {fmt}")
+    X, logits, pairs, values = case(T, D, I, E, dtype, fmt, T * D + E)
+    y = check(X, logits, pairs, values, k, renorm)
+    for ld in (F16, B16):
+        check(X, logits.to(ld), pairs, values, k, renorm)
+    assert torch.equal(y, moe.moe_layer(X, logits.cuda(), *pairs, k, renormalize=renorm)[0])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mx4"])
+def test_masks_ties_and_padding_tokens(fmt):
+    X, logits, pairs, values = case(6, 272, 80, 12, F16, fmt, 1)
+    inf = float("inf")
+    logits[0] = -inf                    # a padding row
+    logits[1, :11] = -inf               # one expert left
+    logits[2] = 0.5                     # all tied
+    logits[3, 4:] = logits[3, 3]        # tied in part
+    logits[4] = torch.finfo(F32).min    # the lowest value is no mask
+    logits[4, 7] = -inf
+    logits[5, 2], logits[5, 9] = 0.0, -0.0
+    logits[5, [0, 1, 3, 4, 5, 6, 7, 8, 10, 11]] = -1.0
+    announce(f"moe masks {fmt}")
+    for renorm in (True, False):
+        y = check(X, logits, pairs, values, 4, renorm)
+        assert int(torch.count_nonzero(y[0])) == 0
+    logits[:] = -inf
+    y, ids, w = moe.moe_layer(X, logits.cuda(), *pairs, 4)
+    assert int(torch.count_nonzero(y)) == 0 and int((ids != -1).sum()) == 0 and int(torch.count_nonzero(w)) == 0
+
+
+def test_padding_tokens_are_not_read():
+    """What an off token's row of X holds reaches nobody's output."""
+    X, logits, pairs, values = case(5, 272, 80, 8, F16, "mx4", 2)
+    logits[3] = -float("inf")
+    want = moe.moe_layer(X, logits.cuda(), *pairs, 2)[0]
+    X[3] = float("nan")
+    got = moe.moe_layer(X, logits.cuda(), *pairs, 2)[0]
+    assert torch.equal(got, want) and int(torch.count_nonzero(got[3])) == 0
+
+
+def test_nan_and_inf_reach_their_own_token_only():
+    X, logits, pairs, values = case(6, 272, 80, 8, B16, "int8", 3)
+    logits[1, 5] = float("nan")
+    logits[2, 3] = float("inf")
+    X[4, 100] = float("inf")
+    y, ids, _ = moe.moe_layer(X, logits.cuda(), *pairs, 2)
+    assert torch.isfinite(y).all(1).cpu().tolist() == [True, False, False, True, False, True]
+    assert int(ids[1, 0]) == 5 and int(ids[2, 0]) == 3
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mx4"])
+@pytest.mark.parametrize("dtype", [F16, B16])
+def test_every_token_chooses_the_same_experts(dtype, fmt):
+    X, logits, pairs, values = case(16, 528, 144, 6, dtype, fmt, 4)
+    logits[:] = logits[0]
+    announce(f"moe all tokens at the same experts {dtype} {fmt}")
+    check(X, logits, pairs, values, 3, True)
+
+
+def test_hidden_values_beyond_fp16():
+    """|h| passes 65504 while the output stays in range: no infinity in between."""
+    X, logits, pairs, values = case(3, 512, 64, 4, F16, "mx4", 5, scale=0.25)
+    X *= 64
+    w2 = (torch.randn((4 * 512, 64), generator=torch.Generator().manual_seed(9)) * 2.0 ** -12).half().cuda()
+    p2, v2 = prepared(w2, "mx4")
+    h = np.abs(np.einsum("eid,td->tei", values[0], f64(X))).max()
+    assert h ** 2 > 65504
+    check(X, logits, (pairs[0], p2), (values[0], v2.reshape(4, 512, 64)), 2, True)
+
+
+def test_strides_workspace_out_and_guard():
+    X, logits, pairs, values = case(7, 272, 80, 8, F16, "mx4", 6)
+    wide = torch.zeros((7, 400), dtype=F16, device="cuda")
+    wide[:, 64:336] = X
+    want = check(X, logits, pairs, values, 2, True)
+    guard = torch.full((7 * 272 + 64,), 3.0, dtype=F16, device="cuda")
+    work = torch.randint(0, 256, (moe.workspace_bytes(7, 80, 2),), dtype=torch.uint8, device="cuda")
+    y, _, _ = moe.moe_layer(wide[:, 64:336], logits.cuda(), *pairs, 2, workspace=work, out=guard[:7 * 272].view(7, 272))
+    assert torch.equal(y, want) and bool((guard[7 * 272:] == 3.0).all())
+    with pytest.raises(binding.Int8mmError):
+        moe.moe_layer(X, logits.cuda(), *pairs, 2, workspace=work[:256])
+    with pytest.raises(binding.Int8mmError):
+        moe.moe_layer(X, logits.cuda(), *pairs, 9)
+
+
+def test_streams_and_graph():
+    X, logits, pairs, _ = case(7, 272, 80, 8, F16, "int8", 7)
+    X2, logits2, pairs2, _ = case(16, 272, 80, 8, B16, "mx4", 8)
+    l1, l2 = logits.cuda(), logits2.cuda()
+    want = moe.moe_layer(X, l1, *pairs, 2)[0], moe.moe_layer(X2, l2, *pairs2, 3)[0]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            a = moe.moe_layer(X, l1, *pairs, 2)[0]
+        with torch.cuda.stream(s2):
+            b = moe.moe_layer(X2, l2, *pairs2, 3)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    work = torch.empty(moe.workspace_bytes(7, 80, 2), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(X)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, ids, w = moe.moe_layer(X, l1, *pairs, 2, workspace=work, out=out)
+    for seed in range(3):
+        l1.copy_(torch.randn((7, 8), generator=torch.Generator().manual_seed(seed)))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = moe.moe_layer(X, l1, *pairs, 2)
+        assert torch.equal(out, want[0]) and torch.equal(ids, want[1]) and torch.equal(w, want[2])
+
+
+def test_a_decode_step_with_the_operators_together():
+    """A few tokens: router logits by the MX4 weight-only product, the layer on MX4 experts,
+    its output quantized for the next product; each stage against its oracle on its own input."""
+    T, D, I, E, k = 6, 528, 144, 16, 4
+    X, _, pairs, values = case(T, D, I, E, B16, "mx4", 11)
+    g = torch.Generator().manual_seed(12)
+    router = (torch.randn((E, D), generator=g) * 0.2).to(B16).cuda()
+    logits = mx4.weight_only_matmul(X, *mx4.prepare_weight(router, 1))
+    y = check(X, logits.cpu(), pairs, values, k, True)
+    nxt = (torch.randn((272, D), generator=g) * 0.05).to(B16).cuda()
+    W = mx4.prepare_weight(nxt, 1)
+    z = f64(mx4.matmul(y, *W))
+    a, b = ref.mx4_round(f64(y)), ref.mx4_round(f64(nxt))
+    S = np.abs(a) @ np.abs(b).T
+    assert (np.abs(z - a @ b.T) <= S * (5 + 32) * 2.0 ** -23 + np.abs(a @ b.T) * 2.0 ** -8 * 1.01 + 1e-30).all()
