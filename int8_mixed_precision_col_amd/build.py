@@ -20,8 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libint8mm.so")
 SOURCES = ["prepare.hip", "quant.hip", "gemm.hip", "gemm_skinny.hip", "decode.hip", "weight_only.hip",
-           "int8mm_abi.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_weight_only.hip", "moe.hip",
-           "mx4_abi.hip"]
+           "int8mm_abi.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_few.hip",
+           "mx4_weight_only.hip", "moe.hip", "mx4_abi.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [

@@ -37,6 +37,11 @@ __host__ __device__ __forceinline__ int mx_ks(int64_t K) {
 }
 __host__ __device__ __forceinline__ int mx_quads(int64_t K) { return (mx_ks(K) + 3) >> 2; }
 
+// The scale operand of the conversion instructions for byte b: they read its exponent field
+// alone, as a power of two from 2^-127 (field 0) to 2^127, and as NaN for 255 (checked for
+// every byte and code).
+__device__ __forceinline__ float mx_scale_operand(unsigned b) { return __builtin_bit_cast(float, b << 23); }
+
 // fp32 of a scale byte: 2^(b - 127), NaN for 255. Byte 0 is the subnormal 2^-127.
 __device__ __forceinline__ float mx_scale(unsigned b) {
   const unsigned u = b == 0 ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23;
@@ -97,17 +102,18 @@ __device__ __forceinline__ unsigned mx_scale_byte(unsigned exponent) {
   return exponent >= 255u ? 255u : exponent >= 2u ? exponent - 2u : 0u;
 }
 
-// Codes of 8 elements under scale byte b (zeros where b is 255). The conversion
-// instruction divides by the power of two and rounds half-even with saturation at 6.
+// Codes of 8 elements under scale byte b. The conversion instruction divides by the power of
+// two and rounds half-even with saturation at 6. Under 255 the codes mean nothing: what is
+// stored has zeros there.
 template <class T>
 __device__ __forceinline__ unsigned mx_codes8(const v4u& x, unsigned b) {
-  const float s = mx_scale(b);
+  const float s = mx_scale_operand(b);
   unsigned c = 0;
   c = T::template to_fp4<0>(c, x[0], s);
   c = T::template to_fp4<1>(c, x[1], s);
   c = T::template to_fp4<2>(c, x[2], s);
   c = T::template to_fp4<3>(c, x[3], s);
-  return b == 255u ? 0u : c;
+  return c;
 }
 
 // 8 codes -> 8 elements of T times s.
@@ -137,6 +143,22 @@ __device__ __forceinline__ unsigned max_over_groups(unsigned v) {
   v = max(static_cast<unsigned>(a[0]), static_cast<unsigned>(a[1]));
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return max(static_cast<unsigned>(b[0]), static_cast<unsigned>(b[1]));
+}
+
+constexpr unsigned kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;  // DPP quad_perm [1,0,3,2], [2,3,0,1]
+
+// Largest value over each aligned group of four lanes.
+__device__ __forceinline__ unsigned max_of_four_lanes(unsigned v) {
+  v = max(v, static_cast<unsigned>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), kQuadXor1, 0xF, 0xF, true)));
+  return max(v, static_cast<unsigned>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), kQuadXor2, 0xF, 0xF, true)));
+}
+
+// The wave's own LDS traffic: its writes are done before its later reads, and its reads
+// before later writes (other waves have other buffers, so no barrier).
+__device__ __forceinline__ void wave_lds_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xF | (0x7 << 4) | (0x0 << 8) | (0x3 << 14));  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
 }
 
 }  // namespace i8mm

@@ -38,11 +38,14 @@ hipError_t run_quantize(const void* X, int64_t M, int64_t K, int64_t ldx, int dt
   return i8mm::launch_mx_quantize(a, dtype, s);
 }
 
-hipError_t run_gemm(const uint8_t* xc, const void* xs, int64_t M, int64_t K, const uint8_t* wc,
-                    const void* ws, int64_t N, int dtype, void* Y, hipStream_t s) {
-  i8mm::MxGemmArgs a{xc, static_cast<const uint32_t*>(xs), wc, static_cast<const uint32_t*>(ws),
-                     int(M), int(N), int(K), Y, int(N)};
-  return i8mm::launch_mx_gemm(a, dtype, s);
+i8mm::MxGemmArgs gemm_args(const uint8_t* xc, const void* xs, int64_t M, int64_t K, const uint8_t* wc,
+                           const void* ws, int64_t N, void* Y) {
+  return {xc, static_cast<const uint32_t*>(xs), wc, static_cast<const uint32_t*>(ws), int(M), int(N), int(K),
+          Y, int(N)};
+}
+
+hipError_t run_gemm(const i8mm::MxGemmArgs& a, int dtype, hipStream_t s) {
+  return i8mm::mx_few(a.M) ? i8mm::launch_mx_few(a, dtype, s) : i8mm::launch_mx_gemm(a, dtype, s);
 }
 
 }  // namespace
@@ -109,11 +112,14 @@ int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype, cons
   if (!aligned16(X) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y) || !aligned16(workspace))
     return INT8MM_E_ALIGN;
   if (workspace_bytes < need) return INT8MM_E_WORKSPACE;
+  if (i8mm::mx_few_inline(M, ldx))
+    return hip_status(i8mm::launch_mx_few_inline(gemm_args(nullptr, nullptr, M, K, w_codes, w_scales, N, Y), X, ldx,
+                                                 dtype, stream));
   uint8_t* xc = static_cast<uint8_t*>(workspace);
   uint8_t* xs = xc + round256(codes_bytes(M, K));
   const hipError_t e = run_quantize(X, M, K, ldx, dtype, xc, xs, stream);
   if (e != hipSuccess) return INT8MM_E_HIP;
-  return hip_status(run_gemm(xc, xs, M, K, w_codes, w_scales, N, dtype, Y, stream));
+  return hip_status(run_gemm(gemm_args(xc, xs, M, K, w_codes, w_scales, N, Y), dtype, stream));
 }
 
 int mx4_matmul_q(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
@@ -123,7 +129,7 @@ int mx4_matmul_q(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int
   if (mx4_matmul_workspace_bytes(M, K, N) == 0 || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y))
     return INT8MM_E_ALIGN;
-  return hip_status(run_gemm(x_codes, x_scales, M, K, w_codes, w_scales, N, dtype, Y, stream));
+  return hip_status(run_gemm(gemm_args(x_codes, x_scales, M, K, w_codes, w_scales, N, Y), dtype, stream));
 }
 
 int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype,

@@ -1,0 +1,151 @@
+// MX4 product for a few tokens (M <= 64): a weight stream instead of output tiles.
+//
+// With so few rows the product is bound by reading W4 once from HBM, and 128 x 128 tiles
+// would leave most of the GPU idle and multiply padding rows. A workgroup owns 16 RG output
+// features and all of M; its waves share the quads of K (four 128-element units each) and
+// their fp32 partial sums meet in LDS. Each unit is one operand of
+// v_mfma_scale_f32_16x16x128_f8f6f4, straight from global memory to registers.
+// Up to 16 tokens X is quantized on the way (INLINE) and the call is one launch: a wave loads
+// a row's whole quad at once (1 KB, a lane holds 8 elements and four lanes a block), and the
+// codes and scale bytes go through a buffer of its own in LDS into operand order. Loading
+// 16-bit X in operand order instead takes 16 gathers per quad whatever the number of rows.
+#include "mx4.hpp"
+#include "mx4_launch.hpp"
+
+namespace i8mm {
+
+constexpr int kFewWaves = 8;
+// bytes of a quantized row's quad in LDS: 256 of codes, 16 of scales, and a skew that puts
+// the 16 rows of an operand read on distinct banks
+constexpr int kFewStride = 256 + 16;
+
+template <class T, int G, int RG, bool INLINE>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const void* X, int64_t ldx) {
+  static_assert(!INLINE || G == 1, "one row group is quantized in registers");
+  __shared__ float red[kFewWaves][16 * G][16 * RG + 1];
+  __shared__ __attribute__((aligned(16))) char s_x[INLINE ? kFewWaves * 16 * kFewStride : 16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int row = lane & 15;
+  const int ks = mx_ks(a.K), quads = mx_quads(a.K);
+  const int groups = a.N / 16, m_groups = (a.M + 15) / 16;
+  const int g0 = blockIdx.x * RG;
+  char* buf = s_x + (INLINE ? wave * 16 * kFewStride : 0);
+  const unsigned lane_off = (lane & 15) * kUnitK + 16 * (lane >> 4);
+
+  v4u w[RG][4], x[G][4];
+  unsigned ws[RG], xs[G];
+  const __amdgpu_buffer_rsrc_t xr =
+      make_rsrc(X, INLINE ? static_cast<unsigned>(((a.M - 1) * ldx + a.K) * 2) : 0u);
+  // units past ks repeat the last one, under padding scales (or, INLINE, zeros)
+  auto load = [&](int q) {
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      const size_t g = min(g0 + r, groups - 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[r][j] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(
+            a.Wc + (g * ks + min(4 * q + j, ks - 1)) * kUnitBytes + lane_off));
+      ws[r] = a.Ws[(g * quads + q) * 64 + lane];
+    }
+    if constexpr (!INLINE) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const size_t g = min(i, m_groups - 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[i][j] = *reinterpret_cast<const v4u*>(a.Xc + (g * ks + min(4 * q + j, ks - 1)) * kUnitBytes + lane_off);
+        xs[i] = a.Xs[(g * quads + q) * 64 + lane];
+      }
+    }
+  };
+  v4f acc[G][RG] = {};
+  for (int q = wave; q < quads; q += kFewWaves) {
+    v4u raw[INLINE ? 16 : 1];
+    if constexpr (INLINE) {
+      const int k = 512 * q + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < a.M) raw[i] = buf_load16(xr, k < a.K ? static_cast<unsigned>(i * ldx + k) * 2u : kOOB);
+    }
+    load(q);
+    if constexpr (INLINE) {
+      wave_lds_fence();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < a.M) {
+          const unsigned b = mx_scale_byte(T::exponent(max_of_four_lanes(mx_max_bits(raw[i]))));
+          *reinterpret_cast<unsigned*>(buf + i * kFewStride + 4 * lane) = mx_codes8<T>(raw[i], b);
+          // block (lane / 4) % 4 of unit lane / 16: byte `unit` of the block's dword
+          if ((lane & 3) == 0) buf[i * kFewStride + 256 + (lane & 12) + (lane >> 4)] = static_cast<char>(b);
+        }
+      wave_lds_fence();
+      const char* p = buf + min(row, a.M - 1) * kFewStride;  // rows past M repeat the last
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[0][j] = *reinterpret_cast<const v4u*>(p + 64 * j + 16 * (lane >> 4));
+      xs[0] = *reinterpret_cast<const unsigned*>(p + 256 + 4 * (lane >> 4));
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        acc[i][r] = mx_mfma<0>(x[i][0], w[r][0], acc[i][r], xs[i], ws[r]);
+        acc[i][r] = mx_mfma<1>(x[i][1], w[r][1], acc[i][r], xs[i], ws[r]);
+        acc[i][r] = mx_mfma<2>(x[i][2], w[r][2], acc[i][r], xs[i], ws[r]);
+        acc[i][r] = mx_mfma<3>(x[i][3], w[r][3], acc[i][r], xs[i], ws[r]);
+      }
+  }
+  // lane l, register e: token 4 (l / 16) + e, feature l % 16
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][16 * i + 4 * (lane >> 4) + e][16 * r + row] = acc[i][r][e];
+  lds_barrier();
+  for (int o = tid; o < 256 * G * RG; o += 64 * kFewWaves) {
+    const int m = o / (16 * RG), n = o % (16 * RG);
+    if (m >= a.M || g0 * 16 + n >= a.N) continue;
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kFewWaves; ++v) s += red[v][m][n];
+    static_cast<typename T::elem*>(a.Y)[static_cast<size_t>(m) * a.ldy + g0 * 16 + n] = T::round(s);
+  }
+}
+
+template <int G, int RG, bool INLINE>
+static hipError_t run(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
+  const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kFewWaves);
+  if (type == kMxF16) hipLaunchKernelGGL((k_mx_few<F16, G, RG, INLINE>), grid, block, 0, s, a, X, ldx);
+  else hipLaunchKernelGGL((k_mx_few<B16, G, RG, INLINE>), grid, block, 0, s, a, X, ldx);
+  return hipGetLastError();
+}
+
+bool mx_few_inline(int64_t M, int64_t ldx) { return M <= 16 && M * ldx < (int64_t(1) << 30); }
+
+// Row groups per workgroup: about one workgroup per CU, up to 4. Measured per call (HIP
+// graphs over rotated weights, fp16, M = 8, RG = 1 / 2 / 4): 8192 x 1024 (K x N) 5.6 / 6.5 /
+// 9.7 us, 4096 x 4096 4.9 / 5.2 / 6.3, 8192 x 8192 10.9 / 9.2 / 11.2, 4096 x 16384 11.1 /
+// 10.2 / 8.9.
+static int few_row_groups(int N) { return N < 16 * 512 ? 1 : N < 16 * 1024 ? 2 : 4; }
+
+template <int G, bool INLINE>
+static hipError_t pick(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
+  const int rg = few_row_groups(a.N);
+  if (rg == 1) return run<G, 1, INLINE>(a, X, ldx, type, s);
+  return rg == 2 ? run<G, 2, INLINE>(a, X, ldx, type, s) : run<G, 4, INLINE>(a, X, ldx, type, s);
+}
+
+hipError_t launch_mx_few_inline(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
+  return pick<1, true>(a, X, ldx, type, s);
+}
+
+// Up to 64 rows: at 64 the tiles are slower still (4096 x 4096 11.3 against 5.9 us, 4096 x
+// 16384 12.7 against 11.2, 8192 x 8192 20.0 against 11.9).
+bool mx_few(int64_t M) { return M <= 64; }
+
+hipError_t launch_mx_few(const MxGemmArgs& a, int type, hipStream_t s) {
+  if (a.M <= 16) return pick<1, false>(a, nullptr, 0, type, s);
+  return a.M <= 32 ? pick<2, false>(a, nullptr, 0, type, s) : pick<4, false>(a, nullptr, 0, type, s);
+}
+
+}  // namespace i8mm

@@ -7,14 +7,6 @@
 
 namespace i8mm {
 
-constexpr unsigned kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;  // DPP quad_perm [1,0,3,2], [2,3,0,1]
-
-// Largest value over each aligned group of four lanes.
-__device__ __forceinline__ unsigned max_of_four_lanes(unsigned v) {
-  v = max(v, static_cast<unsigned>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), kQuadXor1, 0xF, 0xF, true)));
-  return max(v, static_cast<unsigned>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), kQuadXor2, 0xF, 0xF, true)));
-}
-
 // One workgroup per 16 rows x 512 elements (one quad), a wave per 4 rows: lane l holds row
 // l / 16, elements 8 (l % 16) .. + 7 of each of the quad's four units, so that a wave reads
 // 256 contiguous bytes of 4 rows per load and writes 256 contiguous bytes of codes per
@@ -41,7 +33,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a) {
     scale |= b << (8 * u);
     if (4 * q + u < ks)
       *reinterpret_cast<unsigned*>(a.codes + (grp * ks + 4 * q + u) * kUnitBytes + r * kUnitK + 4 * c) =
-          mx_codes8<T>(x[u], b);
+          b == 255u ? 0u : mx_codes8<T>(x[u], b);
   }
   if ((c & 3) == 0) a.scales[(grp * quads + q) * 64 + 16 * (c >> 2) + r] = scale;
 }
@@ -91,7 +83,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize_cols(const uint16_t* W, int
       const unsigned b = mx_scale_byte(T::exponent(top));
       v4u o;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) o[p] = mx_codes8<T>(v[p], b);
+      for (int p = 0; p < 4; ++p) o[p] = b == 255u ? 0u : mx_codes8<T>(v[p], b);
       *reinterpret_cast<v4u*>(codes + (grp * ks + 4 * q + u) * kUnitBytes + (r + j) * kUnitK + 16 * g) = o;
       scale[j] |= b << (8 * u);
     }
@@ -162,7 +154,7 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a) {
   for (int u = 0; u < 4; ++u) {
     const int k = 512 * q + 128 * u + 8 * c;
     if (k >= a.K) continue;
-    const float s = mx_scale((scale >> (8 * u)) & 255u);
+    const float s = mx_scale_operand((scale >> (8 * u)) & 255u);
     if constexpr (TYPE == kMxF32) {
       float* dst = static_cast<float*>(a.out) + row * a.ldo + k;
       const v2f p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v[u], s, 0);

@@ -1,7 +1,7 @@
 // Weight-only MX4 product for at most 16 tokens: Y = X W4^T with 16-bit X (fp16 or bf16),
 // fp32 accumulation, one rounding.
 //
-// One workgroup per 16 output features; its waves share the quads of K and their partial
+// One workgroup per 16 RG output features; its waves share the quads of K and their partial
 // sums meet in LDS (weight_stream.hpp has the arithmetic of a quad).
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
@@ -10,40 +10,64 @@ namespace i8mm {
 
 constexpr int kMxWoWaves = 8;
 
-template <class T>
+template <class T, int RG>
 __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnlyArgs a) {
-  __shared__ float red[kMxWoWaves][16][17];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tok = lane & 15;
-  const int ks = mx_ks(a.K), quads = mx_quads(a.K);
-  // rows past M and elements past K are out of the resource's range and read zeros
+  extern __shared__ __attribute__((aligned(16))) char s_x[];  // [waves][M][kActStride]
+  __shared__ float red[kMxWoWaves][16][16 * RG + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int row = lane & 15;
+  const int ks = mx_ks(a.K), quads = mx_quads(a.K), groups = a.N / 16;
+  const int g0 = blockIdx.x * RG;
+  char* buf = s_x + wave * a.M * kActStride;
+  // elements past K are out of the resource's range and read zeros
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.M - 1) * a.ldx + a.K) * 2));
-  const unsigned row = static_cast<unsigned>(tok * a.ldx);
-  v4f acc = {};
+  const int M = a.M, mrow = min(row, M - 1);  // rows past M repeat the last (outputs discarded)
+  v4f acc[RG] = {};
   for (int q = wave; q < quads; q += kMxWoWaves) {
-    WeightQuad<true> w;
+    WeightQuad<true> w[RG];
     ActQuad<true> x;
-    w.load(a.Wc, a.Ws, blockIdx.x, ks, quads, q, lane);
-    x.load(q, lane, [&](int k) { return buf_load16(xr, tok < a.M && k < a.K ? (row + k) * 2u : kOOB); });
-    mma_quad<T, true>(x, w, acc);
+    x.load(xr, q, a.K, M, lane, [&](int i) { return i < M ? static_cast<unsigned>(i * a.ldx) * 2u : kOOB; });
+#pragma unroll
+    for (int r = 0; r < RG; ++r) w[r].load(a.Wc, a.Ws, min(g0 + r, groups - 1), ks, quads, q, lane);
+    mma_quad<T, true, RG>(
+        w, acc,
+        [&](int p) {
+          wave_lds_fence();
+          x.stage(p, buf, M, lane, [](int i) { return i; });
+          wave_lds_fence();
+        },
+        [&](int, int j, int v) { return act_operand<true>(buf, mrow, j, v, lane); });
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) red[wave][4 * (lane >> 4) + e][tok] = acc[e];
+  for (int r = 0; r < RG; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[wave][4 * (lane >> 4) + e][16 * r + row] = acc[r][e];
   lds_barrier();
-  const int m = tid >> 4, nl = tid & 15;
-  if (m < a.M) {
+  for (int o = tid; o < 256 * RG; o += 64 * kMxWoWaves) {
+    const int m = o / (16 * RG), n = o % (16 * RG);
+    if (m >= M || g0 * 16 + n >= a.N) continue;
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kMxWoWaves; ++w) s += red[w][m][nl];
-    static_cast<typename T::elem*>(a.Y)[static_cast<size_t>(m) * a.N + blockIdx.x * 16 + nl] = T::round(s);
+    for (int v = 0; v < kMxWoWaves; ++v) s += red[v][m][n];
+    static_cast<typename T::elem*>(a.Y)[static_cast<size_t>(m) * a.N + g0 * 16 + n] = T::round(s);
   }
 }
 
-hipError_t launch_mx_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
-  const dim3 grid(a.N / 16);
-  if (type == kMxF16) hipLaunchKernelGGL(k_mx_weight_only<F16>, grid, dim3(64 * kMxWoWaves), 0, s, a);
-  else hipLaunchKernelGGL(k_mx_weight_only<B16>, grid, dim3(64 * kMxWoWaves), 0, s, a);
+template <int RG>
+static hipError_t run_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
+  const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kMxWoWaves);
+  const size_t lds = static_cast<size_t>(kMxWoWaves) * a.M * kActStride;
+  if (type == kMxF16) hipLaunchKernelGGL((k_mx_weight_only<F16, RG>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_mx_weight_only<B16, RG>), grid, block, lds, s, a);
   return hipGetLastError();
+}
+
+hipError_t launch_mx_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
+  // row groups per workgroup: about one workgroup per CU, up to 4 (per call, M = 8, RG = 1 / 2 /
+  // 4: 4096 x 4096 (K x N) 4.7 / 5.3 / 7.3 us, 8192 x 8192 12.1 / 9.3 / 11.7, 4096 x 16384
+  // 14.0 / 10.9 / 9.8)
+  if (a.N < 16 * 512) return run_weight_only<1>(a, type, s);
+  return a.N < 16 * 1024 ? run_weight_only<2>(a, type, s) : run_weight_only<4>(a, type, s);
 }
 
 }  // namespace i8mm

@@ -66,53 +66,111 @@ struct WeightQuad {
   }
 };
 
-// The activations of one quad: x(k) returns the 8 elements at k .. k + 7 of the lane's row.
+// The activations of one quad of K: loaded whole rows at a time (512 bytes, 256 elements,
+// half a wave per row; an MX4 quad has two such pieces), then put through the wave's own LDS
+// buffer into operand order. Loading the operand straight from memory takes XV 16-byte
+// gathers per unit whatever the number of rows, and those, not the weight, then set the time
+// (MX4, 1 x 4096 x 4096: 6.1 us per call; 4.6 so); this takes one load per two rows and piece.
+constexpr int kActPiece = 256;                       // elements
+constexpr int kActStride = kActPiece * 2 + 16;       // bytes between rows in LDS: a 16-byte
+                                                     // skew, so the 16 rows hit distinct banks
 template <bool MX>
 struct ActQuad {
-  v4u x[4][WeightFmt<MX>::XV];
+  static constexpr int P = MX ? 2 : 1;
+  v4u raw[P][8];
+
+  // rows: how many (uniform, at most 16); row i's byte offset is off(i) (kOOB: zeros)
   template <class F>
-  __device__ __forceinline__ void load(int q, int lane, F f) {
-    constexpr int UK = WeightFmt<MX>::UK, KL = WeightFmt<MX>::KL;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int q, int K, int rows, int lane, F off) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int p = 0; p < P; ++p) {
+      const int k = (P * q + p) * kActPiece + 8 * (lane & 31);
 #pragma unroll
-      for (int v = 0; v < WeightFmt<MX>::XV; ++v) x[j][v] = f(4 * UK * q + UK * j + KL * (lane >> 4) + 8 * v);
+      for (int i = 0; i < 8; ++i)
+        if (2 * i < rows) {
+          const unsigned o = off(2 * i + (lane >> 5));
+          raw[p][i] = buf_load16(r, o != kOOB && k < K ? o + 2u * k : kOOB);
+        }
+    }
+  }
+  // piece p into the wave's buffer; slot(i): the buffer row of row i
+  template <class F>
+  __device__ __forceinline__ void stage(int p, char* buf, int rows, int lane, F slot) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (2 * i + (lane >> 5) < rows)
+        *reinterpret_cast<v4u*>(buf + slot(2 * i + (lane >> 5)) * kActStride + 16 * (lane & 31)) = raw[p][i];
   }
 };
 
-// acc += X_quad W_quad^T; the int8 column constant is left to the caller.
-template <class T, bool MX>
-__device__ __forceinline__ void mma_quad(const ActQuad<MX>& x, const WeightQuad<MX>& w, v4f& acc) {
+// The operand of unit j of piece p: 8 elements at KL (l / 16) + 8 v of buffer row `row`.
+template <bool MX>
+__device__ __forceinline__ v4u act_operand(const char* buf, int row, int j, int v, int lane) {
+  constexpr int UK = WeightFmt<MX>::UK, KL = WeightFmt<MX>::KL;
+  return *reinterpret_cast<const v4u*>(buf + row * kActStride + 2 * (UK * j + KL * (lane >> 4) + 8 * v));
+}
+
+// acc[r] += X_quad W_quad[r]^T for RG row groups of the weight that share the activations
+// x(p, j, v): the operand of unit j of piece p (the int8 column constants are left to the
+// caller). `stage(p)` makes piece p available.
+template <class T, bool MX, int RG, class Stage, class X>
+__device__ __forceinline__ void mma_quad(const WeightQuad<MX> (&w)[RG], v4f (&acc)[RG], Stage stage, X x) {
   if constexpr (!MX) {
+    stage(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const v2u h0 = int8x4_to16<T>(w.w[j][0]), h1 = int8x4_to16<T>(w.w[j][1]);
-      const v2u h2 = int8x4_to16<T>(w.w[j][2]), h3 = int8x4_to16<T>(w.w[j][3]);
-      acc = T::mfma(x.x[j][0], v4u{h0[0], h0[1], h1[0], h1[1]}, acc);
-      acc = T::mfma(x.x[j][1], v4u{h2[0], h2[1], h3[0], h3[1]}, acc);
-    }
-  } else if constexpr (T::bf) {
+      const v4u x0 = x(0, j, 0), x1 = x(0, j, 1);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float s = mx_scale((w.s >> (8 * j)) & 255u);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc = T::mfma(x.x[j][v], mx_values8<T>(w.w[j][v], s), acc);
+      for (int r = 0; r < RG; ++r) {
+        const v2u h0 = int8x4_to16<T>(w[r].w[j][0]), h1 = int8x4_to16<T>(w[r].w[j][1]);
+        const v2u h2 = int8x4_to16<T>(w[r].w[j][2]), h3 = int8x4_to16<T>(w[r].w[j][3]);
+        acc[r] = T::mfma(x0, v4u{h0[0], h0[1], h1[0], h1[1]}, acc[r]);
+        acc[r] = T::mfma(x1, v4u{h2[0], h2[1], h3[0], h3[1]}, acc[r]);
+      }
     }
   } else {
-    const unsigned t = pk_max_u16(w.s & 0x00ff00ffu, (w.s >> 8) & 0x00ff00ffu);
-    const unsigned ref = max_over_groups(max(t & 0xffffu, t >> 16));
-    v4f part = {};
+    unsigned ref[RG];
+    v4f part[RG];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned b = (w.s >> (8 * j)) & 255u;
-      // 2^(b - ref), at least the smallest normal; NaN for a NaN block
-      const float s = mx_scale(b == 255u ? 255u : static_cast<unsigned>(max(static_cast<int>(127 + b - ref), 1)));
-#pragma unroll
-      for (int v = 0; v < 4; ++v) part = T::mfma(x.x[j][v], mx_values8<T>(w.w[j][v], s), part);
+    for (int r = 0; r < RG; ++r) {
+      if constexpr (!T::bf) {
+        const unsigned t = pk_max_u16(w[r].s & 0x00ff00ffu, (w[r].s >> 8) & 0x00ff00ffu);
+        ref[r] = max_over_groups(max(t & 0xffffu, t >> 16));
+        part[r] = v4f{};
+      } else {
+        part[r] = acc[r];
+      }
     }
-    const float back = mx_scale(ref);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], back, acc[e]);
+    for (int p = 0; p < 2; ++p) {
+      stage(p);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float s[RG];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          const unsigned b = (w[r].s >> (8 * (2 * p + j))) & 255u;
+          // fp16: 2^(b - ref), at least the smallest normal; NaN for a NaN block
+          s[r] = mx_scale_operand(T::bf || b == 255u ? b : static_cast<unsigned>(max(static_cast<int>(127 + b - ref[r]), 1)));
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const v4u xv = x(p, j, v);
+#pragma unroll
+          for (int r = 0; r < RG; ++r) part[r] = T::mfma(xv, mx_values8<T>(w[r].w[2 * p + j][v], s[r]), part[r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      if constexpr (!T::bf) {
+        const float back = mx_scale(ref[r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] = __builtin_fmaf(part[r][e], back, acc[r][e]);
+      } else {
+        acc[r] = part[r];
+      }
+    }
   }
 }
 
