@@ -8,9 +8,11 @@
 // of y. It is the weights of the chosen experts that bound it: each is read once.
 //
 // k_moe_gate_up: every workgroup works out the routing for itself (T x E logits, a few KB
-// from L2, one wave per token) rather than wait for a launch of its own; workgroup (i, s)
-// then takes rows 16 i .. of the gate and of the up part of the s-th chosen expert, against
-// the tokens that chose it, and writes their hidden values.
+// from L2, one wave per token) rather than wait for a launch of its own. The gate and up rows
+// of all chosen experts, 16 + 16 features at a time, are one list of steps that the
+// workgroups share evenly, whatever the number of experts turns out to be; a workgroup goes
+// over its part with the next step's weights in flight while it multiplies, adds up its
+// waves and writes the hidden values of the tokens that chose the expert.
 // k_moe_down: a workgroup per 16 output features goes over all chosen experts, its waves
 // sharing the (expert, K quad) items in order, so that the weighted sum over experts needs
 // neither atomics nor a third launch and is the same on every run.
@@ -25,16 +27,8 @@
 
 namespace i8mm {
 
-constexpr int kMoeWaves = 8;
-constexpr int kMoeMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
+constexpr int kMoeMaxLists = kMoeMaxTokens * kMoeMaxTopK;
 constexpr int kMoeExpertWords = kMoeMaxExperts / 32;
-
-// What k_moe_gate_up leaves for k_moe_down: per chosen expert its index and its tokens in
-// ascending order, each a byte 16 t + (the expert's place in token t's list).
-struct MoeSlot {
-  uint32_t expert, count;
-  uint8_t token[kMoeMaxTokens];
-};
 
 __device__ __forceinline__ float moe_logit(const void* p, int type, int64_t i) {
   if (type == kMxF32) return static_cast<const float*>(p)[i];
@@ -56,263 +50,332 @@ __device__ __forceinline__ float moe_unkey(unsigned k) {
   return __builtin_bit_cast(float, k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
-// One wave: the list of token t into ids [k] and weights [k] (id -1 and weight 0 past the
-// last expert that is on).
-__device__ __forceinline__ void moe_route(const MoeArgs& a, int t, int lane, int* ids, float* weights) {
-  constexpr int V = kMoeMaxExperts / 64;
-  const int per = (a.E + 63) / 64;  // lane's experts: per * lane ..
+// The chosen experts of all tokens, in LDS: a bit per expert that some token chose, and per
+// expert the mask of its tokens and its place in each one's list. The experts are used in
+// ascending order; `slot` is a place there.
+struct MoeTable {
+  unsigned on[kMoeExpertWords], tokens[kMoeMaxExperts];
+  uint8_t place[kMoeMaxExperts * kMoeMaxTokens];
+
+  __device__ __forceinline__ void clear(int tid, int threads) {
+    if (tid < kMoeExpertWords) on[tid] = 0u;
+    for (int i = tid; i < kMoeMaxExperts; i += threads) tokens[i] = 0u;
+  }
+  __device__ __forceinline__ void add(int expert, int t, int j) {
+    atomicOr(&on[expert >> 5], 1u << (expert & 31));
+    atomicOr(&tokens[expert], 1u << t);
+    place[expert * kMoeMaxTokens + t] = static_cast<uint8_t>(j);
+  }
+};
+
+// A wave's view of MoeTable::on: word i and the number of experts up to its end in lane i.
+struct MoeOrder {
+  int word, upto;
+  __device__ __forceinline__ MoeOrder(const MoeTable& t, int lane) {
+    word = lane < kMoeExpertWords ? static_cast<int>(t.on[lane]) : 0;
+    upto = wave_prefix_sum(__builtin_popcount(static_cast<unsigned>(word)));
+  }
+  __device__ __forceinline__ int count() const { return __builtin_amdgcn_readlane(upto, 63); }
+  __device__ __forceinline__ int expert(int slot) const {  // slot < count()
+    const int at = __builtin_ctzll(__ballot(upto > slot));
+    unsigned bits = static_cast<unsigned>(__builtin_amdgcn_readlane(word, at));
+    int before = slot - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(bits));
+    while (before-- > 0) bits &= bits - 1;
+    return 32 * at + __builtin_ctz(bits);
+  }
+};
+
+// One wave: routes token t and enters its experts into the
+// table; writes the list where ids and weights are given (id -1 and weight 0 past the last
+// expert that is on). Lane l holds experts V l .. V l + V - 1, so that the lowest lane and
+// then the lowest of its experts is the lowest index.
+template <int V>
+__device__ __forceinline__ void moe_route(const MoeArgs& a, int t, int lane, MoeTable& table, int* ids,
+                                          float* weights) {
   unsigned key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = per * lane + i;
-    key[i] = i < per && e < a.E ? moe_key(moe_logit(a.logits, a.logits_type, static_cast<int64_t>(t) * a.E + e)) : 0u;
+    const int e = V * lane + i;
+    key[i] = e < a.E ? moe_key(moe_logit(a.logits, a.logits_type, static_cast<int64_t>(t) * a.E + e)) : 0u;
   }
-  unsigned first = 0;   // the largest key
-  float all = 0.0f;     // sum over every expert
-  float mine = 0.0f;    // lane j: weight of place j, unnormalized
+  unsigned kept[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) kept[i] = key[i];
+  unsigned first = 0, mine = 0;  // the largest key; lane j: that of place j
   int mine_id = -1;
-  float chosen = 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    unsigned best = 0;
+    unsigned best = key[0];
     int at = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 1; i < V; ++i)
       if (key[i] > best) {
         best = key[i];
         at = i;
       }
     const unsigned top = wave_max_u32(best);
-    if (j == 0) {
-      first = top;
-      if (!a.renormalize) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) all += key[i] ? expf(moe_unkey(key[i]) - moe_unkey(top)) : 0.0f;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, 64);
-      }
-    }
     if (top == 0u) break;  // no expert left
+    if (j == 0) first = top;
     const int who = __builtin_ctzll(__ballot(best == top));
-    const int id = per * who + __builtin_amdgcn_readlane(at, who);
-    const float w = expf(moe_unkey(top) - moe_unkey(first));
-    chosen += w;
+    const int id = V * who + (V > 1 ? __builtin_amdgcn_readlane(at, who) : 0);
     if (lane == j) {
-      mine = w;
+      mine = top;
       mine_id = id;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane == who && i == at) key[i] = 0u;
+      if (V * lane + i == id) key[i] = 0u;
   }
+  if (mine_id >= 0) table.add(mine_id, t, lane);
+  if (!ids) return;
+  const float most = moe_unkey(first);
+  const float w = mine ? expf(moe_unkey(mine) - most) : 0.0f;
+  float sum = w;
+  if (!a.renormalize) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += kept[i] ? expf(moe_unkey(kept[i]) - most) : 0.0f;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if (lane < a.k) {
-    ids[lane] = mine_id;
-    weights[lane] = mine_id < 0 ? 0.0f : __fdiv_rn(mine, a.renormalize ? chosen : all);
+    const float p = mine_id < 0 ? 0.0f : __fdiv_rn(w, sum);
+    const int o = t * a.k + lane;
+    ids[o] = mine_id;
+    weights[o] = p;
+    if (a.ids) a.ids[o] = mine_id;
+    if (a.weights) a.weights[o] = p;
   }
 }
 
+constexpr int kUpWaves = 8;
+// LDS for the activations of k_moe_gate_up: with all of X in it (T x D up to 64 K elements) X
+// is read once per workgroup, while the routing is worked out; otherwise each wave reads the
+// quad it multiplies, of the tokens that chose the expert.
+constexpr int kUpResident = 132 << 10;
+template <bool MX>
+__host__ __device__ __forceinline__ bool up_resident(int T, int quads) {
+  return quads * act_bytes<MX>(T) <= kUpResident;
+}
+
 template <class T, bool MX>
-__global__ __launch_bounds__(64 * kMoeWaves) void k_moe_gate_up(MoeArgs a, MoeSlot* slots, float* weights) {
-  extern __shared__ __attribute__((aligned(16))) char s_x[];  // [waves][T][kActStride]
-  __shared__ int s_ids[kMoeMaxSlots];
-  __shared__ float s_w[kMoeMaxSlots];
-  __shared__ unsigned s_on[kMoeExpertWords], s_tokens, s_mask[kMoeMaxSlots];
-  __shared__ uint8_t s_token[kMoeMaxTokens];
-  __shared__ float red[kMoeWaves][2][16][17];
+__global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* ids, float* weights) {
+  extern __shared__ __attribute__((aligned(16))) char s_x[];  // [quads or waves][act_bytes(T)]
+  __shared__ MoeTable table;
+  __shared__ float red[kUpWaves][2][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (tid < kMoeExpertWords) s_on[tid] = 0u;
-  if (tid == kMoeExpertWords) s_tokens = 0u;
-  if (tid < kMoeMaxSlots) s_mask[tid] = 0u;
-  for (int t = wave; t < a.T; t += kMoeWaves) moe_route(a, t, lane, s_ids + t * a.k, s_w + t * a.k);
-  lds_barrier();
-  const int n_lists = a.T * a.k;
-  const int my_id = tid < n_lists ? s_ids[tid] : -1;
-  if (my_id >= 0) atomicOr(&s_on[my_id >> 5], 1u << (my_id & 31));
+  constexpr int UK = WeightFmt<MX>::UK;
+  const int ks = (a.D + UK - 1) / UK, quads = (ks + 3) >> 2, groups = a.I / 16;
+  const bool resident = up_resident<MX>(a.T, quads);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.T - 1) * a.ldx + a.D) * 2));
+  table.clear(tid, 64 * kUpWaves);
   lds_barrier();
   // One workgroup writes what the second launch goes by, all of it from its own view of the
   // logits, so that it is consistent whatever else happens to them meanwhile.
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    const int t = tid / a.k;
-    int rank = 0;
-    if (my_id >= 0) {
-      for (int i = 0; i < my_id >> 5; ++i) rank += __builtin_popcount(s_on[i]);
-      rank += __builtin_popcount(s_on[my_id >> 5] & ((1u << (my_id & 31)) - 1));
-      atomicOr(&s_mask[rank], 1u << t);
-    }
-    lds_barrier();
-    if (tid < n_lists) {
-      weights[tid] = s_w[tid];
-      if (a.ids) a.ids[tid] = my_id;
-      if (a.weights) a.weights[tid] = s_w[tid];
-    }
-    if (my_id >= 0) {
-      const unsigned mask = s_mask[rank];
-      const int c = __builtin_popcount(mask & ((1u << t) - 1));
-      slots[rank].token[c] = static_cast<uint8_t>(16 * t + (tid - t * a.k));
-      if (c == 0) {
-        slots[rank].expert = static_cast<uint32_t>(my_id);
-        slots[rank].count = static_cast<uint32_t>(__builtin_popcount(mask));
-      }
-    }
-    if (tid < gridDim.y && s_mask[tid] == 0u) slots[tid].count = 0u;
+  int* out_ids = blockIdx.x == 0 ? ids : nullptr;
+  for (int t = wave; t < a.T; t += kUpWaves) {
+    if (a.E <= 64) moe_route<1>(a, t, lane, table, out_ids, weights);
+    else if (a.E <= 128) moe_route<2>(a, t, lane, table, out_ids, weights);
+    else moe_route<kMoeMaxExperts / 64>(a, t, lane, table, out_ids, weights);
   }
-  // this workgroup's expert: the blockIdx.y-th that is on
-  const int word = lane < kMoeExpertWords ? static_cast<int>(s_on[lane]) : 0;
-  const int upto = wave_prefix_sum(__builtin_popcount(static_cast<unsigned>(word)));
-  const int slot = blockIdx.y;
-  const uint64_t past = __ballot(upto > slot);
-  if (past == 0) return;  // fewer experts are on
-  const int at = __builtin_ctzll(past);
-  unsigned bits = static_cast<unsigned>(__builtin_amdgcn_readlane(word, at));
-  int before = slot - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(bits));
-  while (before-- > 0) bits &= bits - 1;
-  const int expert = 32 * at + __builtin_ctz(bits);
-  if (my_id == expert) atomicOr(&s_tokens, 1u << (tid / a.k));
+  if (resident)
+    for (int q = wave; q < quads; q += kUpWaves) {
+      ActQuad<MX, 16> x;
+      x.load(xr, q, a.D, a.T, lane, [&](int t) { return static_cast<unsigned>(t * a.ldx) * 2u; });
+      x.store(s_x + q * act_bytes<MX>(a.T), a.T, a.T, lane);
+    }
   lds_barrier();
-  const unsigned tokens = s_tokens;
-  const int count = __builtin_popcount(tokens);
-  if (my_id == expert) {
-    const int t = tid / a.k, c = __builtin_popcount(tokens & ((1u << t) - 1));
-    s_token[c] = static_cast<uint8_t>(16 * t + (tid - t * a.k));
-  }
-  lds_barrier();
+  const MoeOrder order(table, lane);
 
-  constexpr int UK = WeightFmt<MX>::UK;
-  const int ks = (a.D + UK - 1) / UK, quads = (ks + 3) >> 2;
-  const size_t gate = static_cast<size_t>(expert) * 2 * (a.I / 16) + blockIdx.x, up = gate + a.I / 16;
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.T - 1) * a.ldx + a.D) * 2));
-  char* buf = s_x + wave * a.T * kActStride;
-  const int row = min(lane & 15, count - 1);  // rows past the last token repeat it (discarded)
-  v4f acc[2] = {};
-  for (int q = wave; q < quads; q += kMoeWaves) {
-    WeightQuad<MX> w[2];
-    ActQuad<MX> x;
-    x.load(xr, q, a.D, count, lane, [&](int i) {
-      return i < count ? static_cast<unsigned>((s_token[i] >> 4) * a.ldx) * 2u : kOOB; });
-    w[0].load(a.w13, static_cast<const uint32_t*>(a.s13), gate, ks, quads, q, lane);
-    w[1].load(a.w13, static_cast<const uint32_t*>(a.s13), up, ks, quads, q, lane);
-    mma_quad<T, MX, 2>(
-        w, acc,
-        [&](int p) {
-          wave_lds_fence();
-          x.stage(p, buf, count, lane, [](int i) { return i; });
-          wave_lds_fence();
-        },
-        [&](int, int j, int v) { return act_operand<MX>(buf, row, j, v, lane); });
-  }
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][p][4 * (lane >> 4) + e][lane & 15] = acc[p][e];
-  lds_barrier();
-  const int c = tid >> 4, n = tid & 15;
-  if (c < count) {
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kMoeWaves; ++w) {
-      g += red[w][0][c][n];
-      u += red[w][1][c][n];
+  // A step is `par` neighbouring 16-feature groups of one expert, `share` waves on the quads
+  // of each: with fewer quads than waves the waves take several groups at once.
+  const int share = quads >= 5 ? 8 : quads >= 3 ? 4 : quads, par = kUpWaves / share;
+  const int steps = (groups + par - 1) / par;
+  const int64_t all = static_cast<int64_t>(order.count()) * steps;
+  const int first = static_cast<int>(all * blockIdx.x / gridDim.x);
+  const int last = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+  const int sub = wave / share, kk = wave - sub * share;
+
+  WeightQuad<MX> next[2];
+  int next_slot = -1, next_expert = 0;
+  auto prefetch = [&](int step, int q) {
+    const int slot = step / steps;
+    if (slot != next_slot) {
+      next_slot = slot;
+      next_expert = order.expert(slot);
     }
-    if constexpr (!MX) {
-      const float* aw = static_cast<const float*>(a.s13);
-      g *= __fdiv_rn(aw[gate * 16 + n], 127.0f);
-      u *= __fdiv_rn(aw[up * 16 + n], 127.0f);
+    const int group = min((step - slot * steps) * par + sub, groups - 1);
+    const size_t gate = static_cast<size_t>(next_expert) * 2 * groups + group;
+    next[0].load(a.w13, static_cast<const uint32_t*>(a.s13), gate, ks, quads, q, lane);
+    next[1].load(a.w13, static_cast<const uint32_t*>(a.s13), gate + groups, ks, quads, q, lane);
+  };
+  if (first < last && kk < quads) prefetch(first, kk);
+  int slot = -1, expert = 0;
+  unsigned tokens = 0;
+  const int row = min(lane & 15, a.T - 1);  // rows past T repeat the last (discarded)
+  for (int step = first; step < last; ++step) {
+    if (step / steps != slot) {
+      slot = step / steps;
+      expert = order.expert(slot);
+      tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
     }
-    const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
-    const __bf16 hi = static_cast<__bf16>(h);
-    const float rest = h - static_cast<float>(hi);
-    const __bf16 lo = static_cast<__bf16>(fabsf(rest) < __builtin_inff() ? rest : 0.0f);
-    const int list = (s_token[c] >> 4) * a.k + (s_token[c] & 15);
-    const size_t o = static_cast<size_t>(list) * a.I + blockIdx.x * 16 + n;
-    a.h[o] = __builtin_bit_cast(uint16_t, hi);
-    a.h[static_cast<size_t>(n_lists) * a.I + o] = __builtin_bit_cast(uint16_t, lo);
+    v4f acc[2] = {};
+    for (int q = kk; q < quads; q += share) {
+      const char* buf = s_x + (resident ? q : wave) * act_bytes<MX>(a.T);
+      if (!resident) {
+        ActQuad<MX, 16> x;
+        x.load(xr, q, a.D, a.T, lane, [&](int t) {
+          return (tokens >> t) & 1u ? static_cast<unsigned>(t * a.ldx) * 2u : kOOB; });
+        wave_lds_fence();
+        x.store(s_x + wave * act_bytes<MX>(a.T), a.T, a.T, lane);
+        wave_lds_fence();
+      }
+      WeightQuad<MX> w[2] = {next[0], next[1]};
+      if (q + share < quads) prefetch(step, q + share);
+      else if (step + 1 < last) prefetch(step + 1, kk);
+      mma_quad<T, MX, 2>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, a.T, row, j, v, lane); });
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][p][4 * (lane >> 4) + e][lane & 15] = acc[p][e];
+    lds_barrier();
+    for (int o = tid; o < 256 * par; o += 64 * kUpWaves) {
+      const int n = o & 15, t = (o >> 4) & 15, s = o >> 8;
+      const int group = (step - slot * steps) * par + s;
+      if (group >= groups || !((tokens >> t) & 1u)) continue;
+      float g = 0.0f, u = 0.0f;
+      for (int w = 0; w < share; ++w) {
+        g += red[s * share + w][0][t][n];
+        u += red[s * share + w][1][t][n];
+      }
+      if constexpr (!MX) {
+        const float* aw = static_cast<const float*>(a.s13) + (static_cast<size_t>(expert) * 2 * groups + group) * 16 + n;
+        g *= __fdiv_rn(aw[0], 127.0f);
+        u *= __fdiv_rn(aw[a.I], 127.0f);
+      }
+      const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
+      const __bf16 hi = static_cast<__bf16>(h);
+      const float rest = h - static_cast<float>(hi);
+      const __bf16 lo = static_cast<__bf16>(fabsf(rest) < __builtin_inff() ? rest : 0.0f);
+      const int list = t * a.k + table.place[expert * kMoeMaxTokens + t];
+      const size_t at = static_cast<size_t>(list) * a.I + group * 16 + n;
+      a.h[at] = __builtin_bit_cast(uint16_t, hi);
+      a.h[static_cast<size_t>(a.T * a.k) * a.I + at] = __builtin_bit_cast(uint16_t, lo);
+    }
+    lds_barrier();  // red is read
   }
 }
 
-// Rows that a pass of k_moe_down stages: the high parts and the remainders of 8 tokens.
-__host__ __device__ __forceinline__ int moe_down_rows(int T) { return 2 * (T < 8 ? T : 8); }
-
-template <class T, bool MX>
-__global__ __launch_bounds__(64 * kMoeWaves) void k_moe_down(MoeArgs a, const MoeSlot* slots, const float* weights,
-                                                             int n_slots) {
-  // [waves][moe_down_rows(T)][kActStride], then the slots, then the weights
-  extern __shared__ __attribute__((aligned(16))) char s_x[];
-  __shared__ float total[kMoeWaves][kMoeMaxTokens][17];
-  __shared__ int s_n;
+// WAVES waves; a pass over an expert's quads serves TOK of its tokens (2 TOK rows: high parts
+// and remainders).
+template <class T, bool MX, int WAVES, int TOK>
+__global__ __launch_bounds__(64 * WAVES) void k_moe_down(MoeArgs a, const int* ids, const float* weights) {
+  constexpr int ROWS = 2 * TOK;
+  __shared__ __attribute__((aligned(16))) char s_x[WAVES * ROWS * kActStride];
+  __shared__ MoeTable table;
+  __shared__ float s_w[kMoeMaxLists];
+  __shared__ float total[WAVES][kMoeMaxTokens][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_lists = a.T * a.k;
-  char* buf = s_x + wave * moe_down_rows(a.T) * kActStride;
-  MoeSlot* s_slot = reinterpret_cast<MoeSlot*>(s_x + kMoeWaves * moe_down_rows(a.T) * kActStride);
-  float* s_w = reinterpret_cast<float*>(s_slot + n_slots);
-  if (tid == 0) s_n = 0;
-  lds_barrier();
-  if (tid < n_slots) {
-    // Addresses come out of these: kept in range here too, so that a workspace that another
-    // call wrote to meanwhile, which the interface forbids, gives wrong values at worst.
-    MoeSlot v = slots[tid];
-    v.expert = min(v.expert, static_cast<uint32_t>(a.E - 1));
-    v.count = min(v.count, static_cast<uint32_t>(a.T));
-    for (int c = 0; c < kMoeMaxTokens; ++c)
-      v.token[c] = static_cast<uint8_t>(16 * min(v.token[c] >> 4, a.T - 1) + min(v.token[c] & 15, a.k - 1));
-    s_slot[tid] = v;
-    if (v.count) atomicMax(&s_n, tid + 1);  // the slots in use come first
+  char* buf = s_x + wave * ROWS * kActStride;
+  int id = -1;
+  float weight = 0.0f;
+  if (tid < n_lists) {
+    id = ids[tid];
+    weight = weights[tid];
   }
-  if (tid < n_lists) s_w[tid] = weights[tid];
+  table.clear(tid, 64 * WAVES);
   for (int i = lane; i < kMoeMaxTokens * 17; i += 64) (&total[wave][0][0])[i] = 0.0f;
   lds_barrier();
-  const int n = s_n;
+  if (tid < n_lists) {
+    // Addresses come out of the ids: checked here too, so that a workspace that another call
+    // wrote to meanwhile, which the interface forbids, gives wrong values at worst.
+    if (id >= 0 && id < a.E) table.add(id, tid / a.k, tid % a.k);
+    s_w[tid] = weight;
+  }
+  lds_barrier();
+  const MoeOrder order(table, lane);
 
   constexpr int UK = WeightFmt<MX>::UK;
   const int ks = (a.I + UK - 1) / UK, quads = (ks + 3) >> 2;
-  const int items = n * quads, per = (items + kMoeWaves - 1) / kMoeWaves;
-  const int end = min(items, per * (wave + 1));
+  const int items = order.count() * quads, per = (items + WAVES - 1) / WAVES;
+  const int begin = min(items, per * wave), end = min(items, begin + per);
   const unsigned plane = static_cast<unsigned>(n_lists) * a.I * 2u;  // bytes
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, plane * 2u);
   const int r = lane & 15, g = lane >> 4;
-  for (int i = per * wave; i < end;) {
-    const int slot = i / quads;
-    const int stop = min(end, (slot + 1) * quads);
-    const MoeSlot& s = s_slot[slot];
-    const size_t group = static_cast<size_t>(s.expert) * (a.D / 16) + blockIdx.x;
-    const int count = __builtin_amdgcn_readfirstlane(static_cast<int>(s.count));
-    v4f acc[2][1] = {};
-    for (; i < stop; ++i) {
-      const int q = i - slot * quads;
-      WeightQuad<MX> w[1];
-      w[0].load(a.w2, static_cast<const uint32_t*>(a.s2), group, ks, quads, q, lane);
+  WeightQuad<MX> next;
+  auto prefetch = [&](int expert, int q) {
+    next.load(a.w2, static_cast<const uint32_t*>(a.s2), static_cast<size_t>(expert) * (a.D / 16) + blockIdx.x, ks, quads,
+              q, lane);
+  };
+  int slot = begin / quads, expert = 0;
+  if (begin < end) {
+    expert = order.expert(slot);
+    prefetch(expert, begin - slot * quads);
+  }
+  for (int i = begin; i < end; ++slot) {
+    // items [i, stop) are quads of one expert, the wave's share of it
+    const int q0 = i - slot * quads, stop = min(end, (slot + 1) * quads), q1 = stop - slot * quads;
+    const unsigned tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
+    const int count = __builtin_popcount(tokens), current = expert;
+    i = stop;
+    auto list_of = [&](int c) {  // list entry of the expert's c-th token
+      unsigned m = tokens;
+      for (int j = 0; j < c; ++j) m &= m - 1;
+      const int t = __builtin_ctz(m);
+      return t * a.k + table.place[current * kMoeMaxTokens + t];
+    };
+    for (int c0 = 0; c0 < count; c0 += TOK) {
+      const int m = min(count - c0, TOK);
+      const bool last = c0 + TOK >= count;
+      // this lane's rows: byte offsets of rows 2 j + l / 32 in h
+      unsigned off[TOK];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int m = min(count - 8 * p, 8);  // tokens of this pass
-        if (m <= 0) break;                    // wave-uniform
-        ActQuad<MX> x;
-        x.load(hr, q, a.I, 2 * m, lane, [&](int j) -> unsigned {
-          if (j >= 2 * m) return kOOB;
-          const unsigned e = s.token[8 * p + (j < m ? j : j - m)];
-          return ((e >> 4) * a.k + (e & 15u)) * a.I * 2u + (j < m ? 0u : plane);
-        });
-        // operand rows 0-7 are the high parts, 8-15 the remainders; past the last token repeats
-        const int row = min(r & 7, m - 1) + (r < 8 ? 0 : m);
-        mma_quad<B16, MX, 1>(
-            w, acc[p],
-            [&](int piece) {
-              wave_lds_fence();
-              x.stage(piece, buf, 2 * m, lane, [](int j) { return j; });
-              wave_lds_fence();
-            },
-            [&](int, int j, int v) { return act_operand<MX>(buf, row, j, v, lane); });
+      for (int j = 0; j < TOK; ++j) {
+        const int row = 2 * j + (lane >> 5);
+        off[j] = row < 2 * m ? static_cast<unsigned>(list_of(c0 + (row < m ? row : row - m))) * a.I * 2u +
+                                   (row < m ? 0u : plane)
+                             : kOOB;
       }
-    }
-    float scale = 1.0f;
-    if constexpr (!MX) scale = __fdiv_rn(static_cast<const float*>(a.s2)[group * 16 + r], 127.0f);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
+      // operand rows 0 .. TOK - 1 are the high parts, 8 .. the remainders; the others repeat one
+      const int row = min(r & 7, m - 1) + (r < 8 ? 0 : m);
+      v4f acc[1] = {};
+      for (int q = q0; q < q1; ++q) {
+        WeightQuad<MX> w[1] = {next};
+        ActQuad<MX, ROWS> x;
+        x.load(hr, q, a.I, 2 * m, lane, [&](int j) { return off[j >> 1]; });
+        if (q + 1 < q1) {
+          prefetch(expert, q + 1);
+        } else if (!last) {
+          prefetch(expert, q0);
+        } else if (i < end) {
+          expert = order.expert(slot + 1);
+          prefetch(expert, 0);
+        }
+        wave_lds_fence();
+        x.store_piece(0, buf, 2 * m, lane);
+        wave_lds_fence();
+        constexpr int HALF = MX ? 2 : 4;
+        mma_quad<B16, MX, 1, 0, HALF>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
+        if constexpr (MX) {
+          wave_lds_fence();
+          x.store_piece(1, buf, 2 * m, lane);
+          wave_lds_fence();
+          mma_quad<B16, MX, 1, 2, 4>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
+        }
+      }
+      // weigh the sums into the tokens'
+      float scale = 1.0f;
+      if constexpr (!MX)
+        scale = __fdiv_rn(static_cast<const float*>(a.s2)[static_cast<size_t>(current) * a.D + blockIdx.x * 16 + r], 127.0f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // rows 4 g + e (high) and 8 + 4 g + e (remainder) of one token are 32 lanes apart
-        const float y = acc[p][0][e] + __shfl_xor(acc[p][0][e], 32, 64);
-        const int c = 8 * p + 4 * (g & 1) + e;
-        if (g < 2 && c < count) {
-          const unsigned t = s.token[c] >> 4, place = s.token[c] & 15u;
-          total[wave][t][r] += y * scale * s_w[t * a.k + place];
+        // rows c (high) and 8 + c (remainder) of one token are 32 lanes apart
+        const float y = acc[0][e] + __shfl_xor(acc[0][e], 32, 64);
+        const int c = 4 * (g & 1) + e;
+        if (g < 2 && c < m) {
+          const int list = list_of(c0 + c);
+          total[wave][list / a.k][r] += y * scale * s_w[list];
         }
       }
     }
@@ -322,35 +385,44 @@ __global__ __launch_bounds__(64 * kMoeWaves) void k_moe_down(MoeArgs a, const Mo
   if (t < a.T) {
     float y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kMoeWaves; ++w) y += total[w][t][f];
+    for (int w = 0; w < WAVES; ++w) y += total[w][t][f];
     static_cast<typename T::elem*>(a.Y)[static_cast<size_t>(t) * a.D + blockIdx.x * 16 + f] = T::round(y);
   }
 }
 
-template <class T, bool MX>
-static hipError_t run(const MoeArgs& a, MoeSlot* slots, float* weights, hipStream_t s) {
-  const int n_slots = a.E < a.T * a.k ? a.E : a.T * a.k;
-  const size_t lds1 = static_cast<size_t>(kMoeWaves) * a.T * kActStride;
-  const size_t lds2 = static_cast<size_t>(kMoeWaves) * moe_down_rows(a.T) * kActStride + n_slots * sizeof(MoeSlot) +
-                      static_cast<size_t>(a.T) * a.k * sizeof(float);
-  hipLaunchKernelGGL((k_moe_gate_up<T, MX>), dim3(a.I / 16, n_slots), dim3(64 * kMoeWaves), lds1, s, a, slots, weights);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_moe_down<T, MX>), dim3(a.D / 16), dim3(64 * kMoeWaves), lds2, s, a, slots, weights, n_slots);
+constexpr int kMoeBlocks = 256;
+
+template <class T, bool MX, int WAVES, int TOK>
+static hipError_t run_down(const MoeArgs& a, const int* ids, const float* weights, hipStream_t s) {
+  hipLaunchKernelGGL((k_moe_down<T, MX, WAVES, TOK>), dim3(a.D / 16), dim3(64 * WAVES), 0, s, a, ids, weights);
   return hipGetLastError();
 }
 
-// Workspace: the slots, the weights, the hidden values.
+template <class T, bool MX>
+static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
+  const int n_slots = a.E < a.T * a.k ? a.E : a.T * a.k;
+  constexpr int UK = WeightFmt<MX>::UK;
+  const int quads = ((a.D + UK - 1) / UK + 3) / 4;
+  const size_t lds = static_cast<size_t>(up_resident<MX>(a.T, quads) ? quads : kUpWaves) * act_bytes<MX>(a.T);
+  const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16);
+  const unsigned blocks = static_cast<unsigned>(steps < kMoeBlocks ? steps : kMoeBlocks);
+  hipLaunchKernelGGL((k_moe_gate_up<T, MX>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, ids, weights);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return a.T * a.k > 3 * a.E ? run_down<T, MX, 8, 8>(a, ids, weights, s) : run_down<T, MX, 16, 4>(a, ids, weights, s);
+}
+
+// Workspace: the lists' ids and weights, then the hidden values.
 size_t moe_workspace(int T, int I, int k) {
-  return kMoeMaxSlots * (sizeof(MoeSlot) + sizeof(float)) + static_cast<size_t>(T) * k * I * 4;
+  return kMoeMaxLists * (sizeof(int) + sizeof(float)) + static_cast<size_t>(T) * k * I * 4;
 }
 
 hipError_t launch_moe(MoeArgs a, void* workspace, int type, bool mx4, hipStream_t s) {
-  MoeSlot* slots = static_cast<MoeSlot*>(workspace);
-  float* weights = reinterpret_cast<float*>(slots + kMoeMaxSlots);
-  a.h = reinterpret_cast<uint16_t*>(weights + kMoeMaxSlots);
-  if (type == kMxF16) return mx4 ? run<F16, true>(a, slots, weights, s) : run<F16, false>(a, slots, weights, s);
-  return mx4 ? run<B16, true>(a, slots, weights, s) : run<B16, false>(a, slots, weights, s);
+  int* ids = static_cast<int*>(workspace);
+  float* weights = reinterpret_cast<float*>(ids + kMoeMaxLists);
+  a.h = reinterpret_cast<uint16_t*>(weights + kMoeMaxLists);
+  if (type == kMxF16) return mx4 ? run<F16, true>(a, ids, weights, s) : run<F16, false>(a, ids, weights, s);
+  return mx4 ? run<B16, true>(a, ids, weights, s) : run<B16, false>(a, ids, weights, s);
 }
 
 }  // namespace i8mm

@@ -12,31 +12,27 @@ constexpr int kMxWoWaves = 8;
 
 template <class T, int RG>
 __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnlyArgs a) {
-  extern __shared__ __attribute__((aligned(16))) char s_x[];  // [waves][M][kActStride]
+  extern __shared__ __attribute__((aligned(16))) char s_x[];  // [waves][act_bytes(M)]
   __shared__ float red[kMxWoWaves][16][16 * RG + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15;
   const int ks = mx_ks(a.K), quads = mx_quads(a.K), groups = a.N / 16;
   const int g0 = blockIdx.x * RG;
-  char* buf = s_x + wave * a.M * kActStride;
+  char* buf = s_x + wave * act_bytes<true>(a.M);
   // elements past K are out of the resource's range and read zeros
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.M - 1) * a.ldx + a.K) * 2));
   const int M = a.M, mrow = min(row, M - 1);  // rows past M repeat the last (outputs discarded)
   v4f acc[RG] = {};
   for (int q = wave; q < quads; q += kMxWoWaves) {
     WeightQuad<true> w[RG];
-    ActQuad<true> x;
-    x.load(xr, q, a.K, M, lane, [&](int i) { return i < M ? static_cast<unsigned>(i * a.ldx) * 2u : kOOB; });
+    ActQuad<true, 16> x;
+    x.load(xr, q, a.K, M, lane, [&](int i) { return static_cast<unsigned>(i * a.ldx) * 2u; });
 #pragma unroll
     for (int r = 0; r < RG; ++r) w[r].load(a.Wc, a.Ws, min(g0 + r, groups - 1), ks, quads, q, lane);
-    mma_quad<T, true, RG>(
-        w, acc,
-        [&](int p) {
-          wave_lds_fence();
-          x.stage(p, buf, M, lane, [](int i) { return i; });
-          wave_lds_fence();
-        },
-        [&](int, int j, int v) { return act_operand<true>(buf, mrow, j, v, lane); });
+    wave_lds_fence();
+    x.store(buf, M, M, lane);
+    wave_lds_fence();
+    mma_quad<T, true, RG>(w, acc, [&](int j, int v) { return act_operand<true>(buf, M, mrow, j, v, lane); });
   }
 #pragma unroll
   for (int r = 0; r < RG; ++r)
@@ -56,7 +52,7 @@ __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnly
 template <int RG>
 static hipError_t run_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
   const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kMxWoWaves);
-  const size_t lds = static_cast<size_t>(kMxWoWaves) * a.M * kActStride;
+  const size_t lds = static_cast<size_t>(kMxWoWaves) * act_bytes<true>(a.M);
   if (type == kMxF16) hipLaunchKernelGGL((k_mx_weight_only<F16, RG>), grid, block, lds, s, a);
   else hipLaunchKernelGGL((k_mx_weight_only<B16, RG>), grid, block, lds, s, a);
   return hipGetLastError();

@@ -74,52 +74,64 @@ struct WeightQuad {
 constexpr int kActPiece = 256;                       // elements
 constexpr int kActStride = kActPiece * 2 + 16;       // bytes between rows in LDS: a 16-byte
                                                      // skew, so the 16 rows hit distinct banks
-template <bool MX>
+template <bool MX, int ROWS>
 struct ActQuad {
-  static constexpr int P = MX ? 2 : 1;
-  v4u raw[P][8];
+  static constexpr int P = MX ? 2 : 1;  // pieces of a quad
+  v4u raw[P][ROWS / 2];
 
-  // rows: how many (uniform, at most 16); row i's byte offset is off(i) (kOOB: zeros)
+  // the rows below `rows` (uniform, at most ROWS) of quad q; off(i): row i's byte offset, kOOB
+  // for a row of zeros
   template <class F>
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int q, int K, int rows, int lane, F off) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int k = (P * q + p) * kActPiece + 8 * (lane & 31);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < ROWS / 2; ++i)
         if (2 * i < rows) {
-          const unsigned o = off(2 * i + (lane >> 5));
+          const int row = 2 * i + (lane >> 5);
+          const unsigned o = row < rows ? off(row) : kOOB;
           raw[p][i] = buf_load16(r, o != kOOB && k < K ? o + 2u * k : kOOB);
         }
     }
   }
-  // piece p into the wave's buffer; slot(i): the buffer row of row i
-  template <class F>
-  __device__ __forceinline__ void stage(int p, char* buf, int rows, int lane, F slot) const {
+  // into LDS: row i of piece p at buf + i * kActStride
+  __device__ __forceinline__ void store_piece(int p, char* buf, int rows, int lane) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < ROWS / 2; ++i)
       if (2 * i + (lane >> 5) < rows)
-        *reinterpret_cast<v4u*>(buf + slot(2 * i + (lane >> 5)) * kActStride + 16 * (lane & 31)) = raw[p][i];
+        *reinterpret_cast<v4u*>(buf + (2 * i + (lane >> 5)) * kActStride + 16 * (lane & 31)) = raw[p][i];
+  }
+  // all pieces, `stride` rows each
+  __device__ __forceinline__ void store(char* buf, int stride, int rows, int lane) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) store_piece(p, buf + p * stride * kActStride, rows, lane);
   }
 };
-
-// The operand of unit j of piece p: 8 elements at KL (l / 16) + 8 v of buffer row `row`.
 template <bool MX>
-__device__ __forceinline__ v4u act_operand(const char* buf, int row, int j, int v, int lane) {
-  constexpr int UK = WeightFmt<MX>::UK, KL = WeightFmt<MX>::KL;
-  return *reinterpret_cast<const v4u*>(buf + row * kActStride + 2 * (UK * j + KL * (lane >> 4) + 8 * v));
+__host__ __device__ __forceinline__ constexpr int act_bytes(int rows) {
+  return (MX ? 2 : 1) * rows * kActStride;
+}
+
+// The operand of unit j (of the quad's 4), 16-byte part v, from rows that ActQuad stored with
+// `stride` rows per piece.
+template <bool MX>
+__device__ __forceinline__ v4u act_operand(const char* buf, int stride, int row, int j, int v, int lane) {
+  constexpr int UK = WeightFmt<MX>::UK, KL = WeightFmt<MX>::KL, PER = kActPiece / UK;  // units per piece
+  return *reinterpret_cast<const v4u*>(buf + ((j / PER) * stride + row) * kActStride +
+                                       2 * (UK * (j % PER) + KL * (lane >> 4) + 8 * v));
 }
 
 // acc[r] += X_quad W_quad[r]^T for RG row groups of the weight that share the activations
-// x(p, j, v): the operand of unit j of piece p (the int8 column constants are left to the
-// caller). `stage(p)` makes piece p available.
-template <class T, bool MX, int RG, class Stage, class X>
-__device__ __forceinline__ void mma_quad(const WeightQuad<MX> (&w)[RG], v4f (&acc)[RG], Stage stage, X x) {
+// x(j, v): 16-byte part v of unit j (the int8 column constants are left to the caller).
+// J0, J1: of units J0 .. J1 - 1 alone (MX4 in fp16: all four, its reference is theirs).
+template <class T, bool MX, int RG, int J0 = 0, int J1 = 4, class X>
+__device__ __forceinline__ void mma_quad(const WeightQuad<MX> (&w)[RG], v4f (&acc)[RG], X x) {
+  static_assert(!MX || T::bf || J1 - J0 == 4, "the reference of a quad");
   if constexpr (!MX) {
-    stage(0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const v4u x0 = x(0, j, 0), x1 = x(0, j, 1);
+    for (int j = J0; j < J1; ++j) {
+      const v4u x0 = x(j, 0), x1 = x(j, 1);
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
         const v2u h0 = int8x4_to16<T>(w[r].w[j][0]), h1 = int8x4_to16<T>(w[r].w[j][1]);
@@ -142,23 +154,19 @@ __device__ __forceinline__ void mma_quad(const WeightQuad<MX> (&w)[RG], v4f (&ac
       }
     }
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      stage(p);
+    for (int j = J0; j < J1; ++j) {
+      float s[RG];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float s[RG];
+      for (int r = 0; r < RG; ++r) {
+        const unsigned b = (w[r].s >> (8 * j)) & 255u;
+        // fp16: 2^(b - ref), at least the smallest normal; NaN for a NaN block
+        s[r] = mx_scale_operand(T::bf || b == 255u ? b : static_cast<unsigned>(max(static_cast<int>(127 + b - ref[r]), 1)));
+      }
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          const unsigned b = (w[r].s >> (8 * (2 * p + j))) & 255u;
-          // fp16: 2^(b - ref), at least the smallest normal; NaN for a NaN block
-          s[r] = mx_scale_operand(T::bf || b == 255u ? b : static_cast<unsigned>(max(static_cast<int>(127 + b - ref[r]), 1)));
-        }
+      for (int v = 0; v < 4; ++v) {
+        const v4u xv = x(j, v);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const v4u xv = x(p, j, v);
-#pragma unroll
-          for (int r = 0; r < RG; ++r) part[r] = T::mfma(xv, mx_values8<T>(w[r].w[2 * p + j][v], s[r]), part[r]);
-        }
+        for (int r = 0; r < RG; ++r) part[r] = T::mfma(xv, mx_values8<T>(w[r].w[j][v], s[r]), part[r]);
       }
     }
 #pragma unroll
