@@ -190,34 +190,28 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   // of each: with fewer quads than waves the waves take several groups at once.
   const int share = quads >= 5 ? 8 : quads >= 3 ? 4 : quads, par = kUpWaves / share;
   const int steps = (groups + par - 1) / par;
-  const int64_t all = static_cast<int64_t>(order.count()) * steps;
-  const int first = static_cast<int>(all * blockIdx.x / gridDim.x);
-  const int last = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+  // steps [first, last) of the list are this workgroup's
+  const unsigned all = static_cast<unsigned>(order.count() * steps), some = all / gridDim.x, more = all % gridDim.x;
+  const unsigned first = blockIdx.x * some + min(blockIdx.x, more);
+  const int n_steps = static_cast<int>(some + (blockIdx.x < more ? 1u : 0u));
+  if (n_steps == 0) return;
+  int slot = static_cast<int>(first / steps), in = static_cast<int>(first % steps);  // its place in the expert
   const int sub = wave / share, kk = wave - sub * share;
 
   WeightQuad<MX> next[2];
-  int next_slot = -1, next_expert = 0;
-  auto prefetch = [&](int step, int q) {
-    const int slot = step / steps;
-    if (slot != next_slot) {
-      next_slot = slot;
-      next_expert = order.expert(slot);
-    }
-    const int group = min((step - slot * steps) * par + sub, groups - 1);
-    const size_t gate = static_cast<size_t>(next_expert) * 2 * groups + group;
+  auto prefetch = [&](int e, int at, int q) {
+    const int group = min(at * par + sub, groups - 1);
+    const size_t gate = static_cast<size_t>(e) * 2 * groups + group;
     next[0].load(a.w13, static_cast<const uint32_t*>(a.s13), gate, ks, quads, q, lane);
     next[1].load(a.w13, static_cast<const uint32_t*>(a.s13), gate + groups, ks, quads, q, lane);
   };
-  if (first < last && kk < quads) prefetch(first, kk);
-  int slot = -1, expert = 0;
-  unsigned tokens = 0;
+  int expert = order.expert(slot);
+  if (kk < quads) prefetch(expert, in, kk);
   const int row = min(lane & 15, a.T - 1);  // rows past T repeat the last (discarded)
-  for (int step = first; step < last; ++step) {
-    if (step / steps != slot) {
-      slot = step / steps;
-      expert = order.expert(slot);
-      tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
-    }
+  for (int step = 0; step < n_steps; ++step) {
+    const unsigned tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
+    const int next_in = in + 1 < steps ? in + 1 : 0;
+    const int next_expert = next_in == 0 && step + 1 < n_steps ? order.expert(slot + 1) : expert;
     v4f acc[2] = {};
     for (int q = kk; q < quads; q += share) {
       const char* buf = s_x + (resident ? q : wave) * act_bytes<MX>(a.T);
@@ -230,8 +224,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
         wave_lds_fence();
       }
       WeightQuad<MX> w[2] = {next[0], next[1]};
-      if (q + share < quads) prefetch(step, q + share);
-      else if (step + 1 < last) prefetch(step + 1, kk);
+      if (q + share < quads) prefetch(expert, in, q + share);
+      else if (step + 1 < n_steps) prefetch(next_expert, next_in, kk);
       mma_quad<T, MX, 2>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, a.T, row, j, v, lane); });
     }
 #pragma unroll
@@ -241,7 +235,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
     lds_barrier();
     for (int o = tid; o < 256 * par; o += 64 * kUpWaves) {
       const int n = o & 15, t = (o >> 4) & 15, s = o >> 8;
-      const int group = (step - slot * steps) * par + s;
+      const int group = in * par + s;
       if (group >= groups || !((tokens >> t) & 1u)) continue;
       float g = 0.0f, u = 0.0f;
       for (int w = 0; w < share; ++w) {
@@ -263,6 +257,9 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
       a.h[static_cast<size_t>(a.T * a.k) * a.I + at] = __builtin_bit_cast(uint16_t, lo);
     }
     lds_barrier();  // red is read
+    slot += next_in == 0;
+    in = next_in;
+    expert = next_expert;
   }
 }
 

@@ -24,6 +24,10 @@ bool bad_dtype16(int t) { return t != MX4_F16 && t != MX4_BF16; }
 bool bad_dtype(int t) { return t < MX4_F16 || t > MX4_F32; }
 bool too_many(int64_t rows, int64_t K) { return rows > kMaxElements / K; }
 
+bool bad_product(int64_t M, int64_t K, int64_t N) {
+  return bad_m(M) || bad_k(K) || bad_n(N) || too_many(M, K) || too_many(N, K) || too_many(M, N);
+}
+
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t codes_bytes(int64_t rows, int64_t K) {
   return size_t((rows + 15) / 16) * i8mm::mx_ks(K) * i8mm::kUnitBytes;
@@ -99,22 +103,24 @@ int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64
 }
 
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (bad_m(M) || bad_k(K) || bad_n(N) || too_many(M, K) || too_many(N, K) || too_many(M, N)) return 0;
+  if (bad_product(M, K, N) || M <= kMaxFew) return 0;
   return round256(codes_bytes(M, K)) + scales_bytes(M, K);
 }
 
 int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype, const uint8_t* w_codes,
                const uint8_t* w_scales, int64_t N, void* Y, void* workspace, size_t workspace_bytes,
                hipStream_t stream) {
-  if (!X || !w_codes || !w_scales || !Y || !workspace) return INT8MM_E_NULL;
-  const size_t need = mx4_matmul_workspace_bytes(M, K, N);
-  if (need == 0 || bad_ld(ldx, K) || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
+  if (!X || !w_codes || !w_scales || !Y) return INT8MM_E_NULL;
+  if (bad_product(M, K, N) || bad_ld(ldx, K) || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
+  const bool few = M <= kMaxFew;
+  if (few && M * ldx >= kMaxBuffer) return INT8MM_E_SHAPE;
+  if (!few && !workspace) return INT8MM_E_NULL;
   if (!aligned16(X) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y) || !aligned16(workspace))
     return INT8MM_E_ALIGN;
-  if (workspace_bytes < need) return INT8MM_E_WORKSPACE;
-  if (i8mm::mx_few_inline(M, ldx))
+  if (few)
     return hip_status(i8mm::launch_mx_few_inline(gemm_args(nullptr, nullptr, M, K, w_codes, w_scales, N, Y), X, ldx,
                                                  dtype, stream));
+  if (workspace_bytes < mx4_matmul_workspace_bytes(M, K, N)) return INT8MM_E_WORKSPACE;
   uint8_t* xc = static_cast<uint8_t*>(workspace);
   uint8_t* xs = xc + round256(codes_bytes(M, K));
   const hipError_t e = run_quantize(X, M, K, ldx, dtype, xc, xs, stream);
@@ -126,7 +132,7 @@ int mx4_matmul_q(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int
                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int dtype, void* Y,
                  hipStream_t stream) {
   if (!x_codes || !x_scales || !w_codes || !w_scales || !Y) return INT8MM_E_NULL;
-  if (mx4_matmul_workspace_bytes(M, K, N) == 0 || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
+  if (bad_product(M, K, N) || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y))
     return INT8MM_E_ALIGN;
   return hip_status(run_gemm(gemm_args(x_codes, x_scales, M, K, w_codes, w_scales, N, Y), dtype, stream));

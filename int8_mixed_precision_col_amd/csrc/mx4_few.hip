@@ -120,8 +120,6 @@ static hipError_t run(const MxGemmArgs& a, const void* X, int64_t ldx, int type,
   return hipGetLastError();
 }
 
-bool mx_few_inline(int64_t M, int64_t ldx) { return M <= 16 && M * ldx < (int64_t(1) << 30); }
-
 // Row groups per workgroup: about one workgroup per CU, up to 4. Measured per call (HIP
 // graphs over rotated weights, fp16, M = 8, RG = 1 / 2 / 4): 8192 x 1024 (K x N) 5.6 / 6.5 /
 // 9.7 us, 4096 x 4096 4.9 / 5.2 / 6.3, 8192 x 8192 10.9 / 9.2 / 11.2, 4096 x 16384 11.1 /

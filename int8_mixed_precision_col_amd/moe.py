@@ -10,7 +10,7 @@ import functools
 import torch
 
 from . import binding, mx4
-from .binding import _check, _need, _need_shape
+from .binding import _need_shape
 
 
 @functools.lru_cache(maxsize=1024)
@@ -26,10 +26,10 @@ def _rows(pair, name: str) -> tuple[int, int]:
     return int(codes.dtype == torch.uint8), 16 * codes.shape[0]
 
 
-def _need_pair(pair, fmt: int, rows: int, K: int, device, name: str) -> None:
+def _need_pair(pair, fmt: int, rows: int, K: int, like: torch.Tensor, name: str) -> None:
     if fmt:
-        mx4._need_mx4(*pair, rows, K, device, name)
-    elif binding._need_weight(*pair, K, device) != rows:
+        mx4._need_mx4(*pair, rows, K, like, name)
+    elif binding._need_weight(*pair, K, like.device) != rows:
         raise ValueError(f"{name} has {pair[1].numel()} column constants for {rows} output features")
 
 
@@ -46,38 +46,34 @@ def moe_layer(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple
     chosen experts, otherwise they are the softmax over all of them.
     """
     T, D, ld, dt = mx4._need_rows(X, "X")
-    dev = X.device
     if not isinstance(logits, torch.Tensor) or logits.dtype not in mx4.DTYPES or logits.dim() != 2:
         raise ValueError("logits must be a 2-D fp16, bf16 or fp32 tensor")
     E = logits.shape[1]
-    _need_shape(logits, logits.dtype, (T, E), dev, "logits")
+    if logits.shape[0] != T or not logits.is_contiguous() or logits.get_device() != X.get_device():
+        _need_shape(logits, logits.dtype, (T, E), X.device, "logits")
     fmt, rows = _rows(gate_up, "gate_up")
     if _rows(down, "down")[0] != fmt:
         raise ValueError("gate_up and down must be in the same format")
     if E < 1 or rows % (32 * E):
         raise ValueError(f"gate_up has {rows} output features: not E = {E} times 2 I with I a multiple of 16")
     I = rows // (2 * E)
-    _need_pair(gate_up, fmt, rows, D, dev, "gate_up")
-    _need_pair(down, fmt, E * D, I, dev, "down")
+    _need_pair(gate_up, fmt, rows, D, X, "gate_up")
+    _need_pair(down, fmt, E * D, I, X, "down")
     if out is None:
-        out = torch.empty((T, D), dtype=X.dtype, device=dev)
+        out = X.new_empty((T, D))
     else:
-        _need_shape(out, X.dtype, (T, D), dev, "out")
+        _need_shape(out, X.dtype, (T, D), X.device, "out")
     if workspace is None:
         nbytes = workspace_bytes(T, I, top_k)
         if nbytes == 0:
             raise ValueError(f"bad shape for moe_layer: T={T} I={I} top_k={top_k}")
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        workspace = X.new_empty((nbytes,), dtype=torch.uint8)
     else:
-        _need(workspace, torch.uint8, "workspace")
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with mx4._on(dev):
-        _check(mx4.lib().moe_layer(X.data_ptr(), T, D, ld, dt, logits.data_ptr(), E, mx4.DTYPES[logits.dtype],
-                                   top_k, int(renormalize), fmt, gate_up[0].data_ptr(), gate_up[1].data_ptr(),
-                                   down[0].data_ptr(), down[1].data_ptr(), I, out.data_ptr(), ids.data_ptr(),
-                                   weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   binding._stream(X)), "moe_layer")
+        mx4._need_workspace(workspace, X)
+    ids = X.new_empty((T, top_k), dtype=torch.int32)
+    weights = X.new_empty((T, top_k), dtype=torch.float32)
+    mx4._launch("moe_layer", X, X.data_ptr(), T, D, ld, dt, logits.data_ptr(), E, mx4.DTYPES[logits.dtype],
+                top_k, int(renormalize), fmt, gate_up[0].data_ptr(), gate_up[1].data_ptr(), down[0].data_ptr(),
+                down[1].data_ptr(), I, out.data_ptr(), ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(),
+                workspace.numel())
     return out, ids, weights

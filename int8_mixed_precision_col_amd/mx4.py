@@ -9,14 +9,13 @@ in the library's HIP kernels, on the current stream of the tensors' device.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 
 import torch
 
 from . import binding
-from .binding import _check, _f32, _i64, _int, _need, _need_shape, _p  # noqa: F401
+from .binding import Int8mmError, _i64, _int, _need, _need_shape, _p
 
 _sz = ctypes.c_size_t
 
@@ -55,11 +54,22 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _on(device):
-    """Makes `device` current for a launch, where it is not."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _stream(index: int) -> int:
+    """Handle of the current stream of device `index` (no Stream object: these calls are a few
+    microseconds long)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _launch(name: str, t: torch.Tensor, *args) -> None:
+    """One library call on t's device, current or not, and on its current stream."""
+    index = t.get_device()
+    if index == torch._C._cuda_getDevice():
+        rc = getattr(lib(), name)(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = getattr(lib(), name)(*args, _stream(index))
+    if rc:
+        raise Int8mmError(rc, name)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -74,7 +84,10 @@ def _workspace_bytes(M: int, K: int, N: int) -> int:
     return int(lib().mx4_matmul_workspace_bytes(M, K, N))
 
 
-def _need_rows(X: torch.Tensor, name: str, types=(torch.float16, torch.bfloat16)) -> tuple:
+_HALF = (torch.float16, torch.bfloat16)
+
+
+def _need_rows(X: torch.Tensor, name: str, types=_HALF) -> tuple:
     """(M, K, row stride, dtype code) of a matrix whose rows are contiguous."""
     if not isinstance(X, torch.Tensor) or not binding._on_device(X):
         raise ValueError(f"{name} must be a HIP device tensor")
@@ -83,40 +96,50 @@ def _need_rows(X: torch.Tensor, name: str, types=(torch.float16, torch.bfloat16)
     if X.dim() != 2:
         raise ValueError(f"{name} must be 2-D [M, K], got shape {tuple(X.shape)}")
     M, K = X.shape
-    ld = X.stride(0) if M > 1 else K
-    if (K > 1 and X.stride(1) != 1) or ld < K or ld % 8:
+    ld, unit = X.stride()
+    if M == 1:
+        ld = K
+    if (K > 1 and unit != 1) or ld < K or ld % 8:
         raise ValueError(f"{name}'s rows must be contiguous, with a row stride that is a multiple of 8 "
                          f"and at least {K}: its strides are {X.stride()}")
     return M, K, ld, DTYPES[X.dtype]
 
 
-def _need_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: int, K: int, device, name: str) -> None:
-    """A tiled pair of `rows` rows of K elements: the kernels trust its sizes."""
+def _need_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: int, K: int, like: torch.Tensor, name: str) -> None:
+    """A tiled pair of `rows` rows of K elements on `like`'s device: the kernels trust its
+    sizes."""
+    want = _sizes(rows, K)
+    if (codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous()
+            and scales.is_contiguous() and want[0] and codes.numel() == want[0] and scales.numel() == want[1]
+            and codes.get_device() == scales.get_device() == like.get_device()):
+        return
     _need(codes, torch.uint8, f"{name} codes")
     _need(scales, torch.uint8, f"{name} scales")
-    want = _sizes(rows, K)
-    if want[0] == 0 or (codes.numel(), scales.numel()) != want:
-        raise ValueError(f"{name}: {codes.numel()} bytes of codes and {scales.numel()} of scales; {rows} rows of "
-                         f"{K} elements have {want[0]} and {want[1]}")
-    if codes.device != device or scales.device != device:
-        raise ValueError(f"{name} codes and scales must be on {device}")
+    if codes.device != like.device or scales.device != like.device:
+        raise ValueError(f"{name} codes and scales must be on {like.device}")
+    raise ValueError(f"{name}: {codes.numel()} bytes of codes and {scales.numel()} of scales; {rows} rows of "
+                     f"{K} elements have {want[0]} and {want[1]}")
 
 
-def _empty(rows: int, K: int, device) -> tuple[torch.Tensor, torch.Tensor]:
+def _need_workspace(workspace: torch.Tensor, like: torch.Tensor) -> None:
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
+
+
+def _empty(rows: int, K: int, like: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     if _sizes(rows, K)[0] == 0:
         raise ValueError(f"bad shape: {rows} rows of {K} elements")
     groups, ks = (rows + 15) // 16, (K + 127) // 128
-    return (torch.empty((groups, ks, 16, 64), dtype=torch.uint8, device=device),
-            torch.empty((groups, (ks + 3) // 4, 64, 4), dtype=torch.uint8, device=device))
+    return (like.new_empty((groups, ks, 16, 64), dtype=torch.uint8),
+            like.new_empty((groups, (ks + 3) // 4, 64, 4), dtype=torch.uint8))
 
 
 def quantize(X: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     """Rows of fp16 or bf16 X [M, K] -> tiled (codes, scales); M is padded to 16 rows."""
     M, K, ld, dt = _need_rows(X, "X")
-    codes, scales = _empty(M, K, X.device)
-    with _on(X.device):
-        _check(lib().mx4_quantize(X.data_ptr(), M, K, ld, dt, codes.data_ptr(), scales.data_ptr(),
-                                  binding._stream(X)), "mx4_quantize")
+    codes, scales = _empty(M, K, X)
+    _launch("mx4_quantize", X, X.data_ptr(), M, K, ld, dt, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -129,10 +152,8 @@ def prepare_weight(W: torch.Tensor, layout: int = 0) -> tuple[torch.Tensor, torc
     K, N = (R, C) if layout == 0 else (C, R)
     if N % 16:
         raise ValueError("N must be a multiple of 16")
-    codes, scales = _empty(N, K, W.device)
-    with _on(W.device):
-        _check(lib().mx4_prepare_weight(W.data_ptr(), K, N, layout, dt, codes.data_ptr(),
-                                        scales.data_ptr(), binding._stream(W)), "mx4_prepare_weight")
+    codes, scales = _empty(N, K, W)
+    _launch("mx4_prepare_weight", W, W.data_ptr(), K, N, layout, dt, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -152,10 +173,9 @@ def tile_weight(packed: torch.Tensor, block_scales: torch.Tensor, K: int | None 
                          f"N rows (a multiple of 16) of K = {K} elements")
     if block_scales.device != packed.device:
         raise ValueError(f"block_scales must be on {packed.device}")
-    codes, scales = _empty(N, K, packed.device)
-    with _on(packed.device):
-        _check(lib().mx4_tile_weight(packed.data_ptr(), block_scales.data_ptr(), K, N, codes.data_ptr(),
-                                     scales.data_ptr(), binding._stream(packed)), "mx4_tile_weight")
+    codes, scales = _empty(N, K, packed)
+    _launch("mx4_tile_weight", packed, packed.data_ptr(), block_scales.data_ptr(), K, N, codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
@@ -172,56 +192,55 @@ def untile(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int):
 def dequantize(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int,
                dtype: torch.dtype = torch.float16, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values [M, K] of a tiled pair, in fp16, bf16 or fp32."""
-    _need_mx4(codes, scales, M, K, codes.device, "operand")
+    _need_mx4(codes, scales, M, K, codes, "operand")
     if out is None:
         if dtype not in DTYPES:
             raise ValueError(f"dtype must be one of {tuple(DTYPES)}, got {dtype}")
-        out = torch.empty((M, K), dtype=dtype, device=codes.device)
-    m, k, ld, dt = _need_rows(out, "out", tuple(DTYPES))
-    if (m, k) != (M, K) or out.device != codes.device or out.dtype != dtype:
-        raise ValueError(f"out must be {dtype} [{M}, {K}] on {codes.device}, got {out.dtype} {tuple(out.shape)} "
-                         f"on {out.device}")
-    with _on(codes.device):
-        _check(lib().mx4_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, dt, out.data_ptr(), ld,
-                                    binding._stream(codes)), "mx4_dequantize")
+        out = codes.new_empty((M, K), dtype=dtype)
+        ld, dt = K, DTYPES[dtype]
+    else:
+        m, k, ld, dt = _need_rows(out, "out", tuple(DTYPES))
+        if (m, k) != (M, K) or out.device != codes.device or out.dtype != dtype:
+            raise ValueError(f"out must be {dtype} [{M}, {K}] on {codes.device}, got {out.dtype} {tuple(out.shape)} "
+                             f"on {out.device}")
+    _launch("mx4_dequantize", codes, codes.data_ptr(), scales.data_ptr(), M, K, dt, out.data_ptr(), ld)
     return out
 
 
-def _need_weight(w_codes: torch.Tensor, w_scales: torch.Tensor, K: int, device) -> int:
+def _need_weight(w_codes: torch.Tensor, w_scales: torch.Tensor, K: int, like: torch.Tensor) -> int:
     """A tiled weight for K input features; returns N."""
     if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 4:
         raise ValueError("the weight's codes must be the tiled tensor (N / 16, ceil(K / 128), 16, 64)")
     N = 16 * w_codes.shape[0]
-    _need_mx4(w_codes, w_scales, N, K, device, "weight")
+    _need_mx4(w_codes, w_scales, N, K, like, "weight")
     return N
 
 
 def make_workspace(M: int, K: int, N: int, device="cuda") -> torch.Tensor:
-    nbytes = _workspace_bytes(M, K, N)
-    if nbytes == 0:
+    """A workspace for ``matmul`` (empty where the shape needs none: M <= 16)."""
+    if _sizes(M, K)[0] == 0 or _sizes(N, K)[0] == 0 or N % 16:
         raise ValueError(f"bad shape for mx4_matmul: M={M} K={K} N={N}")
-    return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    return torch.empty((_workspace_bytes(M, K, N),), dtype=torch.uint8, device=device)
 
 
 def matmul(X: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
            workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [M, N] = MX4(X) W^T in X's type, for an MX4 weight: X is quantized in the call."""
     M, K, ld, dt = _need_rows(X, "X")
-    N = _need_weight(w_codes, w_scales, K, X.device)
+    N = _need_weight(w_codes, w_scales, K, X)
     if out is None:
-        out = torch.empty((M, N), dtype=X.dtype, device=X.device)
+        out = X.new_empty((M, N))
     else:
         _need_shape(out, X.dtype, (M, N), X.device, "out")
-    if workspace is None:
-        workspace = make_workspace(M, K, N, X.device)
+    if workspace is not None:
+        _need_workspace(workspace, X)
     else:
-        _need(workspace, torch.uint8, "workspace")
-        if workspace.device != X.device:
-            raise ValueError(f"workspace must be on {X.device}")
-    with _on(X.device):
-        _check(lib().mx4_matmul(X.data_ptr(), M, K, ld, dt, w_codes.data_ptr(), w_scales.data_ptr(), N,
-                                out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                binding._stream(X)), "mx4_matmul")
+        nbytes = _workspace_bytes(M, K, N)
+        if nbytes:
+            workspace = X.new_empty((nbytes,), dtype=torch.uint8)
+    ws, wb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _launch("mx4_matmul", X, X.data_ptr(), M, K, ld, dt, w_codes.data_ptr(), w_scales.data_ptr(), N,
+            out.data_ptr(), ws, wb)
     return out
 
 
@@ -229,18 +248,16 @@ def matmul_q(x_codes: torch.Tensor, x_scales: torch.Tensor, M: int, K: int, w_co
              w_scales: torch.Tensor, dtype: torch.dtype = torch.float16,
              out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [M, N] in fp16 or bf16 from X [M, K] already quantized (once for several weights)."""
-    if dtype not in (torch.float16, torch.bfloat16):
+    if dtype not in _HALF:
         raise ValueError(f"dtype must be fp16 or bf16, got {dtype}")
-    _need_mx4(x_codes, x_scales, M, K, x_codes.device, "X")
-    N = _need_weight(w_codes, w_scales, K, x_codes.device)
+    _need_mx4(x_codes, x_scales, M, K, x_codes, "X")
+    N = _need_weight(w_codes, w_scales, K, x_codes)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
+        out = x_codes.new_empty((M, N), dtype=dtype)
     else:
         _need_shape(out, dtype, (M, N), x_codes.device, "out")
-    with _on(x_codes.device):
-        _check(lib().mx4_matmul_q(x_codes.data_ptr(), x_scales.data_ptr(), M, K, w_codes.data_ptr(),
-                                  w_scales.data_ptr(), N, DTYPES[dtype], out.data_ptr(),
-                                  binding._stream(x_codes)), "mx4_matmul_q")
+    _launch("mx4_matmul_q", x_codes, x_codes.data_ptr(), x_scales.data_ptr(), M, K, w_codes.data_ptr(),
+            w_scales.data_ptr(), N, DTYPES[dtype], out.data_ptr())
     return out
 
 
@@ -248,13 +265,11 @@ def weight_only_matmul(X: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.T
                        out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [M, N] = X W^T for at most 16 rows of 16-bit X, as it is, and an MX4 weight."""
     M, K, ld, dt = _need_rows(X, "X")
-    N = _need_weight(w_codes, w_scales, K, X.device)
+    N = _need_weight(w_codes, w_scales, K, X)
     if out is None:
-        out = torch.empty((M, N), dtype=X.dtype, device=X.device)
+        out = X.new_empty((M, N))
     else:
         _need_shape(out, X.dtype, (M, N), X.device, "out")
-    with _on(X.device):
-        _check(lib().mx4_weight_only_matmul(X.data_ptr(), M, K, ld, dt, w_codes.data_ptr(),
-                                            w_scales.data_ptr(), N, out.data_ptr(), binding._stream(X)),
-               "mx4_weight_only_matmul")
+    _launch("mx4_weight_only_matmul", X, X.data_ptr(), M, K, ld, dt, w_codes.data_ptr(), w_scales.data_ptr(), N,
+            out.data_ptr())
     return out

@@ -33,7 +33,7 @@ def fake(monkeypatch):
     lib = FakeLib(mx4.lib())
     monkeypatch.setattr(mx4, "lib", lambda: lib)
     monkeypatch.setattr(binding, "_on_device", lambda t: True)
-    monkeypatch.setattr(binding, "_stream", lambda t: None)
+    monkeypatch.setattr(mx4, "_launch", lambda name, t, *args: getattr(lib, name)(*args))
     yield lib
 
 
