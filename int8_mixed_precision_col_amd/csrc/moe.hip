@@ -85,67 +85,92 @@ struct MoeOrder {
   }
 };
 
-// One wave: routes token t and enters its experts into the
-// table; writes the list where ids and weights are given (id -1 and weight 0 past the last
-// expert that is on). Lane l holds experts V l .. V l + V - 1, so that the lowest lane and
-// then the lowest of its experts is the lowest index.
-template <int V>
-__device__ __forceinline__ void moe_route(const MoeArgs& a, int t, int lane, MoeTable& table, int* ids,
-                                          float* weights) {
-  unsigned key[V];
+// One wave routes NT tokens, two of them side by side (a token's rounds are one chain of
+// dependent steps). Lane l holds experts V l .. V l + V - 1, so that the lowest lane and then
+// the lowest of its experts is the lowest index.
+template <int V, int NT>
+struct MoeRouter {
+  int token[NT];
+  unsigned key[NT][V];
+
+  // tokens t, t + stride (past T: every expert is off)
+  __device__ __forceinline__ MoeRouter(const MoeArgs& a, int t, int stride, int lane) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = V * lane + i;
-    key[i] = e < a.E ? moe_key(moe_logit(a.logits, a.logits_type, static_cast<int64_t>(t) * a.E + e)) : 0u;
-  }
-  unsigned kept[V];
+    for (int p = 0; p < NT; ++p) {
+      token[p] = t + p * stride;
 #pragma unroll
-  for (int i = 0; i < V; ++i) kept[i] = key[i];
-  unsigned first = 0, mine = 0;  // the largest key; lane j: that of place j
-  int mine_id = -1;
-  for (int j = 0; j < a.k; ++j) {
-    unsigned best = key[0];
-    int at = 0;
-#pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
+      for (int i = 0; i < V; ++i) {
+        const int e = V * lane + i;
+        key[p][i] = token[p] < a.T && e < a.E
+                        ? moe_key(moe_logit(a.logits, a.logits_type, static_cast<int64_t>(token[p]) * a.E + e))
+                        : 0u;
       }
-    const unsigned top = wave_max_u32(best);
-    if (top == 0u) break;  // no expert left
-    if (j == 0) first = top;
-    const int who = __builtin_ctzll(__ballot(best == top));
-    const int id = V * who + (V > 1 ? __builtin_amdgcn_readlane(at, who) : 0);
-    if (lane == j) {
-      mine = top;
-      mine_id = id;
+    }
+  }
+
+  // enters the chosen experts into the table; writes the lists where ids is given (id -1 and
+  // weight 0 past the last expert that is on)
+  __device__ __forceinline__ void route(const MoeArgs& a, int lane, MoeTable& table, int* ids, float* weights) {
+    unsigned kept[NT][V], first[NT], mine[NT];  // the keys; the largest; lane j: that of place j
+    int mine_id[NT];
+#pragma unroll
+    for (int p = 0; p < NT; ++p) {
+      first[p] = mine[p] = 0;
+      mine_id[p] = -1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) kept[p][i] = key[p][i];
+    }
+    for (int j = 0; j < a.k; ++j) {
+#pragma unroll
+      for (int p = 0; p < NT; ++p) {
+        unsigned best = key[p][0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+          if (key[p][i] > best) {
+            best = key[p][i];
+            at = i;
+          }
+        const unsigned top = wave_max_u32(best);  // 0: no expert left
+        const int who = __builtin_ctzll(__ballot(best == top));
+        const int id = V * who + (V > 1 ? __builtin_amdgcn_readlane(at, who) : 0);
+        if (j == 0) first[p] = top;
+        if (lane == j && top) {
+          mine[p] = top;
+          mine_id[p] = id;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (V * lane + i == id) key[p][i] = 0u;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (V * lane + i == id) key[i] = 0u;
-  }
-  if (mine_id >= 0) table.add(mine_id, t, lane);
-  if (!ids) return;
-  const float most = moe_unkey(first);
-  const float w = mine ? expf(moe_unkey(mine) - most) : 0.0f;
-  float sum = w;
-  if (!a.renormalize) {
-    sum = 0.0f;
+    for (int p = 0; p < NT; ++p)
+      if (mine_id[p] >= 0) table.add(mine_id[p], token[p], lane);
+    if (!ids) return;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += kept[i] ? expf(moe_unkey(kept[i]) - most) : 0.0f;
-  }
+    for (int p = 0; p < NT; ++p) {
+      const float most = moe_unkey(first[p]);
+      const float w = mine[p] ? expf(moe_unkey(mine[p]) - most) : 0.0f;
+      float sum = w;
+      if (!a.renormalize) {
+        sum = 0.0f;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane < a.k) {
-    const float p = mine_id < 0 ? 0.0f : __fdiv_rn(w, sum);
-    const int o = t * a.k + lane;
-    ids[o] = mine_id;
-    weights[o] = p;
-    if (a.ids) a.ids[o] = mine_id;
-    if (a.weights) a.weights[o] = p;
+        for (int i = 0; i < V; ++i) sum += kept[p][i] ? expf(moe_unkey(kept[p][i]) - most) : 0.0f;
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      if (lane < a.k && token[p] < a.T) {
+        const float share = mine_id[p] < 0 ? 0.0f : __fdiv_rn(w, sum);
+        const int o = token[p] * a.k + lane;
+        ids[o] = mine_id[p];
+        weights[o] = share;
+        if (a.ids) a.ids[o] = mine_id[p];
+        if (a.weights) a.weights[o] = share;
+      }
+    }
   }
-}
+};
 
 constexpr int kUpWaves = 8;
 // LDS for the activations of k_moe_gate_up: with all of X in it (T x D up to 64 K elements) X
@@ -167,22 +192,27 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   const int ks = (a.D + UK - 1) / UK, quads = (ks + 3) >> 2, groups = a.I / 16;
   const bool resident = up_resident<MX>(a.T, quads);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.T - 1) * a.ldx + a.D) * 2));
-  table.clear(tid, 64 * kUpWaves);
-  lds_barrier();
-  // One workgroup writes what the second launch goes by, all of it from its own view of the
-  // logits, so that it is consistent whatever else happens to them meanwhile.
-  int* out_ids = blockIdx.x == 0 ? ids : nullptr;
-  for (int t = wave; t < a.T; t += kUpWaves) {
-    if (a.E <= 64) moe_route<1>(a, t, lane, table, out_ids, weights);
-    else if (a.E <= 128) moe_route<2>(a, t, lane, table, out_ids, weights);
-    else moe_route<kMoeMaxExperts / 64>(a, t, lane, table, out_ids, weights);
+  // the logits first, then X: both are on their way while the table is cleared and the wave
+  // routes its tokens
+  static_assert(2 * kUpWaves >= kMoeMaxTokens, "two tokens per wave");
+  auto row_of = [&](int t) { return static_cast<unsigned>(t * a.ldx) * 2u; };
+  ActQuad<MX, 16> x;
+  auto route = [&](auto router) {
+    if (resident && wave < quads) x.load(xr, wave, a.D, a.T, lane, row_of);
+    table.clear(tid, 64 * kUpWaves);
+    lds_barrier();
+    // One workgroup writes what the second launch goes by, all of it from its own view of the
+    // logits, so that it is consistent whatever else happens to them meanwhile.
+    router.route(a, lane, table, blockIdx.x == 0 ? ids : nullptr, weights);
+  };
+  constexpr int V = kMoeMaxExperts / 64;
+  if (a.T > kUpWaves) {
+    if (a.E <= 64) route(MoeRouter<1, 2>(a, wave, kUpWaves, lane));
+    else route(MoeRouter<V, 2>(a, wave, kUpWaves, lane));
+  } else {
+    if (a.E <= 64) route(MoeRouter<1, 1>(a, wave, kUpWaves, lane));
+    else route(MoeRouter<V, 1>(a, wave, kUpWaves, lane));
   }
-  if (resident)
-    for (int q = wave; q < quads; q += kUpWaves) {
-      ActQuad<MX, 16> x;
-      x.load(xr, q, a.D, a.T, lane, [&](int t) { return static_cast<unsigned>(t * a.ldx) * 2u; });
-      x.store(s_x + q * act_bytes<MX>(a.T), a.T, a.T, lane);
-    }
   lds_barrier();
   const MoeOrder order(table, lane);
 
@@ -194,7 +224,6 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   const unsigned all = static_cast<unsigned>(order.count() * steps), some = all / gridDim.x, more = all % gridDim.x;
   const unsigned first = blockIdx.x * some + min(blockIdx.x, more);
   const int n_steps = static_cast<int>(some + (blockIdx.x < more ? 1u : 0u));
-  if (n_steps == 0) return;
   int slot = static_cast<int>(first / steps), in = static_cast<int>(first % steps);  // its place in the expert
   const int sub = wave / share, kk = wave - sub * share;
 
@@ -205,8 +234,19 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
     next[0].load(a.w13, static_cast<const uint32_t*>(a.s13), gate, ks, quads, q, lane);
     next[1].load(a.w13, static_cast<const uint32_t*>(a.s13), gate + groups, ks, quads, q, lane);
   };
-  int expert = order.expert(slot);
-  if (kk < quads) prefetch(expert, in, kk);
+  int expert = 0;
+  if (n_steps > 0) {
+    expert = order.expert(slot);
+    if (kk < quads) prefetch(expert, in, kk);
+  }
+  if (resident) {
+    if (wave < quads) x.store(s_x + wave * act_bytes<MX>(a.T), a.T, a.T, lane);
+    for (int q = wave + kUpWaves; q < quads; q += kUpWaves) {
+      x.load(xr, q, a.D, a.T, lane, row_of);
+      x.store(s_x + q * act_bytes<MX>(a.T), a.T, a.T, lane);
+    }
+  }
+  lds_barrier();
   const int row = min(lane & 15, a.T - 1);  // rows past T repeat the last (discarded)
   for (int step = 0; step < n_steps; ++step) {
     const unsigned tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
@@ -216,9 +256,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
     for (int q = kk; q < quads; q += share) {
       const char* buf = s_x + (resident ? q : wave) * act_bytes<MX>(a.T);
       if (!resident) {
-        ActQuad<MX, 16> x;
-        x.load(xr, q, a.D, a.T, lane, [&](int t) {
-          return (tokens >> t) & 1u ? static_cast<unsigned>(t * a.ldx) * 2u : kOOB; });
+        x.load(xr, q, a.D, a.T, lane, [&](int t) { return (tokens >> t) & 1u ? row_of(t) : kOOB; });
         wave_lds_fence();
         x.store(s_x + wave * act_bytes<MX>(a.T), a.T, a.T, lane);
         wave_lds_fence();
@@ -269,7 +307,10 @@ template <class T, bool MX, int WAVES, int TOK>
 __global__ __launch_bounds__(64 * WAVES) void k_moe_down(MoeArgs a, const int* ids, const float* weights) {
   constexpr int ROWS = 2 * TOK;
   __shared__ __attribute__((aligned(16))) char s_x[WAVES * ROWS * kActStride];
-  __shared__ MoeTable table;
+  __shared__ unsigned s_tokens[kMoeMaxExperts];
+  __shared__ uint8_t s_place[kMoeMaxExperts * kMoeMaxTokens], s_pass[kMoeMaxLists];
+  __shared__ uint64_t s_first[kMoeMaxLists / 64];
+  __shared__ int s_id[kMoeMaxLists];
   __shared__ float s_w[kMoeMaxLists];
   __shared__ float total[WAVES][kMoeMaxTokens][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -281,21 +322,43 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_down(MoeArgs a, const int* i
     id = ids[tid];
     weight = weights[tid];
   }
-  table.clear(tid, 64 * WAVES);
+  for (int i = tid; i < a.E; i += 64 * WAVES) s_tokens[i] = 0u;
   for (int i = lane; i < kMoeMaxTokens * 17; i += 64) (&total[wave][0][0])[i] = 0.0f;
   lds_barrier();
+  // Addresses come out of the ids: checked here too, so that a workspace that another call
+  // wrote to meanwhile, which the interface forbids, gives wrong values at worst.
+  const int t_of = tid / a.k;
+  if (id >= a.E) id = -1;
+  if (id >= 0) {
+    atomicOr(&s_tokens[id], 1u << t_of);
+    s_place[id * kMoeMaxTokens + t_of] = static_cast<uint8_t>(tid - t_of * a.k);
+  }
   if (tid < n_lists) {
-    // Addresses come out of the ids: checked here too, so that a workspace that another call
-    // wrote to meanwhile, which the interface forbids, gives wrong values at worst.
-    if (id >= 0 && id < a.E) table.add(id, tid / a.k, tid % a.k);
+    s_id[tid] = id;
     s_w[tid] = weight;
   }
   lds_barrier();
-  const MoeOrder order(table, lane);
+  // Passes: TOK tokens of one expert, each found by the list entry of its first token and kept
+  // in that order. A pass is a wave's unit whatever its expert, so that an expert with many
+  // tokens does not hold up one wave.
+  const int before = id < 0 ? 0 : __builtin_popcount(s_tokens[id] & ((1u << (t_of & 31)) - 1));
+  const uint64_t starts = __ballot(id >= 0 && before % TOK == 0);
+  if (lane == 0 && wave < kMoeMaxLists / 64) s_first[wave] = starts;
+  lds_barrier();
+  int passes = 0, mine = 0;
+#pragma unroll
+  for (int i = 0; i < kMoeMaxLists / 64; ++i) {
+    if (i == wave) mine = passes;
+    passes += __builtin_popcountll(s_first[i]);
+  }
+  if (id >= 0 && before % TOK == 0)
+    s_pass[mine + __builtin_popcountll(starts & ((uint64_t(1) << lane) - 1))] = static_cast<uint8_t>(tid);
+  lds_barrier();
+  passes = __builtin_amdgcn_readfirstlane(passes);
 
   constexpr int UK = WeightFmt<MX>::UK;
   const int ks = (a.I + UK - 1) / UK, quads = (ks + 3) >> 2;
-  const int items = order.count() * quads, per = (items + WAVES - 1) / WAVES;
+  const int items = passes * quads, per = (items + WAVES - 1) / WAVES;
   const int begin = min(items, per * wave), end = min(items, begin + per);
   const unsigned plane = static_cast<unsigned>(n_lists) * a.I * 2u;  // bytes
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, plane * 2u);
@@ -305,75 +368,73 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_down(MoeArgs a, const int* i
     next.load(a.w2, static_cast<const uint32_t*>(a.s2), static_cast<size_t>(expert) * (a.D / 16) + blockIdx.x, ks, quads,
               q, lane);
   };
-  int slot = begin / quads, expert = 0;
+  auto expert_of = [&](int pass) { return __builtin_amdgcn_readfirstlane(s_id[s_pass[pass]]); };
+  int pass = begin / quads, expert = 0;
   if (begin < end) {
-    expert = order.expert(slot);
-    prefetch(expert, begin - slot * quads);
+    expert = expert_of(pass);
+    prefetch(expert, begin - pass * quads);
   }
-  for (int i = begin; i < end; ++slot) {
-    // items [i, stop) are quads of one expert, the wave's share of it
-    const int q0 = i - slot * quads, stop = min(end, (slot + 1) * quads), q1 = stop - slot * quads;
-    const unsigned tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
-    const int count = __builtin_popcount(tokens), current = expert;
+  for (int i = begin; i < end; ++pass) {
+    // items [i, stop) are quads of one pass, the wave's share of it
+    const int q0 = i - pass * quads, stop = min(end, (pass + 1) * quads), q1 = stop - pass * quads;
+    const int current = expert;
+    const unsigned t0 = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(s_pass[pass])) / static_cast<unsigned>(a.k);
+    // the pass's tokens: this one and those after it
+    const unsigned tokens = __builtin_amdgcn_readfirstlane(s_tokens[current]) & ~((1u << t0) - 1);
+    const int m = min(__builtin_popcount(tokens), TOK);
     i = stop;
-    auto list_of = [&](int c) {  // list entry of the expert's c-th token
-      unsigned m = tokens;
-      for (int j = 0; j < c; ++j) m &= m - 1;
-      const int t = __builtin_ctz(m);
-      return t * a.k + table.place[current * kMoeMaxTokens + t];
+    auto list_of = [&](int c) {  // list entry of the pass's c-th token
+      unsigned b = tokens;
+      for (int j = 0; j < c; ++j) b &= b - 1;
+      const int t = __builtin_ctz(b);
+      return t * a.k + s_place[current * kMoeMaxTokens + t];
     };
-    for (int c0 = 0; c0 < count; c0 += TOK) {
-      const int m = min(count - c0, TOK);
-      const bool last = c0 + TOK >= count;
-      // this lane's rows: byte offsets of rows 2 j + l / 32 in h
-      unsigned off[TOK];
+    // this lane's rows: byte offsets of rows 2 j + l / 32 in h
+    unsigned off[TOK];
 #pragma unroll
-      for (int j = 0; j < TOK; ++j) {
-        const int row = 2 * j + (lane >> 5);
-        off[j] = row < 2 * m ? static_cast<unsigned>(list_of(c0 + (row < m ? row : row - m))) * a.I * 2u +
-                                   (row < m ? 0u : plane)
-                             : kOOB;
+    for (int j = 0; j < TOK; ++j) {
+      const int row = 2 * j + (lane >> 5);
+      off[j] = row < 2 * m ? static_cast<unsigned>(list_of(row < m ? row : row - m)) * a.I * 2u +
+                                 (row < m ? 0u : plane)
+                           : kOOB;
+    }
+    // operand rows 0 .. TOK - 1 are the high parts, 8 .. the remainders; the others repeat one
+    const int row = min(r & 7, m - 1) + (r < 8 ? 0 : m);
+    v4f acc[1] = {};
+    for (int q = q0; q < q1; ++q) {
+      WeightQuad<MX> w[1] = {next};
+      ActQuad<MX, ROWS> x;
+      x.load(hr, q, a.I, 2 * m, lane, [&](int j) { return off[j >> 1]; });
+      if (q + 1 < q1) {
+        prefetch(expert, q + 1);
+      } else if (i < end) {
+        expert = expert_of(pass + 1);
+        prefetch(expert, 0);
       }
-      // operand rows 0 .. TOK - 1 are the high parts, 8 .. the remainders; the others repeat one
-      const int row = min(r & 7, m - 1) + (r < 8 ? 0 : m);
-      v4f acc[1] = {};
-      for (int q = q0; q < q1; ++q) {
-        WeightQuad<MX> w[1] = {next};
-        ActQuad<MX, ROWS> x;
-        x.load(hr, q, a.I, 2 * m, lane, [&](int j) { return off[j >> 1]; });
-        if (q + 1 < q1) {
-          prefetch(expert, q + 1);
-        } else if (!last) {
-          prefetch(expert, q0);
-        } else if (i < end) {
-          expert = order.expert(slot + 1);
-          prefetch(expert, 0);
-        }
+      wave_lds_fence();
+      x.store_piece(0, buf, 2 * m, lane);
+      wave_lds_fence();
+      constexpr int HALF = MX ? 2 : 4;
+      mma_quad<B16, MX, 1, 0, HALF>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
+      if constexpr (MX) {
         wave_lds_fence();
-        x.store_piece(0, buf, 2 * m, lane);
+        x.store_piece(1, buf, 2 * m, lane);
         wave_lds_fence();
-        constexpr int HALF = MX ? 2 : 4;
-        mma_quad<B16, MX, 1, 0, HALF>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
-        if constexpr (MX) {
-          wave_lds_fence();
-          x.store_piece(1, buf, 2 * m, lane);
-          wave_lds_fence();
-          mma_quad<B16, MX, 1, 2, 4>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
-        }
+        mma_quad<B16, MX, 1, 2, 4>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
       }
-      // weigh the sums into the tokens'
-      float scale = 1.0f;
-      if constexpr (!MX)
-        scale = __fdiv_rn(static_cast<const float*>(a.s2)[static_cast<size_t>(current) * a.D + blockIdx.x * 16 + r], 127.0f);
+    }
+    // weigh the sums into the tokens'
+    float scale = 1.0f;
+    if constexpr (!MX)
+      scale = __fdiv_rn(static_cast<const float*>(a.s2)[static_cast<size_t>(current) * a.D + blockIdx.x * 16 + r], 127.0f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // rows c (high) and 8 + c (remainder) of one token are 32 lanes apart
-        const float y = acc[0][e] + __shfl_xor(acc[0][e], 32, 64);
-        const int c = 4 * (g & 1) + e;
-        if (g < 2 && c < m) {
-          const int list = list_of(c0 + c);
-          total[wave][list / a.k][r] += y * scale * s_w[list];
-        }
+    for (int e = 0; e < 4; ++e) {
+      // rows c (high) and 8 + c (remainder) of one token are 32 lanes apart
+      const float y = acc[0][e] + __shfl_xor(acc[0][e], 32, 64);
+      const int c = 4 * (g & 1) + e;
+      if (g < 2 && c < m) {
+        const int list = list_of(c);
+        total[wave][list / a.k][r] += y * scale * s_w[list];
       }
     }
   }
