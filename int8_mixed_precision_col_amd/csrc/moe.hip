@@ -224,6 +224,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   const unsigned all = static_cast<unsigned>(order.count() * steps), some = all / gridDim.x, more = all % gridDim.x;
   const unsigned first = blockIdx.x * some + min(blockIdx.x, more);
   const int n_steps = static_cast<int>(some + (blockIdx.x < more ? 1u : 0u));
+  if (n_steps == 0) return;
   int slot = static_cast<int>(first / steps), in = static_cast<int>(first % steps);  // its place in the expert
   const int sub = wave / share, kk = wave - sub * share;
 
@@ -234,11 +235,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
     next[0].load(a.w13, static_cast<const uint32_t*>(a.s13), gate, ks, quads, q, lane);
     next[1].load(a.w13, static_cast<const uint32_t*>(a.s13), gate + groups, ks, quads, q, lane);
   };
-  int expert = 0;
-  if (n_steps > 0) {
-    expert = order.expert(slot);
-    if (kk < quads) prefetch(expert, in, kk);
-  }
+  // unconditional (a wave without a quad repeats the last), so that the wait for X below counts
+  // these loads and does not wait for them
+  int expert = order.expert(slot);
+  prefetch(expert, in, min(kk, quads - 1));
   if (resident) {
     if (wave < quads) x.store(s_x + wave * act_bytes<MX>(a.T), a.T, a.T, lane);
     for (int q = wave + kUpWaves; q < quads; q += kUpWaves) {
