@@ -77,7 +77,8 @@ int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64
  * by both blocks' powers of two and accumulated in fp32, Y is rounded once to dtype
  * (MX4_F16 or MX4_BF16, X's type).
  * M <= 16 is one launch, without a workspace, and needs M ldx < 2^30; more rows are a
- * quantization launch and the product (M <= 64 a weight stream, beyond that output tiles).
+ * quantization launch and the product (M <= 64 a weight stream, beyond that output tiles;
+ * where K is long and the tiles are few, K is split and a third launch joins the sums).
  *   workspace   at least mx4_matmul_workspace_bytes(M, K, N) bytes (0 where M <= 16, then
  *               workspace may be NULL, and on bad shapes); its contents do not matter. Calls
  *               that may run at the same time need workspaces of their own.
@@ -87,10 +88,15 @@ int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype,
                const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, void* Y,
                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* The product alone, X already MX4 (mx4_quantize): once for several weights. */
+/*
+ * The product alone, X already MX4 (mx4_quantize): once for several weights.
+ *   workspace   at least mx4_matmul_q_workspace_bytes(M, K, N) bytes; often 0 (and on bad
+ *               shapes), then workspace may be NULL. Otherwise as for mx4_matmul.
+ */
+size_t mx4_matmul_q_workspace_bytes(int64_t M, int64_t K, int64_t N);
 int mx4_matmul_q(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int dtype, void* Y,
-                 hipStream_t stream);
+                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Y [M, N] = X W^T with X as it is, for a few tokens: 1 <= M <= 16 and M ldx < 2^30 (X is

@@ -33,6 +33,8 @@ size_t codes_bytes(int64_t rows, int64_t K) {
   return size_t((rows + 15) / 16) * i8mm::mx_ks(K) * i8mm::kUnitBytes;
 }
 size_t scales_bytes(int64_t rows, int64_t K) { return size_t((rows + 15) / 16) * i8mm::mx_quads(K) * 256; }
+// scratch of the product itself
+size_t part_bytes(int64_t M, int64_t K, int64_t N) { return i8mm::mx_few(M) ? 0 : i8mm::mx_gemm_part_bytes(M, N, K); }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? INT8MM_OK : INT8MM_E_HIP; }
 
@@ -43,9 +45,9 @@ hipError_t run_quantize(const void* X, int64_t M, int64_t K, int64_t ldx, int dt
 }
 
 i8mm::MxGemmArgs gemm_args(const uint8_t* xc, const void* xs, int64_t M, int64_t K, const uint8_t* wc,
-                           const void* ws, int64_t N, void* Y) {
+                           const void* ws, int64_t N, void* Y, void* part) {
   return {xc, static_cast<const uint32_t*>(xs), wc, static_cast<const uint32_t*>(ws), int(M), int(N), int(K),
-          Y, int(N)};
+          Y, int(N), part};
 }
 
 hipError_t run_gemm(const i8mm::MxGemmArgs& a, int dtype, hipStream_t s) {
@@ -104,7 +106,11 @@ int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64
 
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (bad_product(M, K, N) || M <= kMaxFew) return 0;
-  return round256(codes_bytes(M, K)) + scales_bytes(M, K);
+  return round256(codes_bytes(M, K)) + round256(scales_bytes(M, K)) + part_bytes(M, K, N);
+}
+
+size_t mx4_matmul_q_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  return bad_product(M, K, N) ? 0 : part_bytes(M, K, N);
 }
 
 int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype, const uint8_t* w_codes,
@@ -118,24 +124,29 @@ int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype, cons
   if (!aligned16(X) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y) || !aligned16(workspace))
     return INT8MM_E_ALIGN;
   if (few)
-    return hip_status(i8mm::launch_mx_few_inline(gemm_args(nullptr, nullptr, M, K, w_codes, w_scales, N, Y), X, ldx,
+    return hip_status(i8mm::launch_mx_few_inline(gemm_args(nullptr, nullptr, M, K, w_codes, w_scales, N, Y, nullptr), X, ldx,
                                                  dtype, stream));
   if (workspace_bytes < mx4_matmul_workspace_bytes(M, K, N)) return INT8MM_E_WORKSPACE;
   uint8_t* xc = static_cast<uint8_t*>(workspace);
   uint8_t* xs = xc + round256(codes_bytes(M, K));
   const hipError_t e = run_quantize(X, M, K, ldx, dtype, xc, xs, stream);
   if (e != hipSuccess) return INT8MM_E_HIP;
-  return hip_status(run_gemm(gemm_args(xc, xs, M, K, w_codes, w_scales, N, Y), dtype, stream));
+  uint8_t* part = xs + round256(scales_bytes(M, K));
+  return hip_status(run_gemm(gemm_args(xc, xs, M, K, w_codes, w_scales, N, Y, part), dtype, stream));
 }
 
 int mx4_matmul_q(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int64_t K,
                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int dtype, void* Y,
-                 hipStream_t stream) {
+                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!x_codes || !x_scales || !w_codes || !w_scales || !Y) return INT8MM_E_NULL;
   if (bad_product(M, K, N) || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
-  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y))
+  const size_t need = part_bytes(M, K, N);
+  if (need && !workspace) return INT8MM_E_NULL;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y) ||
+      !aligned16(workspace))
     return INT8MM_E_ALIGN;
-  return hip_status(run_gemm(gemm_args(x_codes, x_scales, M, K, w_codes, w_scales, N, Y), dtype, stream));
+  if (workspace_bytes < need) return INT8MM_E_WORKSPACE;
+  return hip_status(run_gemm(gemm_args(x_codes, x_scales, M, K, w_codes, w_scales, N, Y, workspace), dtype, stream));
 }
 
 int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype,

@@ -168,7 +168,15 @@ __device__ __forceinline__ void mx_epilogue(const MxGemmArgs& g, v4f (&acc)[C::B
   }
 }
 
-template <class C, class T>
+// The part of K that split s of n takes, in quads: [first, last).
+__device__ __forceinline__ void split_range(int quads, int s, int n, int& first, int& last) {
+  first = quads * s / n;
+  last = quads * (s + 1) / n;
+}
+
+// PART: split blockIdx.y of gridDim.y of the K quads, its fp32 sums to g.part in the order of
+// the accumulators: [split][tile][wave][i][j][lane] of v4f.
+template <class C, class T, bool PART>
 __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, int group_m) {
   static_assert(C::STAGES == 4, "a quad of slabs is one turn of the ring");
   int tn, tm;
@@ -212,11 +220,13 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
 #pragma unroll
     for (int j = 0; j < C::BM; ++j) b.acc[i][j] = v4f{};
 
-  b.issue_scales(0);
-  b.template issue<0>(0);
-  b.template issue<1>(1);
-  b.template issue<2>(2);
-  b.template issue<3>(3);
+  int q0 = 0, q1 = b.quads;
+  if constexpr (PART) split_range(b.quads, blockIdx.y, gridDim.y, q0, q1);
+  b.issue_scales(q0);
+  b.template issue<0>(4 * q0);
+  b.template issue<1>(4 * q0 + 1);
+  b.template issue<2>(4 * q0 + 2);
+  b.template issue<3>(4 * q0 + 3);
   wait_and_barrier<3 * MxBlock<C>::NQ>();  // scales 0 and slab 0 landed
 #pragma unroll
   for (int j = 0; j < C::BM; ++j) {
@@ -229,7 +239,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
     b.sa[i] = b.scale_a(i);
   }
   // whole quads: slabs past K are zeros
-  for (int kt = 0; kt < b.ks; kt += 4) {
+  for (int kt = 4 * q0; kt < 4 * q1; kt += 4) {
     b.template step<0>(kt);
     b.template step<1>(kt + 1);
     b.template step<2>(kt + 2);
@@ -237,7 +247,39 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
   }
   // no DMA may still be writing this block's LDS when it is reused or the block exits
   __builtin_amdgcn_s_waitcnt(0);
-  mx_epilogue<C, T>(g, b.acc, n0, m0, wn, wm, b.lane);
+  if constexpr (PART) {
+    v4f* dst = static_cast<v4f*>(g.part) +
+               ((static_cast<size_t>(blockIdx.y) * gridDim.x + tn * tiles_m + tm) * C::NW + b.wave) * C::BN * C::BM * 64 +
+               b.lane;
+#pragma unroll
+    for (int i = 0; i < C::BN; ++i)
+#pragma unroll
+      for (int j = 0; j < C::BM; ++j) dst[(i * C::BM + j) * 64] = b.acc[i][j];
+  } else {
+    mx_epilogue<C, T>(g, b.acc, n0, m0, wn, wm, b.lane);
+  }
+}
+
+// Y from the splits' sums, added in order: a wave per accumulator block of a tile.
+template <class C, class T>
+__global__ __launch_bounds__(256) void k_mx_gemm_join(MxGemmArgs g, int tiles, int tiles_m, int splits) {
+  typedef typename T::elem v4t __attribute__((ext_vector_type(4)));
+  constexpr int BLOCKS = C::NW * C::BN * C::BM;
+  const int lane = threadIdx.x & 63;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);  // tile, wave, i, j
+  if (at >= tiles * BLOCKS) return;
+  const int tile = at / BLOCKS, in = at % BLOCKS;
+  const int wave = in / (C::BN * C::BM), i = in / C::BM % C::BN, j = in % C::BM;
+  const int n = tile / tiles_m * C::TN + wave % C::WGN * C::WTN + 16 * i + 4 * (lane >> 4);
+  const int m = tile % tiles_m * C::TM + wave / C::WGN * C::WTM + 16 * j + (lane & 15);
+  if (m >= g.M || n >= g.N) return;
+  const v4f* src = static_cast<const v4f*>(g.part) + static_cast<size_t>(at) * 64 + lane;
+  v4f sum = src[0];
+  for (int s = 1; s < splits; ++s) sum += src[static_cast<size_t>(s) * tiles * BLOCKS * 64];
+  v4t out;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = T::round(sum[e]);
+  *reinterpret_cast<v4t*>(static_cast<typename T::elem*>(g.Y) + static_cast<size_t>(m) * g.ldy + n) = out;
 }
 
 #undef I8MM_LDS
@@ -252,13 +294,47 @@ static hipError_t run(const MxGemmArgs& g, int type, hipStream_t s) {
   const int tiles_n = (g.N + C::TN - 1) / C::TN, tiles_m = (g.M + C::TM - 1) / C::TM;
   const int group_m = tiles_m < 8 ? tiles_m : 8;
   if (type == kMxF16)
-    hipLaunchKernelGGL((k_mx_gemm<C, F16>), dim3(tiles_n * tiles_m), dim3(C::NT), 0, s, g, tiles_m, group_m);
+    hipLaunchKernelGGL((k_mx_gemm<C, F16, false>), dim3(tiles_n * tiles_m), dim3(C::NT), 0, s, g, tiles_m, group_m);
   else
-    hipLaunchKernelGGL((k_mx_gemm<C, B16>), dim3(tiles_n * tiles_m), dim3(C::NT), 0, s, g, tiles_m, group_m);
+    hipLaunchKernelGGL((k_mx_gemm<C, B16, false>), dim3(tiles_n * tiles_m), dim3(C::NT), 0, s, g, tiles_m, group_m);
   return hipGetLastError();
 }
 
+template <class C, class T>
+static hipError_t run_split(const MxGemmArgs& g, int splits, hipStream_t s) {
+  const int tiles_n = (g.N + C::TN - 1) / C::TN, tiles_m = (g.M + C::TM - 1) / C::TM, tiles = tiles_n * tiles_m;
+  hipLaunchKernelGGL((k_mx_gemm<C, T, true>), dim3(tiles, splits), dim3(C::NT), 0, s, g, tiles_m,
+                     tiles_m < 8 ? tiles_m : 8);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int blocks = tiles * C::NW * C::BN * C::BM;
+  hipLaunchKernelGGL((k_mx_gemm_join<C, T>), dim3((blocks + 3) / 4), dim3(256), 0, s, g, tiles, tiles_m, splits);
+  return hipGetLastError();
+}
+
+// A long K over few tiles leaves most CUs idle while each tile waits for its slabs: K is then
+// split, the sums of the splits joined by a second launch. Joining costs 3 to 5 us, so K has at
+// least 16 quads (7.5 K elements); more than 192 workgroups write more sums than the split
+// saves. Measured, us per product, unsplit against the splits taken here: 128 x 12288 x 4096
+// 30.7 / 15.7 (6), 128 x 12288 x 512 22.7 / 11.1 (8), 256 x 8192 x 1024 16.6 / 11.8 (5), 1024 x
+// 8192 x 1024 16.8 / 15.0 (3), 128 x 12288 x 12288 33.7 / 26.8 (2); but 128 x 4096 x 4096 10.2 /
+// 11.5 (2) and 512 x 12288 x 4096 30.0 / 32.0 (3).
+int mx_gemm_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((N + 127) / 128) * ((M + 127) / 128), quads = mx_quads(K);
+  if (quads < 16) return 1;
+  const int64_t most = quads / 3 < 8 ? quads / 3 : 8, by_tiles = 192 / tiles;
+  const int64_t splits = by_tiles < most ? by_tiles : most;
+  return splits < 2 ? 1 : static_cast<int>(splits);
+}
+
+size_t mx_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
+  const int splits = mx_gemm_splits(M, N, K);
+  return splits < 2 ? 0 : static_cast<size_t>(splits) * ((N + 127) / 128) * ((M + 127) / 128) * 128 * 128 * 4;
+}
+
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int type, hipStream_t s) {
+  const int splits = mx_gemm_splits(g.M, g.N, g.K);
+  if (splits > 1) return type == kMxF16 ? run_split<MxS, F16>(g, splits, s) : run_split<MxS, B16>(g, splits, s);
   Tile t;
   best_cost([&](int tn, int tm) {
     return static_cast<long>((g.N + tn - 1) / tn) * ((g.M + tm - 1) / tm); }, &t);

@@ -42,8 +42,12 @@ struct MxGemmArgs {
   const uint32_t* Ws;
   int M, N, K;
   void* Y;
-  int ldy;  // row stride of Y in elements
+  int ldy;     // row stride of Y in elements
+  void* part;  // mx_gemm_part_bytes(M, N, K) of scratch
 };
+// Splits of K that a product of few tiles is computed in (1: none), and their fp32 sums' size.
+int mx_gemm_splits(int64_t M, int64_t N, int64_t K);
+size_t mx_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_gemm(const MxGemmArgs& a, int type, hipStream_t s);
 // The same for a few rows: whether it takes them, and the launch. The inline form, for at most
 // 16 rows, takes 16-bit X itself (a.Xc and a.Xs unused; (M - 1) ldx + K < 2^30).

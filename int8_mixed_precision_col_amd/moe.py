@@ -63,13 +63,10 @@ def moe_layer(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple
         out = X.new_empty((T, D))
     else:
         _need_shape(out, X.dtype, (T, D), X.device, "out")
-    if workspace is None:
-        nbytes = workspace_bytes(T, I, top_k)
-        if nbytes == 0:
-            raise ValueError(f"bad shape for moe_layer: T={T} I={I} top_k={top_k}")
-        workspace = X.new_empty((nbytes,), dtype=torch.uint8)
-    else:
-        mx4._need_workspace(workspace, X)
+    nbytes = workspace_bytes(T, I, top_k)
+    if nbytes == 0:
+        raise ValueError(f"bad shape for moe_layer: T={T} I={I} top_k={top_k}")
+    workspace = mx4._scratch(workspace, nbytes, X)
     ids = X.new_empty((T, top_k), dtype=torch.int32)
     weights = X.new_empty((T, top_k), dtype=torch.float32)
     mx4._launch("moe_layer", X, X.data_ptr(), T, D, ld, dt, logits.data_ptr(), E, mx4.DTYPES[logits.dtype],

@@ -29,7 +29,8 @@ SIGNATURES = {
     "mx4_dequantize": (_int, [_p, _p, _i64, _i64, _int, _p, _i64, _p]),
     "mx4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "mx4_matmul": (_int, [_p, _i64, _i64, _i64, _int, _p, _p, _i64, _p, _p, _sz, _p]),
-    "mx4_matmul_q": (_int, [_p, _p, _i64, _i64, _p, _p, _i64, _int, _p, _p]),
+    "mx4_matmul_q_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mx4_matmul_q": (_int, [_p, _p, _i64, _i64, _p, _p, _i64, _int, _p, _p, _sz, _p]),
     "mx4_weight_only_matmul": (_int, [_p, _i64, _i64, _i64, _int, _p, _p, _i64, _p, _p]),
     "moe_layer_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "moe_layer": (_int, [_p, _i64, _i64, _i64, _int, _p, _i64, _int, _i64, _int, _int, _p, _p, _p,
@@ -80,8 +81,10 @@ def _sizes(rows: int, K: int) -> tuple[int, int]:
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_bytes(M: int, K: int, N: int) -> int:
-    return int(lib().mx4_matmul_workspace_bytes(M, K, N))
+def _workspace_bytes(M: int, K: int, N: int) -> tuple[int, int]:
+    """What mx4_matmul and mx4_matmul_q need."""
+    L = lib()
+    return int(L.mx4_matmul_workspace_bytes(M, K, N)), int(L.mx4_matmul_q_workspace_bytes(M, K, N))
 
 
 _HALF = (torch.float16, torch.bfloat16)
@@ -121,10 +124,14 @@ def _need_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: int, K: int, like
                      f"{K} elements have {want[0]} and {want[1]}")
 
 
-def _need_workspace(workspace: torch.Tensor, like: torch.Tensor) -> None:
+def _scratch(workspace: torch.Tensor | None, nbytes: int, like: torch.Tensor) -> torch.Tensor | None:
+    """The caller's workspace, checked, or a new one of nbytes (None for 0)."""
+    if workspace is None:
+        return like.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
     _need(workspace, torch.uint8, "workspace")
     if workspace.device != like.device:
         raise ValueError(f"workspace must be on {like.device}")
+    return workspace
 
 
 def _empty(rows: int, K: int, like: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
@@ -217,10 +224,11 @@ def _need_weight(w_codes: torch.Tensor, w_scales: torch.Tensor, K: int, like: to
 
 
 def make_workspace(M: int, K: int, N: int, device="cuda") -> torch.Tensor:
-    """A workspace for ``matmul`` (empty where the shape needs none: M <= 16)."""
+    """A workspace for ``matmul`` (empty where the shape needs none: M <= 16), enough for
+    ``matmul_q`` too."""
     if _sizes(M, K)[0] == 0 or _sizes(N, K)[0] == 0 or N % 16:
         raise ValueError(f"bad shape for mx4_matmul: M={M} K={K} N={N}")
-    return torch.empty((_workspace_bytes(M, K, N),), dtype=torch.uint8, device=device)
+    return torch.empty((_workspace_bytes(M, K, N)[0],), dtype=torch.uint8, device=device)
 
 
 def matmul(X: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
@@ -232,12 +240,7 @@ def matmul(X: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
         out = X.new_empty((M, N))
     else:
         _need_shape(out, X.dtype, (M, N), X.device, "out")
-    if workspace is not None:
-        _need_workspace(workspace, X)
-    else:
-        nbytes = _workspace_bytes(M, K, N)
-        if nbytes:
-            workspace = X.new_empty((nbytes,), dtype=torch.uint8)
+    workspace = _scratch(workspace, _workspace_bytes(M, K, N)[0], X)
     ws, wb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _launch("mx4_matmul", X, X.data_ptr(), M, K, ld, dt, w_codes.data_ptr(), w_scales.data_ptr(), N,
             out.data_ptr(), ws, wb)
@@ -246,7 +249,7 @@ def matmul(X: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
 
 def matmul_q(x_codes: torch.Tensor, x_scales: torch.Tensor, M: int, K: int, w_codes: torch.Tensor,
              w_scales: torch.Tensor, dtype: torch.dtype = torch.float16,
-             out: torch.Tensor | None = None) -> torch.Tensor:
+             workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [M, N] in fp16 or bf16 from X [M, K] already quantized (once for several weights)."""
     if dtype not in _HALF:
         raise ValueError(f"dtype must be fp16 or bf16, got {dtype}")
@@ -256,8 +259,10 @@ def matmul_q(x_codes: torch.Tensor, x_scales: torch.Tensor, M: int, K: int, w_co
         out = x_codes.new_empty((M, N), dtype=dtype)
     else:
         _need_shape(out, dtype, (M, N), x_codes.device, "out")
+    workspace = _scratch(workspace, _workspace_bytes(M, K, N)[1], x_codes)
+    ws, wb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _launch("mx4_matmul_q", x_codes, x_codes.data_ptr(), x_scales.data_ptr(), M, K, w_codes.data_ptr(),
-            w_scales.data_ptr(), N, DTYPES[dtype], out.data_ptr())
+            w_scales.data_ptr(), N, DTYPES[dtype], out.data_ptr(), ws, wb)
     return out
 
 

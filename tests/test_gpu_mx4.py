@@ -168,7 +168,9 @@ def product_case(M, K, N, dtype, seed):
 
 PRODUCTS = [(1, 16, 16), (1, 4096, 256), (3, 1040, 48), (16, 128, 16), (16, 1024, 1024), (17, 528, 272),
             (40, 2064, 144), (64, 4096, 512), (65, 144, 4112), (100, 16, 800), (256, 1024, 256), (300, 1040, 528),
-            (513, 2048, 272), (1000, 640, 1296)]
+            (513, 2048, 272), (1000, 640, 1296),
+            # K split over few tiles: 8 of 24 quads, 5 of 16 with a short last one, 2
+            (65, 12288, 272), (130, 7760, 528), (140, 8208, 4112)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
@@ -178,7 +180,7 @@ def test_matmul(M, K, N, dtype):
     x, w, xv, wv = product_case(M, K, N, dtype, M + N)
     W = mx4.prepare_weight(w, 1)
     want, S = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
-    roundings = -(-K // 128) + 32
+    roundings = -(-K // 128) + 32   # 32: the waves or splits that are joined
     guard = torch.full((M * N + 64,), 3.0, dtype=dtype, device="cuda")
     y = mx4.matmul(x, *W, out=guard[:M * N].view(M, N))
     check_sum(y, want, S, dtype, roundings)
@@ -284,19 +286,19 @@ def test_streams_and_two_calls_at_once():
         assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(c, want[2])
 
 
-@pytest.mark.parametrize("M", [9, 40, 200])
-def test_graph_capture_and_replay(M):
-    x = rows(M, 1040, F16, 1)
-    W = mx4.prepare_weight(rows(528, 1040, F16, 3), 1)
+@pytest.mark.parametrize("M,K", [(9, 1040), (40, 1040), (200, 1040), (100, 8192)])
+def test_graph_capture_and_replay(M, K):
+    x = rows(M, K, F16, 1)
+    W = mx4.prepare_weight(rows(528, K, F16, 3), 1)
     out = torch.empty((M, 528), dtype=F16, device="cuda")
-    work = mx4.make_workspace(M, 1040, 528)
+    work = mx4.make_workspace(M, K, 528)
     mx4.matmul(x, *W, workspace=work, out=out)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         mx4.matmul(x, *W, workspace=work, out=out)
     for seed in range(3):
-        x.copy_(rows(M, 1040, F16, 10 + seed))
+        x.copy_(rows(M, K, F16, 10 + seed))
         out.zero_()
         graph.replay()
         torch.cuda.synchronize()
