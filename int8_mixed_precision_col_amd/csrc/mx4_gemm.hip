@@ -300,6 +300,33 @@ static hipError_t run(const MxGemmArgs& g, int type, hipStream_t s) {
   return hipGetLastError();
 }
 
+static hipError_t run_tile(Tile t, const MxGemmArgs& g, int type, hipStream_t s) {
+  if (t == Tile::L) return run<MxL>(g, type, s);
+  if (t == Tile::M) return run<MxM>(g, type, s);
+  return run<MxS>(g, type, s);
+}
+
+// Features [n0, n1) as a product of their own (n0 a multiple of 16), into the same rows of Y.
+static MxGemmArgs feature_slice(const MxGemmArgs& g, int n0, int n1) {
+  MxGemmArgs s = g;
+  s.Wc = g.Wc + static_cast<size_t>(n0 / 16) * mx_ks(g.K) * kUnitBytes;
+  s.Ws = g.Ws + static_cast<size_t>(n0 / 16) * mx_quads(g.K) * 64;
+  s.Y = static_cast<uint16_t*>(g.Y) + n0;
+  s.N = n1 - n0;
+  return s;
+}
+
+static double tile_cost(long M, long N, Tile* t) {
+  return best_cost([&](int tn, int tm) { return ((N + tn - 1) / tn) * ((M + tm - 1) / tm); }, t);
+}
+
+// The leading features that fill whole waves of 256 x 256 tiles, 0 if that is none or all.
+static int whole_wave_features(long M, long N) {
+  const long cus = device_cus(), tiles_m = (M + 255) / 256;
+  const long n = ((N + 255) / 256) * tiles_m / cus * cus / tiles_m * 256;
+  return n < N ? static_cast<int>(n) : 0;
+}
+
 template <class C, class T>
 static hipError_t run_split(const MxGemmArgs& g, int splits, hipStream_t s) {
   const int tiles_n = (g.N + C::TN - 1) / C::TN, tiles_m = (g.M + C::TM - 1) / C::TM, tiles = tiles_n * tiles_m;
@@ -335,12 +362,20 @@ size_t mx_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_mx_gemm(const MxGemmArgs& g, int type, hipStream_t s) {
   const int splits = mx_gemm_splits(g.M, g.N, g.K);
   if (splits > 1) return type == kMxF16 ? run_split<MxS, F16>(g, splits, s) : run_split<MxS, B16>(g, splits, s);
-  Tile t;
-  best_cost([&](int tn, int tm) {
-    return static_cast<long>((g.N + tn - 1) / tn) * ((g.M + tm - 1) / tm); }, &t);
-  if (t == Tile::L) return run<MxL>(g, type, s);
-  if (t == Tile::M) return run<MxM>(g, type, s);
-  return run<MxS>(g, type, s);
+  // Tile shape, and a second launch for the features beyond whole waves of 256 x 256 tiles, by
+  // the int8 product's estimate (gemm_tiles.hpp): the tiles' relative rates are within a few
+  // percent of its (4096 x 12288 x 49152: 128 x 256 tiles at 0.86 of the 256 x 256 rate, 128 x
+  // 128 at 0.80), and it picks the fastest shape or one within 3% of it for 64 to 4096 rows of
+  // 1040 x 528 to 12288 x 49152. Two launches: 2048 x 4096 x 11008 56.3 -> 51.2 us.
+  Tile t, rest_t;
+  const double single = tile_cost(g.M, g.N, &t);
+  const int lead = whole_wave_features(g.M, g.N);
+  if (lead > 0 && tile_cost(g.M, lead, &rest_t) + tile_cost(g.M, g.N - lead, &rest_t) + 0.05 < single) {
+    const hipError_t e = run<MxL>(feature_slice(g, 0, lead), type, s);
+    if (e != hipSuccess) return e;
+    return run_tile(rest_t, feature_slice(g, lead, g.N), type, s);
+  }
+  return run_tile(t, g, type, s);
 }
 
 }  // namespace i8mm

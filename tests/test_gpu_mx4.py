@@ -170,7 +170,9 @@ PRODUCTS = [(1, 16, 16), (1, 4096, 256), (3, 1040, 48), (16, 128, 16), (16, 1024
             (40, 2064, 144), (64, 4096, 512), (65, 144, 4112), (100, 16, 800), (256, 1024, 256), (300, 1040, 528),
             (513, 2048, 272), (1000, 640, 1296),
             # K split over few tiles: 8 of 24 quads, 5 of 16 with a short last one, 2
-            (65, 12288, 272), (130, 7760, 528), (140, 8208, 4112)]
+            (65, 12288, 272), (130, 7760, 528), (140, 8208, 4112),
+            # two launches: whole waves of 256 x 256 tiles, then the rest
+            (2048, 272, 10000)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
