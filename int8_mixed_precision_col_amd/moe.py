@@ -20,16 +20,23 @@ def workspace_bytes(T: int, I: int, top_k: int) -> int:
 
 def _rows(pair, name: str) -> tuple[int, int]:
     """(weight format, output features) of a prepared weight pair."""
-    codes, consts = pair
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 4 or codes.dtype not in (torch.int8, torch.uint8):
+    codes, _ = pair
+    shape = codes.shape if isinstance(codes, torch.Tensor) else ()
+    if len(shape) != 4 or codes.dtype not in (torch.int8, torch.uint8):
         raise ValueError(f"{name} must be a prepared int8 or MX4 weight")
-    return int(codes.dtype == torch.uint8), 16 * codes.shape[0]
+    return int(codes.dtype is torch.uint8), 16 * shape[0]
 
 
 def _need_pair(pair, fmt: int, rows: int, K: int, like: torch.Tensor, name: str) -> None:
+    codes, consts = pair
     if fmt:
-        mx4._need_mx4(*pair, rows, K, like, name)
-    elif binding._need_weight(*pair, K, like.device) != rows:
+        mx4._need_mx4(codes, consts, rows, K, like, name)
+        return
+    if (consts.dtype is torch.float32 and codes.is_contiguous() and consts.is_contiguous() and consts.numel() == rows
+            and consts.dim() == 1 and codes.numel() == binding._prepared_bytes(K, rows) != 0
+            and codes.get_device() == consts.get_device() == like.get_device()):
+        return
+    if binding._need_weight(codes, consts, K, like.device) != rows:
         raise ValueError(f"{name} has {pair[1].numel()} column constants for {rows} output features")
 
 
@@ -48,8 +55,8 @@ def moe_layer(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple
     T, D, ld, dt = mx4._need_rows(X, "X")
     if not isinstance(logits, torch.Tensor) or logits.dtype not in mx4.DTYPES or logits.dim() != 2:
         raise ValueError("logits must be a 2-D fp16, bf16 or fp32 tensor")
-    E = logits.shape[1]
-    if logits.shape[0] != T or not logits.is_contiguous() or logits.get_device() != X.get_device():
+    rows, E = logits.shape
+    if rows != T or not logits.is_contiguous() or logits.get_device() != X.get_device():
         _need_shape(logits, logits.dtype, (T, E), X.device, "logits")
     fmt, rows = _rows(gate_up, "gate_up")
     if _rows(down, "down")[0] != fmt:

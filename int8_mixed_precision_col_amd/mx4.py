@@ -61,14 +61,19 @@ def _stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+@functools.cache
+def _function(name: str):
+    return getattr(lib(), name)
+
+
 def _launch(name: str, t: torch.Tensor, *args) -> None:
     """One library call on t's device, current or not, and on its current stream."""
     index = t.get_device()
     if index == torch._C._cuda_getDevice():
-        rc = getattr(lib(), name)(*args, _stream(index))
+        rc = _function(name)(*args, _stream(index))
     else:
         with torch.cuda.device(index):
-            rc = getattr(lib(), name)(*args, _stream(index))
+            rc = _function(name)(*args, _stream(index))
     if rc:
         raise Int8mmError(rc, name)
 
@@ -87,25 +92,27 @@ def _workspace_bytes(M: int, K: int, N: int) -> tuple[int, int]:
     return int(L.mx4_matmul_workspace_bytes(M, K, N)), int(L.mx4_matmul_q_workspace_bytes(M, K, N))
 
 
-_HALF = (torch.float16, torch.bfloat16)
+_HALF = {torch.float16: 0, torch.bfloat16: 1}
 
 
 def _need_rows(X: torch.Tensor, name: str, types=_HALF) -> tuple:
     """(M, K, row stride, dtype code) of a matrix whose rows are contiguous."""
     if not isinstance(X, torch.Tensor) or not binding._on_device(X):
         raise ValueError(f"{name} must be a HIP device tensor")
-    if X.dtype not in types:
-        raise ValueError(f"{name} must be one of {types}, got {X.dtype}")
-    if X.dim() != 2:
-        raise ValueError(f"{name} must be 2-D [M, K], got shape {tuple(X.shape)}")
-    M, K = X.shape
+    dt = types.get(X.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be one of {tuple(types)}, got {X.dtype}")
+    shape = X.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D [M, K], got shape {tuple(shape)}")
+    M, K = shape
     ld, unit = X.stride()
     if M == 1:
         ld = K
     if (K > 1 and unit != 1) or ld < K or ld % 8:
         raise ValueError(f"{name}'s rows must be contiguous, with a row stride that is a multiple of 8 "
                          f"and at least {K}: its strides are {X.stride()}")
-    return M, K, ld, DTYPES[X.dtype]
+    return M, K, ld, dt
 
 
 def _need_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: int, K: int, like: torch.Tensor, name: str) -> None:
@@ -206,7 +213,7 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int,
         out = codes.new_empty((M, K), dtype=dtype)
         ld, dt = K, DTYPES[dtype]
     else:
-        m, k, ld, dt = _need_rows(out, "out", tuple(DTYPES))
+        m, k, ld, dt = _need_rows(out, "out", DTYPES)
         if (m, k) != (M, K) or out.device != codes.device or out.dtype != dtype:
             raise ValueError(f"out must be {dtype} [{M}, {K}] on {codes.device}, got {out.dtype} {tuple(out.shape)} "
                              f"on {out.device}")
@@ -216,9 +223,10 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int,
 
 def _need_weight(w_codes: torch.Tensor, w_scales: torch.Tensor, K: int, like: torch.Tensor) -> int:
     """A tiled weight for K input features; returns N."""
-    if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 4:
+    shape = w_codes.shape if isinstance(w_codes, torch.Tensor) else ()
+    if len(shape) != 4:
         raise ValueError("the weight's codes must be the tiled tensor (N / 16, ceil(K / 128), 16, 64)")
-    N = 16 * w_codes.shape[0]
+    N = 16 * shape[0]
     _need_mx4(w_codes, w_scales, N, K, like, "weight")
     return N
 
