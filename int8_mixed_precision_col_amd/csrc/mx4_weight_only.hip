@@ -22,16 +22,40 @@ __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnly
   // elements past K are out of the resource's range and read zeros
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.M - 1) * a.ldx + a.K) * 2));
   const int M = a.M, mrow = min(row, M - 1);  // rows past M repeat the last (outputs discarded)
+  // With one row group the wave's next quad is on its way while this one is multiplied (16 x
+  // 4096 x 4096 5.4 -> 5.1 us); with more the registers it takes cost more than it gives (16 x
+  // 8192 x 8192, two groups: 10.5 -> 11.7 us).
+  constexpr bool AHEAD = RG == 1;
   v4f acc[RG] = {};
-  for (int q = wave; q < quads; q += kMxWoWaves) {
-    WeightQuad<true> w[RG];
-    ActQuad<true, 16> x;
+  WeightQuad<true> w[RG], next[AHEAD ? RG : 1];
+  ActQuad<true, 16> x;
+  auto load_x = [&](int q) {
     x.load(xr, q, a.K, M, lane, [&](int i) { return static_cast<unsigned>(i * a.ldx) * 2u; });
+  };
+  auto load_w = [&](auto& to, int q) {
 #pragma unroll
-    for (int r = 0; r < RG; ++r) w[r].load(a.Wc, a.Ws, min(g0 + r, groups - 1), ks, quads, q, lane);
+    for (int r = 0; r < RG; ++r) to[r].load(a.Wc, a.Ws, min(g0 + r, groups - 1), ks, quads, q, lane);
+  };
+  if (AHEAD && wave < quads) {
+    load_x(wave);
+    if constexpr (AHEAD) load_w(next, wave);
+  }
+  for (int q = wave; q < quads; q += kMxWoWaves) {
+    if constexpr (!AHEAD) {
+      load_x(q);
+      load_w(w, q);
+    }
     wave_lds_fence();
     x.store(buf, M, M, lane);
     wave_lds_fence();
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int r = 0; r < RG; ++r) w[r] = next[r];
+      if (q + kMxWoWaves < quads) {
+        load_x(q + kMxWoWaves);
+        load_w(next, q + kMxWoWaves);
+      }
+    }
     mma_quad<T, true, RG>(w, acc, [&](int j, int v) { return act_operand<true>(buf, M, mrow, j, v, lane); });
   }
 #pragma unroll
