@@ -60,6 +60,8 @@ def check(X, logits, pairs, values, k, renorm, **kw):
     (1, 16, 16, 1, 1, True), (1, 512, 256, 8, 2, True), (5, 528, 144, 10, 3, False), (16, 1040, 528, 4, 4, True),
     (16, 256, 128, 70, 8, False), (9, 144, 48, 500, 16, True), (2, 2064, 32, 3, 1, False), (16, 128, 1040, 2, 2, False),
     (13, 640, 272, 64, 6, True),
+    # X past, at and within what the first launch holds in LDS at once; long hidden rows
+    (16, 4224, 32, 3, 2, True), (16, 4096, 48, 4, 2, False), (3, 12304, 32, 4, 2, True), (4, 64, 4112, 3, 2, True),
 ])
 def test_layer(T, D, I, E, k, renorm, dtype, fmt):
     announce(f"moe T={T} D={D} I={I} E={E} k={k} {dtype} {fmt}")

@@ -171,8 +171,10 @@ PRODUCTS = [(1, 16, 16), (1, 4096, 256), (3, 1040, 48), (16, 128, 16), (16, 1024
             (513, 2048, 272), (1000, 640, 1296),
             # K split over few tiles: 8 of 24 quads, 5 of 16 with a short last one, 2
             (65, 12288, 272), (130, 7760, 528), (140, 8208, 4112),
-            # two launches: whole waves of 256 x 256 tiles, then the rest
-            (2048, 272, 10000)]
+            # two launches: whole waves of 256 x 256 tiles, then the rest; 128 x 256 tiles
+            (2048, 272, 10000), (512, 144, 16384),
+            # few rows: long K, and two and four groups of features per workgroup
+            (16, 12304, 48), (40, 12304, 144), (5, 272, 8208), (5, 272, 16400), (20, 272, 16400), (50, 144, 16400)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
@@ -216,7 +218,7 @@ def test_matmul_strided_rows(M, dtype):
 
 
 WEIGHT_ONLY = [(1, 16, 16), (1, 4096, 512), (2, 144, 272), (5, 528, 48), (8, 1040, 4112), (13, 8192, 272), (16, 4112, 16),
-               (16, 2048, 1040), (9, 512, 8208)]
+               (16, 2048, 1040), (9, 512, 8208), (3, 528, 16400), (16, 12304, 48)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
@@ -305,6 +307,37 @@ def test_graph_capture_and_replay(M, K):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, mx4.matmul(x, *W))
+
+
+def test_offsets_beyond_32_bits():
+    """A weight of over 4 GB of codes and activations of over 4 GB: the last rows are right."""
+    N, K, M = 131088, 65536, 3
+    announce(f"mx4 with {N} x {K} weights")
+    w = rows(32, K, B16, 1, 2)
+    tail = mx4.prepare_weight(w, 1)
+    codes = torch.zeros((N // 16, K // 128, 16, 64), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((N // 16, K // 512, 64, 4), dtype=torch.uint8, device="cuda")
+    assert codes.numel() > 1 << 32
+    codes[-1], scales[-1] = tail[0][1], tail[1][1]
+    codes[0], scales[0] = tail[0][0], tail[1][0]
+    wv = ref.mx4_round(f64(w))
+    for f, m, roundings in ((mx4.matmul, M, K // 128 + 32), (mx4.matmul, 70, K // 128 + 32),
+                            (mx4.weight_only_matmul, M, K // 4 + 32)):
+        x = rows(m, K, B16, 2, 2)
+        xv = f64(x) if f is mx4.weight_only_matmul else ref.mx4_round(f64(x))
+        y = f(x, codes, scales)
+        want, S = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+        check_sum(torch.cat((y[:, :16], y[:, -16:]), 1), want, S, B16, roundings)
+        assert int(torch.count_nonzero(y[:, 16:-16])) == 0
+    del codes, scales
+    big = torch.zeros((32784, K + 64), dtype=B16, device="cuda")
+    big[-5:, :K] = rows(5, K, B16, 3)
+    q = mx4.quantize(big[:, :K])
+    last = mx4.quantize(big[-16:, :K])
+    assert torch.equal(q[0][-1], last[0][0]) and torch.equal(q[1][-1], last[1][0])
+    back = mx4.dequantize(*q, 32784, K, B16)
+    assert np.array_equal(f64(back[-5:]), ref.mx4_round(f64(big[-5:, :K])))
+    assert int(torch.count_nonzero(back[:-5])) == 0
 
 
 def test_quantize_once_for_three_weights():

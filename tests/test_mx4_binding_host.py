@@ -148,3 +148,35 @@ def test_moe_refused(fake):
     with pytest.raises(ValueError):
         moe.moe_layer(X, lg, a8, (b8[0], torch.zeros(4 * 48)), 2)
     assert fake.calls == []
+
+
+def test_launch_makes_the_tensors_device_current(monkeypatch):
+    """A tensor on another device than the current one: the call runs under its device, on its
+    stream; a status other than 0 is raised."""
+    seen = []
+
+    class Tensor:
+        def get_device(self):
+            return 1
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            seen.append(("enter", self.index))
+
+        def __exit__(self, *exc):
+            seen.append(("exit", self.index))
+
+    status = 0
+    monkeypatch.setattr(mx4.torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(mx4.torch.cuda, "device", Device)
+    monkeypatch.setattr(mx4, "_stream", lambda index: 100 + index)
+    monkeypatch.setattr(mx4, "_function", lambda name: lambda *args: (seen.append((name, args)), status)[1])
+    mx4._launch("mx4_quantize", Tensor(), 7, 8)
+    assert seen == [("enter", 1), ("mx4_quantize", (7, 8, 101)), ("exit", 1)]
+    status = 2
+    with pytest.raises(binding.Int8mmError):
+        mx4._launch("mx4_quantize", Tensor(), 7, 8)
+    assert seen[-1] == ("exit", 1)
