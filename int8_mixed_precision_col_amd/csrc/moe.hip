@@ -462,6 +462,9 @@ static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s)
   constexpr int UK = WeightFmt<MX>::UK;
   const int quads = ((a.D + UK - 1) / UK + 3) / 4;
   const size_t lds = static_cast<size_t>(up_resident<MX>(a.T, quads) ? quads : kUpWaves) * act_bytes<MX>(a.T);
+  constexpr size_t kStatic = sizeof(MoeTable) + sizeof(float) * kUpWaves * 2 * 16 * 17;
+  static_assert(kUpResident + kStatic <= kMaxLds && kUpWaves * act_bytes<MX>(kMoeMaxTokens) + kStatic <= kMaxLds,
+                "k_moe_gate_up's LDS");
   const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16);
   const unsigned blocks = static_cast<unsigned>(steps < kMoeBlocks ? steps : kMoeBlocks);
   hipLaunchKernelGGL((k_moe_gate_up<T, MX>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, ids, weights);

@@ -7,6 +7,10 @@
 
 namespace i8mm {
 
+// LDS of a workgroup: a launch that asks for more ends the queue, so launchers that size it by
+// their arguments check.
+constexpr size_t kMaxLds = 160 << 10;
+
 // Element types of the C ABI (mx4_dtype).
 enum MxType { kMxF16 = 0, kMxBf16 = 1, kMxF32 = 2 };
 

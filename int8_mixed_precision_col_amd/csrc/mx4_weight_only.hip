@@ -12,8 +12,10 @@ constexpr int kMxWoWaves = 8;
 
 template <class T, int RG>
 __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnlyArgs a) {
-  extern __shared__ __attribute__((aligned(16))) char s_x[];  // [waves][act_bytes(M)]
-  __shared__ float red[kMxWoWaves][16][16 * RG + 1];
+  // [waves][act_bytes(M)], and once the products are done the waves' sums: both at a time do
+  // not fit for 16 tokens and four row groups
+  extern __shared__ __attribute__((aligned(16))) char s_x[];
+  float(*red)[16][16 * RG + 1] = reinterpret_cast<float(*)[16][16 * RG + 1]>(s_x);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15;
   const int ks = mx_ks(a.K), quads = mx_quads(a.K), groups = a.N / 16;
@@ -58,6 +60,7 @@ __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnly
     }
     mma_quad<T, true, RG>(w, acc, [&](int j, int v) { return act_operand<true>(buf, M, mrow, j, v, lane); });
   }
+  lds_barrier();  // every wave is done with its rows
 #pragma unroll
   for (int r = 0; r < RG; ++r)
 #pragma unroll
@@ -76,7 +79,10 @@ __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnly
 template <int RG>
 static hipError_t run_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
   const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kMxWoWaves);
-  const size_t lds = static_cast<size_t>(kMxWoWaves) * act_bytes<true>(a.M);
+  const size_t rows = static_cast<size_t>(kMxWoWaves) * act_bytes<true>(a.M);
+  const size_t sums = sizeof(float) * kMxWoWaves * 16 * (16 * RG + 1);
+  const size_t lds = rows > sums ? rows : sums;
+  if (lds > kMaxLds) return hipErrorInvalidConfiguration;
   if (type == kMxF16) hipLaunchKernelGGL((k_mx_weight_only<F16, RG>), grid, block, lds, s, a);
   else hipLaunchKernelGGL((k_mx_weight_only<B16, RG>), grid, block, lds, s, a);
   return hipGetLastError();

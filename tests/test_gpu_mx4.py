@@ -218,7 +218,7 @@ def test_matmul_strided_rows(M, dtype):
 
 
 WEIGHT_ONLY = [(1, 16, 16), (1, 4096, 512), (2, 144, 272), (5, 528, 48), (8, 1040, 4112), (13, 8192, 272), (16, 4112, 16),
-               (16, 2048, 1040), (9, 512, 8208), (3, 528, 16400), (16, 12304, 48)]
+               (16, 2048, 1040), (9, 512, 8208), (3, 528, 16400), (16, 12304, 48), (16, 528, 16400)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
