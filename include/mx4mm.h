@@ -76,12 +76,13 @@ int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64
  * Y [M, N] = MX4(X) W^T: X is quantized as by mx4_quantize, the products of codes are scaled
  * by both blocks' powers of two and accumulated in fp32, Y is rounded once to dtype
  * (MX4_F16 or MX4_BF16, X's type).
- * M <= 16 is one launch, without a workspace, and needs M ldx < 2^30; more rows are a
- * quantization launch and the product (M <= 64 a weight stream, beyond that output tiles;
- * where K is long and the tiles are few, K is split and a third launch joins the sums).
- *   workspace   at least mx4_matmul_workspace_bytes(M, K, N) bytes (0 where M <= 16, then
- *               workspace may be NULL, and on bad shapes); its contents do not matter. Calls
- *               that may run at the same time need workspaces of their own.
+ * Few rows (M <= 16, and up to 64 with M ceil(K / 512) <= 96) are one launch, without a
+ * workspace, and need M ldx < 2^30; more are a quantization launch and the product (M <= 64
+ * a weight stream, beyond that output tiles; where K is long and the tiles are few, K is
+ * split and a third launch joins the sums).
+ *   workspace   at least mx4_matmul_workspace_bytes(M, K, N) bytes (0 for the few rows above,
+ *               then workspace may be NULL, and on bad shapes); its contents do not matter.
+ *               Calls that may run at the same time need workspaces of their own.
  */
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N);
 int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype,

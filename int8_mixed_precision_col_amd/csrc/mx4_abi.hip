@@ -105,7 +105,7 @@ int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64
 }
 
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (bad_product(M, K, N) || M <= kMaxFew) return 0;
+  if (bad_product(M, K, N) || i8mm::mx_few_inline(M, K)) return 0;
   return round256(codes_bytes(M, K)) + round256(scales_bytes(M, K)) + part_bytes(M, K, N);
 }
 
@@ -118,7 +118,7 @@ int mx4_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype, cons
                hipStream_t stream) {
   if (!X || !w_codes || !w_scales || !Y) return INT8MM_E_NULL;
   if (bad_product(M, K, N) || bad_ld(ldx, K) || bad_dtype16(dtype)) return INT8MM_E_SHAPE;
-  const bool few = M <= kMaxFew;
+  const bool few = i8mm::mx_few_inline(M, K);
   if (few && M * ldx >= kMaxBuffer) return INT8MM_E_SHAPE;
   if (!few && !workspace) return INT8MM_E_NULL;
   if (!aligned16(X) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y) || !aligned16(workspace))

@@ -5,10 +5,10 @@
 // features and all of M; its waves share the quads of K (four 128-element units each) and
 // their fp32 partial sums meet in LDS. Each unit is one operand of
 // v_mfma_scale_f32_16x16x128_f8f6f4, straight from global memory to registers.
-// Up to 16 tokens X is quantized on the way (INLINE) and the call is one launch: a wave loads
-// a row's whole quad at once (1 KB, a lane holds 8 elements and four lanes a block), and the
-// codes and scale bytes go through a buffer of its own in LDS into operand order. Loading
-// 16-bit X in operand order instead takes 16 gathers per quad whatever the number of rows.
+// With few enough rows X is quantized on the way and the call is one launch: a wave loads a
+// row's whole quad at once (1 KB, a lane holds 8 elements and four lanes a block), and the codes
+// and scale bytes go through LDS into operand order. Loading 16-bit X in operand order instead
+// takes 16 gathers per quad whatever the number of rows (8 x 4096 x 4096: 6.7 against 4.8 us).
 #include "mx4.hpp"
 #include "mx4_launch.hpp"
 
@@ -19,24 +19,41 @@ constexpr int kFewWaves = 8;
 // the 16 rows of an operand read on distinct banks
 constexpr int kFewStride = 256 + 16;
 
-template <class T, int G, int RG, bool INLINE>
+// Where the MX4 activations come from: already tiled; quantized by each wave for the quads it
+// multiplies; or all of them quantized by the workgroup's waves together, into LDS.
+enum class FewX { kTiled, kOwn, kShared };
+
+// A row's quad, 8 elements per lane, to codes and scale bytes at `to`.
+template <class T>
+__device__ __forceinline__ void few_quantize(const v4u& x, char* to, int lane) {
+  const unsigned b = mx_scale_byte(T::exponent(max_of_four_lanes(mx_max_bits(x))));
+  *reinterpret_cast<unsigned*>(to + 4 * lane) = mx_codes8<T>(x, b);
+  // block (lane / 4) % 4 of unit lane / 16: byte `unit` of the block's dword
+  if ((lane & 3) == 0) to[256 + (lane & 12) + (lane >> 4)] = static_cast<char>(b);
+}
+
+template <class T, int G, int RG, FewX FROM>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const void* X, int64_t ldx) {
-  static_assert(!INLINE || G == 1, "one row group is quantized in registers");
-  __shared__ float red[kFewWaves][16 * G][16 * RG + 1];
-  __shared__ __attribute__((aligned(16))) char s_x[INLINE ? kFewWaves * 16 * kFewStride : 16];
+  static_assert(FROM != FewX::kOwn || G == 1, "a wave quantizes one row group");
+  // rows of kFewStride, then the waves' sums in their place: few_lds()
+  extern __shared__ __attribute__((aligned(16))) char s_x[];
+  float(*red)[16 * G][16 * RG + 1] = reinterpret_cast<float(*)[16 * G][16 * RG + 1]>(s_x);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15;
   const int ks = mx_ks(a.K), quads = mx_quads(a.K);
   const int groups = a.N / 16, m_groups = (a.M + 15) / 16;
   const int g0 = blockIdx.x * RG;
-  char* buf = s_x + (INLINE ? wave * 16 * kFewStride : 0);
   const unsigned lane_off = (lane & 15) * kUnitK + 16 * (lane >> 4);
 
   v4u w[RG][4], x[G][4];
   unsigned ws[RG], xs[G];
   const __amdgpu_buffer_rsrc_t xr =
-      make_rsrc(X, INLINE ? static_cast<unsigned>(((a.M - 1) * ldx + a.K) * 2) : 0u);
-  // units past ks repeat the last one, under padding scales (or, INLINE, zeros)
+      make_rsrc(X, FROM != FewX::kTiled ? static_cast<unsigned>(((a.M - 1) * ldx + a.K) * 2) : 0u);
+  auto load_row = [&](int m, int q) {  // 8 elements per lane of row m's quad; zeros past K
+    const int k = 512 * q + 8 * lane;
+    return buf_load16(xr, k < a.K ? static_cast<unsigned>(m * ldx + k) * 2u : kOOB);
+  };
+  // units past ks repeat the last one, under padding scales (or zeros)
   auto load = [&](int q) {
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
@@ -47,7 +64,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const v
             a.Wc + (g * ks + min(4 * q + j, ks - 1)) * kUnitBytes + lane_off));
       ws[r] = a.Ws[(g * quads + q) * 64 + lane];
     }
-    if constexpr (!INLINE) {
+    if constexpr (FROM == FewX::kTiled) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         const size_t g = min(i, m_groups - 1);
@@ -58,31 +75,50 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const v
       }
     }
   };
+  if constexpr (FROM == FewX::kShared) {
+    // (row, quad) pairs over the waves, four at a time; the first weights are asked for in between
+    const int pairs = a.M * quads;
+    for (int base = wave; base < pairs; base += 4 * kFewWaves) {
+      v4u raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = base + i * kFewWaves;
+        if (t < pairs) raw[i] = load_row(t / quads, t % quads);
+      }
+      if (base == wave && wave < quads) load(wave);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = base + i * kFewWaves;
+        if (t < pairs) few_quantize<T>(raw[i], s_x + ((t % quads) * a.M + t / quads) * kFewStride, lane);
+      }
+    }
+    lds_barrier();
+  }
   v4f acc[G][RG] = {};
   for (int q = wave; q < quads; q += kFewWaves) {
-    v4u raw[INLINE ? 16 : 1];
-    if constexpr (INLINE) {
-      const int k = 512 * q + 8 * lane;
+    v4u raw[FROM == FewX::kOwn ? 16 : 1];
+    if constexpr (FROM == FewX::kOwn) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i < a.M) raw[i] = buf_load16(xr, k < a.K ? static_cast<unsigned>(i * ldx + k) * 2u : kOOB);
+        if (i < a.M) raw[i] = load_row(i, q);
     }
-    load(q);
-    if constexpr (INLINE) {
-      wave_lds_fence();
+    if (FROM != FewX::kShared || q != wave) load(q);
+    if constexpr (FROM != FewX::kTiled) {
+      const char* rows = s_x + (FROM == FewX::kOwn ? wave * 16 : q * a.M) * kFewStride;
+      if constexpr (FROM == FewX::kOwn) {
+        wave_lds_fence();
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < a.M) {
-          const unsigned b = mx_scale_byte(T::exponent(max_of_four_lanes(mx_max_bits(raw[i]))));
-          *reinterpret_cast<unsigned*>(buf + i * kFewStride + 4 * lane) = mx_codes8<T>(raw[i], b);
-          // block (lane / 4) % 4 of unit lane / 16: byte `unit` of the block's dword
-          if ((lane & 3) == 0) buf[i * kFewStride + 256 + (lane & 12) + (lane >> 4)] = static_cast<char>(b);
-        }
-      wave_lds_fence();
-      const char* p = buf + min(row, a.M - 1) * kFewStride;  // rows past M repeat the last
+        for (int i = 0; i < 16; ++i)
+          if (i < a.M) few_quantize<T>(raw[i], s_x + (wave * 16 + i) * kFewStride, lane);
+        wave_lds_fence();
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[0][j] = *reinterpret_cast<const v4u*>(p + 64 * j + 16 * (lane >> 4));
-      xs[0] = *reinterpret_cast<const unsigned*>(p + 256 + 4 * (lane >> 4));
+      for (int i = 0; i < G; ++i) {
+        const char* p = rows + min(16 * i + row, a.M - 1) * kFewStride;  // rows past M repeat the last
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = *reinterpret_cast<const v4u*>(p + 64 * j + 16 * (lane >> 4));
+        xs[i] = *reinterpret_cast<const unsigned*>(p + 256 + 4 * (lane >> 4));
+      }
     }
 #pragma unroll
     for (int i = 0; i < G; ++i)
@@ -94,6 +130,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const v
         acc[i][r] = mx_mfma<3>(x[i][3], w[r][3], acc[i][r], xs[i], ws[r]);
       }
   }
+  if constexpr (FROM != FewX::kTiled) lds_barrier();  // every wave is done with the rows
   // lane l, register e: token 4 (l / 16) + e, feature l % 16
 #pragma unroll
   for (int i = 0; i < G; ++i)
@@ -112,11 +149,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const v
   }
 }
 
-template <int G, int RG, bool INLINE>
+static size_t few_lds(int64_t M, int64_t K, int G, int RG, FewX from) {
+  const size_t rows = from == FewX::kTiled ? 0 : from == FewX::kOwn ? kFewWaves * 16 : mx_quads(K) * M;
+  const size_t sums = sizeof(float) * kFewWaves * 16 * G * (16 * RG + 1);
+  return rows * kFewStride > sums ? rows * kFewStride : sums;
+}
+
+template <int G, int RG, FewX FROM>
 static hipError_t run(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
   const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kFewWaves);
-  if (type == kMxF16) hipLaunchKernelGGL((k_mx_few<F16, G, RG, INLINE>), grid, block, 0, s, a, X, ldx);
-  else hipLaunchKernelGGL((k_mx_few<B16, G, RG, INLINE>), grid, block, 0, s, a, X, ldx);
+  const size_t lds = few_lds(a.M, a.K, G, RG, FROM);
+  if (lds > kMaxLds) return hipErrorInvalidConfiguration;
+  if (type == kMxF16) hipLaunchKernelGGL((k_mx_few<F16, G, RG, FROM>), grid, block, lds, s, a, X, ldx);
+  else hipLaunchKernelGGL((k_mx_few<B16, G, RG, FROM>), grid, block, lds, s, a, X, ldx);
   return hipGetLastError();
 }
 
@@ -126,15 +171,27 @@ static hipError_t run(const MxGemmArgs& a, const void* X, int64_t ldx, int type,
 // 10.2 / 8.9.
 static int few_row_groups(int N) { return N < 16 * 512 ? 1 : N < 16 * 1024 ? 2 : 4; }
 
-template <int G, bool INLINE>
+template <int G, FewX FROM>
 static hipError_t pick(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
   const int rg = few_row_groups(a.N);
-  if (rg == 1) return run<G, 1, INLINE>(a, X, ldx, type, s);
-  return rg == 2 ? run<G, 2, INLINE>(a, X, ldx, type, s) : run<G, 4, INLINE>(a, X, ldx, type, s);
+  if (rg == 1) return run<G, 1, FROM>(a, X, ldx, type, s);
+  return rg == 2 ? run<G, 2, FROM>(a, X, ldx, type, s) : run<G, 4, FROM>(a, X, ldx, type, s);
 }
 
+// One launch instead of a quantization and a product. Up to 16 rows always; more while the
+// workgroup has at most 96 (row, quad) pairs to quantize, which every workgroup does again
+// (K x N, one launch against two, us in graphs: 32 rows of 1024 x 1024 5.0 / 5.2, 64 of 512 x 512
+// 4.9 / 6.2, 48 of 1024 x 1024 6.3 / 6.2, 24 of 2048 x 4096 6.4 / 5.6; 32 of 2048 x 4096, 128
+// pairs, 7.4 / 5.7; outside graphs the second launch costs another 4 us of the caller's time).
+bool mx_few_inline(int64_t M, int64_t K) { return M <= 16 || (M <= 64 && M * mx_quads(K) <= 96); }
+
+// Up to 16 rows, by the workgroup together while K has at most two quads, so that six of its
+// eight waves do not watch (16 rows of 1024 x 1024 3.5 against 3.9 us, of 2048 x 1024 4.7 against
+// 4.4).
 hipError_t launch_mx_few_inline(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
-  return pick<1, true>(a, X, ldx, type, s);
+  if (a.M <= 16)
+    return mx_quads(a.K) <= 2 ? pick<1, FewX::kShared>(a, X, ldx, type, s) : pick<1, FewX::kOwn>(a, X, ldx, type, s);
+  return a.M <= 32 ? pick<2, FewX::kShared>(a, X, ldx, type, s) : pick<4, FewX::kShared>(a, X, ldx, type, s);
 }
 
 // Up to 64 rows: at 64 the tiles are slower still (4096 x 4096 11.3 against 5.9 us, 4096 x
@@ -142,8 +199,8 @@ hipError_t launch_mx_few_inline(const MxGemmArgs& a, const void* X, int64_t ldx,
 bool mx_few(int64_t M) { return M <= 64; }
 
 hipError_t launch_mx_few(const MxGemmArgs& a, int type, hipStream_t s) {
-  if (a.M <= 16) return pick<1, false>(a, nullptr, 0, type, s);
-  return a.M <= 32 ? pick<2, false>(a, nullptr, 0, type, s) : pick<4, false>(a, nullptr, 0, type, s);
+  if (a.M <= 16) return pick<1, FewX::kTiled>(a, nullptr, 0, type, s);
+  return a.M <= 32 ? pick<2, FewX::kTiled>(a, nullptr, 0, type, s) : pick<4, FewX::kTiled>(a, nullptr, 0, type, s);
 }
 
 }  // namespace i8mm

@@ -53,10 +53,11 @@ struct MxGemmArgs {
 int mx_gemm_splits(int64_t M, int64_t N, int64_t K);
 size_t mx_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_gemm(const MxGemmArgs& a, int type, hipStream_t s);
-// The same for a few rows: whether it takes them, and the launch. The inline form, for at most
-// 16 rows, takes 16-bit X itself (a.Xc and a.Xs unused; (M - 1) ldx + K < 2^30).
+// The same for a few rows: whether it takes them, and the launch. The inline form takes 16-bit
+// X itself (a.Xc and a.Xs unused; M ldx < 2^30).
 bool mx_few(int64_t M);
 hipError_t launch_mx_few(const MxGemmArgs& a, int type, hipStream_t s);
+bool mx_few_inline(int64_t M, int64_t K);
 hipError_t launch_mx_few_inline(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s);
 
 // Y [M][N] = X W4^T for at most 16 rows of 16-bit X.

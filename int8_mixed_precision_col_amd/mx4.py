@@ -232,7 +232,7 @@ def _need_weight(w_codes: torch.Tensor, w_scales: torch.Tensor, K: int, like: to
 
 
 def make_workspace(M: int, K: int, N: int, device="cuda") -> torch.Tensor:
-    """A workspace for ``matmul`` (empty where the shape needs none: M <= 16), enough for
+    """A workspace for ``matmul`` (empty where the shape needs none: few rows), enough for
     ``matmul_q`` too."""
     if _sizes(M, K)[0] == 0 or _sizes(N, K)[0] == 0 or N % 16:
         raise ValueError(f"bad shape for mx4_matmul: M={M} K={K} N={N}")

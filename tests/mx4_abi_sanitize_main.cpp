@@ -72,6 +72,7 @@ int main() {
   // the largest shapes that are taken
   expect("codes largest", static_cast<long long>(mx4_codes_bytes(int64_t(1) << 24, 4096)), int64_t(1) << 35);
   expect("matmul ws few", static_cast<long long>(mx4_matmul_workspace_bytes(16, 4096, 4096)), 0);
+  expect("matmul ws 64 rows", static_cast<long long>(mx4_matmul_workspace_bytes(64, 512, 4096)), 0);
   expect("workspace", mx4_matmul(P, 64, 4096, 4096, 0, B, B, 4096, P, P, 1, nullptr), INT8MM_E_WORKSPACE);
   if (failures == 0) printf("all checks passed\n");
   return failures ? 1 : 0;

@@ -174,7 +174,8 @@ PRODUCTS = [(1, 16, 16), (1, 4096, 256), (3, 1040, 48), (16, 128, 16), (16, 1024
             # two launches: whole waves of 256 x 256 tiles, then the rest; 128 x 256 tiles
             (2048, 272, 10000), (512, 144, 16384),
             # few rows: long K, and two and four groups of features per workgroup
-            (16, 12304, 48), (40, 12304, 144), (5, 272, 8208), (5, 272, 16400), (20, 272, 16400), (50, 144, 16400)]
+            (16, 12304, 48), (40, 12304, 144), (32, 1040, 272), (64, 512, 528), (48, 1024, 8208), (33, 96, 16400),
+            (17, 2048, 144), (64, 1040, 8208), (5, 272, 8208), (5, 272, 16400), (20, 272, 16400), (50, 144, 16400)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])

@@ -37,7 +37,8 @@ def test_sizes(L):
         assert L.mx4_codes_bytes(rows, K) == g * ks * 1024
         assert L.mx4_scales_bytes(rows, K) == g * -(-ks // 4) * 256
         need = L.mx4_matmul_workspace_bytes(rows, K, 64)
-        assert need == 0 if rows <= 16 else need >= g * ks * 1024 + g * -(-ks // 4) * 256
+        one_launch = rows <= 16 or (rows <= 64 and rows * -(-ks // 4) <= 96)
+        assert need == 0 if one_launch else need >= g * ks * 1024 + g * -(-ks // 4) * 256
     for rows, K in [(0, 64), (64, 0), (64, 24), (1 << 25, 64), (64, (1 << 20) + 16), (1 << 24, 1 << 20), (-5, 64)]:
         assert L.mx4_codes_bytes(rows, K) == 0 and L.mx4_scales_bytes(rows, K) == 0
     assert L.mx4_matmul_workspace_bytes(64, 64, 24) == 0
@@ -62,7 +63,7 @@ QUANT = dict(X=P, M=8, K=64, ldx=64, dt=0, codes=P, scales=P)
 PREP = dict(W=P, K=64, N=32, layout=0, dt=0, codes=P, scales=P)
 TILE = dict(packed=P, bs=P, K=64, N=32, codes=P, scales=P)
 DEQ = dict(codes=P, scales=P, M=8, K=64, dt=2, out=P, ldo=64)
-MM = dict(X=P, M=24, K=64, ldx=64, dt=1, wc=P, ws=P, N=32, Y=P, work=P, wb=BIG)
+MM = dict(X=P, M=100, K=64, ldx=64, dt=1, wc=P, ws=P, N=32, Y=P, work=P, wb=BIG)
 MMQ = dict(xc=P, xs=P, M=100, K=8192, wc=P, ws=P, N=128, dt=0, Y=P, work=P, wb=BIG)
 WO = dict(X=P, M=8, K=64, ldx=64, dt=0, wc=P, ws=P, N=32, Y=P)
 MOE = dict(X=P, T=4, D=64, ldx=64, dt=0, logits=P, E=8, ldt=2, k=2, renorm=1, fmt=0, w13=P, s13=P, w2=P, s2=P,
@@ -95,6 +96,7 @@ def test_every_pointer_is_checked(L, name):
     ("mx4_dequantize", dict(dt=3), E_SHAPE), ("mx4_dequantize", dict(dt=-1), E_SHAPE),
     ("mx4_quantize", dict(M=1 << 24, K=1 << 20, ldx=1 << 20), E_SHAPE),
     ("mx4_prepare_weight", dict(layout=2), E_SHAPE),
+    ("mx4_matmul", dict(M=64, ldx=1 << 24), E_SHAPE),   # one launch: X behind a buffer resource
     ("mx4_matmul_q", dict(wb=64), E_WS), ("mx4_matmul", dict(M=16, ldx=1 << 26), E_SHAPE), ("mx4_matmul", dict(wb=0), E_WS), ("mx4_matmul", dict(M=4096, wb=4096), E_WS),
     ("mx4_weight_only_matmul", dict(M=17), E_SHAPE), ("mx4_weight_only_matmul", dict(M=16, ldx=1 << 26), E_SHAPE),
     ("moe_layer", dict(T=0), E_SHAPE), ("moe_layer", dict(T=17), E_SHAPE), ("moe_layer", dict(D=56), E_SHAPE),
