@@ -8,20 +8,27 @@
 // of y. It is the weights of the chosen experts that bound it: each is read once.
 //
 // k_moe_gate_up: every workgroup works out the routing for itself (T x E logits, a few KB
-// from L2, one wave per token) rather than wait for a launch of its own. The gate and up rows
-// of all chosen experts, 16 + 16 features at a time, are one list of steps that the
-// workgroups share evenly, whatever the number of experts turns out to be; a workgroup goes
-// over its part with the next step's weights in flight while it multiplies, adds up its
-// waves and writes the hidden values of the tokens that chose the expert.
+// from L2, one wave per token) rather than wait for a launch of its own: 1.4 us for up to 8
+// tokens, 2.8 for 16. The gate and up rows of all chosen experts, 16 + 16 features at a time,
+// are one list of steps that 256 workgroups, one per CU, share evenly, whatever the number of
+// experts turns out to be; a workgroup goes over its part with the next step's weights in
+// flight while it multiplies, adds up its waves and writes the hidden values of the tokens
+// that chose the expert.
 // k_moe_down: a workgroup per 16 output features goes over all chosen experts, its waves
-// sharing the (expert, K quad) items in order, so that the weighted sum over experts needs
-// neither atomics nor a third launch and is the same on every run.
+// sharing the (pass, K quad) items in order (a pass: up to four tokens of one expert), so
+// that the weighted sum over experts needs neither atomics nor a third launch and is the same
+// on every run.
 //
 // The hidden values stay near fp32: they are kept as a bf16 pair, high part and remainder
 // (16 significant bits, the full exponent range, so that no |h| > 65504 turns into an
-// infinity), and the pair costs nothing in the down product: an expert has few tokens, so
-// rows 0-7 of the 16-row operand hold the high parts of eight of them and rows 8-15 the
-// remainders, and their two sums are added in the end.
+// infinity). The pair costs no instructions in the down product: a pass has four tokens, so
+// rows 0-3 of the 16-row operand hold their high parts and rows 8-11 the remainders, and the
+// two sums are added in the end.
+//
+// Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
+// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 162 us, 5.4 TB/s, MX4 97 us, 4.8 TB/s;
+// of 2048 x 768 77 and 51 us; 1 token of these 20.9 and 15.5 us, of which 7.5 and 4.0 us are the
+// bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
 
@@ -182,6 +189,29 @@ __host__ __device__ __forceinline__ bool up_resident(int T, int quads) {
   return quads * act_bytes<MX>(T) <= kUpResident;
 }
 
+constexpr int kMoeBlocks = 256;
+
+// Waves that share the quads of a group: a workgroup's steps each cost a turn per quad of a wave
+// and about as much again for the sums' exchange and the hidden values, so the fewest of
+// steps x (1 + turns). Few sharers exchange little and give each wave loads to have in flight
+// over a step's end; many leave fewer features to the last step. Measured, us per layer at 8 /
+// 4 / 2 sharers: 16 tokens, 8 of 64 experts of 4096 x 1280, MX4 116 / 100 / 97, int8 172 / 162 /
+// 167; of 2048 x 768, int8 87 / 81 / 77, 4 tokens 45 / 42 / 44, 1 token 21.7 / 20.2 / 23.2; 1
+// token of 4096 x 1280, MX4 28 / 28 / 25. (One: 102, 179, 82, 40, 28.8 and 31.)
+__device__ __forceinline__ int up_share(int experts, int groups, int quads) {
+  const int most = quads >= 5 ? 8 : quads >= 3 ? 4 : quads;
+  int best = most, least = 0x7fffffff;
+  for (int share = most; share >= 2 || share == most; share >>= 1) {
+    const int par = kUpWaves / share, steps = experts * ((groups + par - 1) / par);
+    const int cost = (steps + kMoeBlocks - 1) / kMoeBlocks * (1 + (quads + share - 1) / share);
+    if (cost < least) {
+      least = cost;
+      best = share;
+    }
+  }
+  return best;
+}
+
 template <class T, bool MX>
 __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* ids, float* weights) {
   extern __shared__ __attribute__((aligned(16))) char s_x[];  // [quads or waves][act_bytes(T)]
@@ -217,8 +247,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   const MoeOrder order(table, lane);
 
   // A step is `par` neighbouring 16-feature groups of one expert, `share` waves on the quads
-  // of each: with fewer quads than waves the waves take several groups at once.
-  const int share = quads >= 5 ? 8 : quads >= 3 ? 4 : quads, par = kUpWaves / share;
+  // of each.
+  const int share = up_share(order.count(), groups, quads), par = kUpWaves / share;
   const int steps = (groups + par - 1) / par;
   // steps [first, last) of the list are this workgroup's
   const unsigned all = static_cast<unsigned>(order.count() * steps), some = all / gridDim.x, more = all % gridDim.x;
@@ -301,11 +331,18 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   }
 }
 
-// WAVES waves; a pass over an expert's quads serves TOK of its tokens (2 TOK rows: high parts
-// and remainders).
-template <class T, bool MX, int WAVES, int TOK>
-__global__ __launch_bounds__(64 * WAVES) void k_moe_down(MoeArgs a, const int* ids, const float* weights) {
-  constexpr int ROWS = 2 * TOK;
+// A pass over an expert's quads serves TOK of its tokens (2 TOK rows: high parts and
+// remainders); further ones read its weights again, from a cache. Eight tokens per pass leave
+// LDS for 8 waves instead of 16: 132 for 114 us (16 tokens, 8 of 64 experts of 2048 x 1280,
+// int8), 112.6 for 111.2 (8 of 32 of 4096 x 1280), 51.8 for 51.0 (4 of 8), 24.3 for 21.9 (one
+// expert), and at best 39.9 for 41.5 (8 tokens, 4 of 8). A load of the next item's h ahead of the
+// products, as the weights', leaves 8 waves too for MX4 (111 for 97 us, 16 tokens of 4096 x
+// 1280) and gave nothing where 16 fit (int8).
+constexpr int kDownWaves = 16, kDownTokens = 4;
+
+template <class T, bool MX>
+__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const int* ids, const float* weights) {
+  constexpr int WAVES = kDownWaves, TOK = kDownTokens, ROWS = 2 * TOK;
   __shared__ __attribute__((aligned(16))) char s_x[WAVES * ROWS * kActStride];
   __shared__ unsigned s_tokens[kMoeMaxExperts];
   __shared__ uint8_t s_place[kMoeMaxExperts * kMoeMaxTokens], s_pass[kMoeMaxLists];
@@ -448,14 +485,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_down(MoeArgs a, const int* i
   }
 }
 
-constexpr int kMoeBlocks = 256;
-
-template <class T, bool MX, int WAVES, int TOK>
-static hipError_t run_down(const MoeArgs& a, const int* ids, const float* weights, hipStream_t s) {
-  hipLaunchKernelGGL((k_moe_down<T, MX, WAVES, TOK>), dim3(a.D / 16), dim3(64 * WAVES), 0, s, a, ids, weights);
-  return hipGetLastError();
-}
-
 template <class T, bool MX>
 static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
   const int n_slots = a.E < a.T * a.k ? a.E : a.T * a.k;
@@ -470,7 +499,8 @@ static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s)
   hipLaunchKernelGGL((k_moe_gate_up<T, MX>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, ids, weights);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return a.T * a.k > 3 * a.E ? run_down<T, MX, 8, 8>(a, ids, weights, s) : run_down<T, MX, 16, 4>(a, ids, weights, s);
+  hipLaunchKernelGGL((k_moe_down<T, MX>), dim3(a.D / 16), dim3(64 * kDownWaves), 0, s, a, ids, weights);
+  return hipGetLastError();
 }
 
 // Workspace: the lists' ids and weights, then the hidden values.

@@ -73,6 +73,19 @@ def test_layer(T, D, I, E, k, renorm, dtype, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "mx4"])
+@pytest.mark.parametrize("T,k", [(1, 4), (1, 8), (16, 8)])
+def test_eight_four_and_two_waves_on_a_rows_quads(T, k, fmt):
+    """33 groups of features of 4, 8 or all 24 experts, five quads a row: the first launch's
+    list of steps fits its workgroups once with 8, 4 and 2 waves on a row."""
+    D, I, E = 1040 if fmt == "int8" else 2064, 528, 24
+    announce(f"moe T={T} D={D} I={I} E={E} k={k} {fmt}")
+    X, logits, pairs, values = case(T, D, I, E, F16, fmt, 10 * T + k)
+    if T > 1:
+        logits[torch.arange(E) % T, torch.arange(E)] += 20  # every expert has a token
+    check(X, logits, pairs, values, k, True)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mx4"])
 def test_masks_ties_and_padding_tokens(fmt):
     X, logits, pairs, values = case(6, 272, 80, 12, F16, fmt, 1)
     inf = float("inf")
