@@ -32,8 +32,10 @@ __device__ __forceinline__ void few_quantize(const v4u& x, char* to, int lane) {
   if ((lane & 3) == 0) to[256 + (lane & 12) + (lane >> 4)] = static_cast<char>(b);
 }
 
-template <class T, int G, int RG, FewX FROM>
-__global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const void* X, int64_t ldx) {
+// ROWS (kOwn): the most rows; up to 4 leave registers for 6 waves per SIMD, three workgroups
+// per CU, which wait for their loads beside each other.
+template <class T, int G, int RG, FewX FROM, int ROWS>
+__global__ __launch_bounds__(64 * kFewWaves, FROM == FewX::kOwn && ROWS <= 4 ? 6 : 2) void k_mx_few(MxGemmArgs a, const void* X, int64_t ldx) {
   static_assert(FROM != FewX::kOwn || G == 1, "a wave quantizes one row group");
   // rows of kFewStride, then the waves' sums in their place: few_lds()
   extern __shared__ __attribute__((aligned(16))) char s_x[];
@@ -96,20 +98,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const v
   }
   v4f acc[G][RG] = {};
   for (int q = wave; q < quads; q += kFewWaves) {
-    v4u raw[FROM == FewX::kOwn ? 16 : 1];
+    v4u raw[FROM == FewX::kOwn ? ROWS : 1];
     if constexpr (FROM == FewX::kOwn) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < ROWS; ++i)
         if (i < a.M) raw[i] = load_row(i, q);
     }
     if (FROM != FewX::kShared || q != wave) load(q);
     if constexpr (FROM != FewX::kTiled) {
-      const char* rows = s_x + (FROM == FewX::kOwn ? wave * 16 : q * a.M) * kFewStride;
+      const char* rows = s_x + (FROM == FewX::kOwn ? wave * ROWS : q * a.M) * kFewStride;
       if constexpr (FROM == FewX::kOwn) {
         wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < a.M) few_quantize<T>(raw[i], s_x + (wave * 16 + i) * kFewStride, lane);
+        for (int i = 0; i < ROWS; ++i)
+          if (i < a.M) few_quantize<T>(raw[i], s_x + (wave * ROWS + i) * kFewStride, lane);
         wave_lds_fence();
       }
 #pragma unroll
@@ -149,33 +151,34 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxGemmArgs a, const v
   }
 }
 
-static size_t few_lds(int64_t M, int64_t K, int G, int RG, FewX from) {
-  const size_t rows = from == FewX::kTiled ? 0 : from == FewX::kOwn ? kFewWaves * 16 : mx_quads(K) * M;
+static size_t few_lds(int64_t M, int64_t K, int G, int RG, FewX from, int most) {
+  const size_t rows = from == FewX::kTiled ? 0 : from == FewX::kOwn ? kFewWaves * most : mx_quads(K) * M;
   const size_t sums = sizeof(float) * kFewWaves * 16 * G * (16 * RG + 1);
   return rows * kFewStride > sums ? rows * kFewStride : sums;
 }
 
-template <int G, int RG, FewX FROM>
+template <int G, int RG, FewX FROM, int ROWS = 16 * G>
 static hipError_t run(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
   const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kFewWaves);
-  const size_t lds = few_lds(a.M, a.K, G, RG, FROM);
+  const size_t lds = few_lds(a.M, a.K, G, RG, FROM, ROWS);
   if (lds > kMaxLds) return hipErrorInvalidConfiguration;
-  if (type == kMxF16) hipLaunchKernelGGL((k_mx_few<F16, G, RG, FROM>), grid, block, lds, s, a, X, ldx);
-  else hipLaunchKernelGGL((k_mx_few<B16, G, RG, FROM>), grid, block, lds, s, a, X, ldx);
+  if (type == kMxF16) hipLaunchKernelGGL((k_mx_few<F16, G, RG, FROM, ROWS>), grid, block, lds, s, a, X, ldx);
+  else hipLaunchKernelGGL((k_mx_few<B16, G, RG, FROM, ROWS>), grid, block, lds, s, a, X, ldx);
   return hipGetLastError();
 }
 
-// Row groups per workgroup: about one workgroup per CU, up to 4. Measured per call (HIP
-// graphs over rotated weights, fp16, M = 8, RG = 1 / 2 / 4): 8192 x 1024 (K x N) 5.6 / 6.5 /
-// 9.7 us, 4096 x 4096 4.9 / 5.2 / 6.3, 8192 x 8192 10.9 / 9.2 / 11.2, 4096 x 16384 11.1 /
-// 10.2 / 8.9.
-static int few_row_groups(int N) { return N < 16 * 512 ? 1 : N < 16 * 1024 ? 2 : 4; }
-
+// Row groups per workgroup where one workgroup fills a CU, by its registers or by the work on X
+// that each repeats: as many as make one round of workgroups, up to 4. Measured per call (HIP
+// graphs over rotated weights, fp16, K x N, RG = 1 / 2 / 4): M = 16, X quantized on the way, 4096 x
+// 4096 6.3 / 6.2 / 7.7 us, 4096 x 6144 8.5 / 6.8 / 7.9, 8192 x 8192 14.8 / 11.5 / 13.2, 4096 x
+// 10240 11.6 / 11.3 / 8.6, 12288 x 12288 28.9 / 25.5 / 20.1; M = 64, X tiled, 4096 x 4096 6.2 /
+// 7.6 / 8.9, 8192 x 8192 15.2 / 13.6 / 14.7, 4096 x 10240 11.9 / 11.7 / 9.8, 12288 x 12288 30.7 /
+// 27.5 / 21.7.
 template <int G, FewX FROM>
 static hipError_t pick(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
-  const int rg = few_row_groups(a.N);
-  if (rg == 1) return run<G, 1, FROM>(a, X, ldx, type, s);
-  return rg == 2 ? run<G, 2, FROM>(a, X, ldx, type, s) : run<G, 4, FROM>(a, X, ldx, type, s);
+  const int groups = a.N / 16;
+  if (groups <= 256) return run<G, 1, FROM>(a, X, ldx, type, s);
+  return groups <= 512 ? run<G, 2, FROM>(a, X, ldx, type, s) : run<G, 4, FROM>(a, X, ldx, type, s);
 }
 
 // One launch instead of a quantization and a product. Up to 16 rows always; more while the
@@ -187,10 +190,13 @@ bool mx_few_inline(int64_t M, int64_t K) { return M <= 16 || (M <= 64 && M * mx_
 
 // Up to 16 rows, by the workgroup together while K has at most two quads, so that six of its
 // eight waves do not watch (16 rows of 1024 x 1024 3.5 against 3.9 us, of 2048 x 1024 4.7 against
-// 4.4).
+// 4.4). Up to 4 rows, one group per workgroup and three workgroups per CU, in place of the
+// choice above: 4096 x 4096 4.2 against 4.3 us, 4096 x 10240 6.7 / 7.1, 12288 x 12288 16.6 /
+// 16.3 (two rows 14.6 / 16.1), 2048 x 32768 9.0 / 10.8, 8192 x 28672 23.3 / 24.8.
 hipError_t launch_mx_few_inline(const MxGemmArgs& a, const void* X, int64_t ldx, int type, hipStream_t s) {
-  if (a.M <= 16)
-    return mx_quads(a.K) <= 2 ? pick<1, FewX::kShared>(a, X, ldx, type, s) : pick<1, FewX::kOwn>(a, X, ldx, type, s);
+  if (a.M <= 16 && mx_quads(a.K) <= 2) return pick<1, FewX::kShared>(a, X, ldx, type, s);
+  if (a.M <= 4) return run<1, 1, FewX::kOwn, 4>(a, X, ldx, type, s);
+  if (a.M <= 16) return pick<1, FewX::kOwn>(a, X, ldx, type, s);
   return a.M <= 32 ? pick<2, FewX::kShared>(a, X, ldx, type, s) : pick<4, FewX::kShared>(a, X, ldx, type, s);
 }
 
@@ -198,9 +204,16 @@ hipError_t launch_mx_few_inline(const MxGemmArgs& a, const void* X, int64_t ldx,
 // 16384 12.7 against 11.2, 8192 x 8192 20.0 against 11.9).
 bool mx_few(int64_t M) { return M <= 64; }
 
+// X already tiled takes few registers, so that several workgroups share a CU and one group each
+// is best, or near it, until their reading X again shows. RG = 1 / 2 / 4, us: M = 16, 4096 x 4096
+// 4.1 / 4.8 / 7.4, 8192 x 8192 9.2 / 8.7 / 13.2, 12288 x 12288 16.9 / 17.9 / 20.6, 8192 x 28672
+// 25.7 / 24.5 / 22.9; M = 32, 4096 x 4096 4.6 / 6.1 / 7.8, 8192 x 8192 10.9 / 11.4 / 13.3, 4096 x
+// 16384 10.6 / 10.8 / 11.1, 2048 x 32768 11.2 / 10.4 / 10.7, 8192 x 28672 32.8 / 28.8 / 25.0.
 hipError_t launch_mx_few(const MxGemmArgs& a, int type, hipStream_t s) {
-  if (a.M <= 16) return pick<1, FewX::kTiled>(a, nullptr, 0, type, s);
-  return a.M <= 32 ? pick<2, FewX::kTiled>(a, nullptr, 0, type, s) : pick<4, FewX::kTiled>(a, nullptr, 0, type, s);
+  if (a.M <= 16) return run<1, 1, FewX::kTiled>(a, nullptr, 0, type, s);
+  if (a.M <= 32)
+    return a.N < 16 * 1024 ? run<2, 1, FewX::kTiled>(a, nullptr, 0, type, s) : run<2, 4, FewX::kTiled>(a, nullptr, 0, type, s);
+  return pick<4, FewX::kTiled>(a, nullptr, 0, type, s);
 }
 
 }  // namespace i8mm

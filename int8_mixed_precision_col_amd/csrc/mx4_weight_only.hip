@@ -2,7 +2,9 @@
 // fp32 accumulation, one rounding.
 //
 // One workgroup per 16 RG output features; its waves share the quads of K and their partial
-// sums meet in LDS (weight_stream.hpp has the arithmetic of a quad).
+// sums meet in LDS (weight_stream.hpp has the arithmetic of a quad). Bound by the weight's bytes
+// and, for small ones, by launch and first loads: 1 x 12288 x 12288 15.1 us (5.3 TB/s, K x N), 1 x
+// 8192 x 8192 8.4 us (4.2 TB/s), 1 x 4096 x 4096 4.2 us.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
 
@@ -10,8 +12,14 @@ namespace i8mm {
 
 constexpr int kMxWoWaves = 8;
 
-template <class T, int RG>
-__global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnlyArgs a) {
+// Waves per SIMD that the registers have to leave room for, 2 of each workgroup: what keeps
+// HBM busy is workgroups beside each other on a CU, each waiting for its own loads, and it is
+// the rows of X on their way to LDS that take the registers.
+constexpr int wo_waves(int rows) { return rows <= 2 ? 6 : rows <= 8 ? 4 : 2; }
+
+// For at most ROWS tokens.
+template <class T, int RG, int ROWS>
+__global__ __launch_bounds__(64 * kMxWoWaves, wo_waves(ROWS)) void k_mx_weight_only(MxWeightOnlyArgs a) {
   // [waves][act_bytes(M)], and once the products are done the waves' sums: both at a time do
   // not fit for 16 tokens and four row groups
   extern __shared__ __attribute__((aligned(16))) char s_x[];
@@ -30,7 +38,7 @@ __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnly
   constexpr bool AHEAD = RG == 1;
   v4f acc[RG] = {};
   WeightQuad<true> w[RG], next[AHEAD ? RG : 1];
-  ActQuad<true, 16> x;
+  ActQuad<true, ROWS> x;
   auto load_x = [&](int q) {
     x.load(xr, q, a.K, M, lane, [&](int i) { return static_cast<unsigned>(i * a.ldx) * 2u; });
   };
@@ -76,24 +84,34 @@ __global__ __launch_bounds__(64 * kMxWoWaves) void k_mx_weight_only(MxWeightOnly
   }
 }
 
-template <int RG>
+template <int RG, int ROWS>
 static hipError_t run_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
   const dim3 grid((a.N / 16 + RG - 1) / RG), block(64 * kMxWoWaves);
   const size_t rows = static_cast<size_t>(kMxWoWaves) * act_bytes<true>(a.M);
   const size_t sums = sizeof(float) * kMxWoWaves * 16 * (16 * RG + 1);
   const size_t lds = rows > sums ? rows : sums;
   if (lds > kMaxLds) return hipErrorInvalidConfiguration;
-  if (type == kMxF16) hipLaunchKernelGGL((k_mx_weight_only<F16, RG>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((k_mx_weight_only<B16, RG>), grid, block, lds, s, a);
+  if (type == kMxF16) hipLaunchKernelGGL((k_mx_weight_only<F16, RG, ROWS>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_mx_weight_only<B16, RG, ROWS>), grid, block, lds, s, a);
   return hipGetLastError();
 }
 
+// Row groups per workgroup, by what was measured (us per call, fp16, RG = 1 / 2 / 4, K x N).
 hipError_t launch_mx_weight_only(const MxWeightOnlyArgs& a, int type, hipStream_t s) {
-  // row groups per workgroup: about one workgroup per CU, up to 4 (per call, M = 8, RG = 1 / 2 /
-  // 4: 4096 x 4096 (K x N) 4.7 / 5.3 / 7.3 us, 8192 x 8192 12.1 / 9.3 / 11.7, 4096 x 16384
-  // 14.0 / 10.9 / 9.8)
-  if (a.N < 16 * 512) return run_weight_only<1>(a, type, s);
-  return a.N < 16 * 1024 ? run_weight_only<2>(a, type, s) : run_weight_only<4>(a, type, s);
+  const int groups = a.N / 16;
+  // Up to 2 rows three workgroups fit a CU, and one group each is best or near it at any N: M =
+  // 2, 4096 x 4096 4.3 / 4.9 / 6.5, 8192 x 8192 8.5 / 8.5 / 10.7, 12288 x 12288 15.1 / 17.4 / 17.0,
+  // 2048 x 32768 9.7 / 9.5 / 11.4, 512 x 16384 4.7 / 4.0 / 5.0.
+  if (a.M <= 2) return run_weight_only<1, 2>(a, type, s);
+  // Up to 8 two do (with 4 groups one): M = 4, 4096 x 4096 4.4 / 5.1 / 7.1, 4096 x 6144 5.4 / 5.5 /
+  // 7.4, 8192 x 8192 9.3 / 8.7 / 11.2, 4096 x 10240 7.1 / 7.7 / 7.9, 2048 x 32768 12.2 / 10.1 / 12.7;
+  // M = 8, 4096 x 4096 4.8 / 5.4 / 7.3, 4096 x 6144 6.1 / 5.8 / 7.6, 4096 x 10240 7.9 / 8.4 / 8.2.
+  if (a.M <= 8) return groups <= 256 ? run_weight_only<1, 8>(a, type, s) : run_weight_only<2, 8>(a, type, s);
+  // Beyond that one per CU: as many groups as make one round of workgroups. M = 16, 4096 x 4096
+  // 5.3 / 6.1 / 7.9, 4096 x 5120 8.0 / 6.3 / 8.1, 8192 x 8192 14.5 / 10.6 / 12.8, 8192 x 10240 19.9 /
+  // 17.2 / 13.6, 4096 x 16384 15.5 / 12.5 / 10.5.
+  if (groups <= 256) return run_weight_only<1, 16>(a, type, s);
+  return groups <= 512 ? run_weight_only<2, 16>(a, type, s) : run_weight_only<4, 16>(a, type, s);
 }
 
 }  // namespace i8mm

@@ -175,7 +175,8 @@ PRODUCTS = [(1, 16, 16), (1, 4096, 256), (3, 1040, 48), (16, 128, 16), (16, 1024
             (2048, 272, 10000), (512, 144, 16384),
             # few rows: long K, and two and four groups of features per workgroup
             (16, 12304, 48), (40, 12304, 144), (32, 1040, 272), (64, 512, 528), (48, 1024, 8208), (33, 96, 16400),
-            (17, 2048, 144), (64, 1040, 8208), (5, 272, 8208), (5, 272, 16400), (20, 272, 16400), (50, 144, 16400)]
+            (17, 2048, 144), (64, 1040, 8208), (5, 272, 8208), (5, 272, 16400), (20, 272, 16400), (50, 144, 16400),
+            (4, 1552, 4112), (12, 2064, 4112), (9, 1552, 8208), (30, 2064, 4112), (20, 2064, 16400)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
@@ -219,7 +220,8 @@ def test_matmul_strided_rows(M, dtype):
 
 
 WEIGHT_ONLY = [(1, 16, 16), (1, 4096, 512), (2, 144, 272), (5, 528, 48), (8, 1040, 4112), (13, 8192, 272), (16, 4112, 16),
-               (16, 2048, 1040), (9, 512, 8208), (3, 528, 16400), (16, 12304, 48), (16, 528, 16400)]
+               (16, 2048, 1040), (9, 512, 8208), (3, 528, 16400), (16, 12304, 48), (16, 528, 16400),
+               (2, 8208, 4112), (12, 1040, 4112), (4, 2064, 5136)]
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
