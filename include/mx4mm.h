@@ -67,7 +67,9 @@ int mx4_tile_weight(const uint8_t* packed, const uint8_t* block_scales, int64_t 
 
 /*
  * The values of tiled codes and scales: out [M, K], row stride ldo, any mx4_dtype. Exact in
- * MX4_F32 and MX4_BF16; in MX4_F16 rounded once where the value is outside fp16's range.
+ * MX4_F32 and MX4_BF16, but values of 2^128 and more, which only a weight from mx4_tile_weight
+ * can hold (bytes 253 and 254), become infinities, there and where a product takes the
+ * weight's values as bf16; in MX4_F16 rounded once where the value is outside fp16's range.
  */
 int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, int dtype,
                    void* out, int64_t ldo, hipStream_t stream);
@@ -118,7 +120,8 @@ int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int
  *   Y[t] = sum over the chosen e of p_e Down_e (silu(Gate_e X[t]) * (Up_e X[t])).
  * An expert whose logit is -inf is off for the token; where fewer than top_k are on, the
  * rest of the list is empty, and a token with none (a padding row) gets zeros and costs no
- * weight traffic. A NaN counts as the largest logit and makes the token's output NaN.
+ * weight traffic. A NaN counts as the largest logit and makes the token's output NaN, and so
+ * does a logit of +inf.
  *   X             [T, D], row stride ldx (a multiple of 8, >= D, T ldx < 2^30), dtype
  *                 MX4_F16 or MX4_BF16.
  *   logits        [T, E] contiguous, logits_dtype any mx4_dtype; 1 <= E <= 512,

@@ -70,7 +70,7 @@ struct WeightQuad {
 // half a wave per row; an MX4 quad has two such pieces), then put through the wave's own LDS
 // buffer into operand order. Loading the operand straight from memory takes XV 16-byte
 // gathers per unit whatever the number of rows, and those, not the weight, then set the time
-// (MX4, 1 x 4096 x 4096: 6.1 us per call; 4.6 so); this takes one load per two rows and piece.
+// (MX4, 1 x 4096 x 4096: 6.1 us per call; 4.2 so); this takes one load per two rows and piece.
 constexpr int kActPiece = 256;                       // elements
 constexpr int kActStride = kActPiece * 2 + 16;       // bytes between rows in LDS: a 16-byte
                                                      // skew, so the 16 rows hit distinct banks

@@ -196,6 +196,8 @@ def tile_weight(packed: torch.Tensor, block_scales: torch.Tensor, K: int | None 
 def untile(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int):
     """Packed codes [M, 16 ceil(K / 32)] and scale bytes [M, ceil(K / 32)] held in a tiled pair
     (a copy; layout only)."""
+    if codes.dim() != 4 or not 0 <= M <= 16 * codes.shape[0] or not 0 <= K <= 128 * codes.shape[1]:
+        raise ValueError(f"codes of shape {tuple(codes.shape)} do not hold {M} rows of {K} elements")
     g, ks, nb = codes.shape[0], codes.shape[1], (K + 31) // 32
     packed = codes.permute(0, 2, 1, 3).reshape(g * 16, ks * 64)[:M, :16 * nb].contiguous()
     # scales [group, quad, (block of the unit, row), unit]

@@ -131,6 +131,14 @@ def test_weight_conversion_refused(fake):
     assert fake.calls[-1][1][2:4] == (48, 32)
 
 
+def test_untile_refused():
+    codes, scales = torch.zeros(2, 1, 16, 64, dtype=torch.uint8), torch.zeros(2, 1, 64, 4, dtype=torch.uint8)
+    assert mx4.untile(codes, scales, 32, 128)[0].shape == (32, 64)
+    for args in ((codes, scales, 33, 128), (codes, scales, 32, 144), (codes, scales, -1, 128), (codes[0], scales, 16, 128)):
+        with pytest.raises(ValueError):
+            mx4.untile(*args)
+
+
 def test_moe_refused(fake):
     X, lg, gu, dn = f16(3, 64), torch.zeros(3, 4), pair(4 * 2 * 32, 64), pair(4 * 64, 32)
     bad = [
