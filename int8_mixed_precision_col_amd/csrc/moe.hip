@@ -26,8 +26,8 @@
 // two sums are added in the end.
 //
 // Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
-// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 162 us, 5.4 TB/s, MX4 97 us, 4.8 TB/s;
-// of 2048 x 768 77 and 51 us; 1 token of these 20.9 and 15.5 us, of which 7.5 and 4.0 us are the
+// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 165 us, 5.5 TB/s, MX4 94.5 us, 5.0 TB/s;
+// of 2048 x 768 75 and 48 us; 1 token of these 19.3 and 14.9 us, of which 7.5 and 4.0 us are the
 // bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
@@ -189,7 +189,10 @@ __host__ __device__ __forceinline__ bool up_resident(int T, int quads) {
   return quads * act_bytes<MX>(T) <= kUpResident;
 }
 
-constexpr int kMoeBlocks = 256;
+// Workgroups of k_moe_gate_up: one per CU. Two where they fit (int8 takes 124 registers) and a step is long, D of 15 quads (3.6 K) and more: 1 / 2 / 4 tokens, 8 of 64 experts of
+// 4096 x 1280, 36.7 -> 36.4, 53 -> 49 and 85 -> 81 us; but of 2048 x 768 19.3 -> 20.4, 26.5 -> 26.8 and
+// 41.2 -> 41.7, and 4 of 60 of 3328 x 1280 23.4 -> 23.4, 30.8 -> 31.8 and 47.0 -> 48.6.
+constexpr int kMoeBlocks = 256, kUpLongQuads = 15;
 
 // Waves that share the quads of a group: a workgroup's steps each cost a turn per quad of a wave
 // and about as much again for the sums' exchange and the hidden values, so the fewest of
@@ -198,12 +201,12 @@ constexpr int kMoeBlocks = 256;
 // 4 / 2 sharers: 16 tokens, 8 of 64 experts of 4096 x 1280, MX4 116 / 100 / 97, int8 172 / 162 /
 // 167; of 2048 x 768, int8 87 / 81 / 77, 4 tokens 45 / 42 / 44, 1 token 21.7 / 20.2 / 23.2; 1
 // token of 4096 x 1280, MX4 28 / 28 / 25. (One: 102, 179, 82, 40, 28.8 and 31.)
-__device__ __forceinline__ int up_share(int experts, int groups, int quads) {
+__device__ __forceinline__ int up_share(int experts, int groups, int quads, int blocks) {
   const int most = quads >= 5 ? 8 : quads >= 3 ? 4 : quads;
   int best = most, least = 0x7fffffff;
   for (int share = most; share >= 2 || share == most; share >>= 1) {
     const int par = kUpWaves / share, steps = experts * ((groups + par - 1) / par);
-    const int cost = (steps + kMoeBlocks - 1) / kMoeBlocks * (1 + (quads + share - 1) / share);
+    const int cost = (steps + blocks - 1) / blocks * (1 + (quads + share - 1) / share);
     if (cost < least) {
       least = cost;
       best = share;
@@ -212,7 +215,11 @@ __device__ __forceinline__ int up_share(int experts, int groups, int quads) {
   return best;
 }
 
-template <class T, bool MX>
+// V experts per lane and NT tokens per wave in the routing; RES: all of X in LDS. Kernels of their
+// own rather than branches of one: a launch runs a few KB of code, once, and finds it faster in
+// 8 KB than in 37 (1 token, 8 of 64 experts of 2048 x 768, int8 20.9 -> 19.2 us; 8 tokens of 4096 x
+// 1280, MX4, 79 -> 73 us).
+template <class T, bool MX, int V, int NT, bool RES>
 __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* ids, float* weights) {
   extern __shared__ __attribute__((aligned(16))) char s_x[];  // [quads or waves][act_bytes(T)]
   __shared__ MoeTable table;
@@ -220,35 +227,26 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr int UK = WeightFmt<MX>::UK;
   const int ks = (a.D + UK - 1) / UK, quads = (ks + 3) >> 2, groups = a.I / 16;
-  const bool resident = up_resident<MX>(a.T, quads);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.T - 1) * a.ldx + a.D) * 2));
   // the logits first, then X: both are on their way while the table is cleared and the wave
   // routes its tokens
   static_assert(2 * kUpWaves >= kMoeMaxTokens, "two tokens per wave");
   auto row_of = [&](int t) { return static_cast<unsigned>(t * a.ldx) * 2u; };
-  ActQuad<MX, 16> x;
-  auto route = [&](auto router) {
-    if (resident && wave < quads) x.load(xr, wave, a.D, a.T, lane, row_of);
-    table.clear(tid, 64 * kUpWaves);
-    lds_barrier();
-    // One workgroup writes what the second launch goes by, all of it from its own view of the
-    // logits, so that it is consistent whatever else happens to them meanwhile.
-    router.route(a, lane, table, blockIdx.x == 0 ? ids : nullptr, weights);
-  };
-  constexpr int V = kMoeMaxExperts / 64;
-  if (a.T > kUpWaves) {
-    if (a.E <= 64) route(MoeRouter<1, 2>(a, wave, kUpWaves, lane));
-    else route(MoeRouter<V, 2>(a, wave, kUpWaves, lane));
-  } else {
-    if (a.E <= 64) route(MoeRouter<1, 1>(a, wave, kUpWaves, lane));
-    else route(MoeRouter<V, 1>(a, wave, kUpWaves, lane));
-  }
+  ActQuad<MX, 8 * NT> x;
+  MoeRouter<V, NT> router(a, wave, kUpWaves, lane);
+  if (RES && wave < quads) x.load(xr, wave, a.D, a.T, lane, row_of);
+  table.clear(tid, 64 * kUpWaves);
+  lds_barrier();
+  // One workgroup writes what the second launch goes by, all of it from its own view of the
+  // logits, so that it is consistent whatever else happens to them meanwhile.
+  router.route(a, lane, table, blockIdx.x == 0 ? ids : nullptr, weights);
   lds_barrier();
   const MoeOrder order(table, lane);
 
   // A step is `par` neighbouring 16-feature groups of one expert, `share` waves on the quads
   // of each.
-  const int share = up_share(order.count(), groups, quads), par = kUpWaves / share;
+  const int share = up_share(order.count(), groups, quads, gridDim.x > kMoeBlocks ? 2 * kMoeBlocks : kMoeBlocks);
+  const int par = kUpWaves / share;
   const int steps = (groups + par - 1) / par;
   // steps [first, last) of the list are this workgroup's
   const unsigned all = static_cast<unsigned>(order.count() * steps), some = all / gridDim.x, more = all % gridDim.x;
@@ -269,7 +267,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   // these loads and does not wait for them
   int expert = order.expert(slot);
   prefetch(expert, in, min(kk, quads - 1));
-  if (resident) {
+  if constexpr (RES) {
     if (wave < quads) x.store(s_x + wave * act_bytes<MX>(a.T), a.T, a.T, lane);
     for (int q = wave + kUpWaves; q < quads; q += kUpWaves) {
       x.load(xr, q, a.D, a.T, lane, row_of);
@@ -284,8 +282,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
     const int next_expert = next_in == 0 && step + 1 < n_steps ? order.expert(slot + 1) : expert;
     v4f acc[2] = {};
     for (int q = kk; q < quads; q += share) {
-      const char* buf = s_x + (resident ? q : wave) * act_bytes<MX>(a.T);
-      if (!resident) {
+      const char* buf = s_x + (RES ? q : wave) * act_bytes<MX>(a.T);
+      if constexpr (!RES) {
         x.load(xr, q, a.D, a.T, lane, [&](int t) { return (tokens >> t) & 1u ? row_of(t) : kOOB; });
         wave_lds_fence();
         x.store(s_x + wave * act_bytes<MX>(a.T), a.T, a.T, lane);
@@ -485,19 +483,30 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const i
   }
 }
 
-template <class T, bool MX>
-static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
+template <class T, bool MX, int V, int NT, bool RES>
+static hipError_t run_up(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
   const int n_slots = a.E < a.T * a.k ? a.E : a.T * a.k;
   constexpr int UK = WeightFmt<MX>::UK;
   const int quads = ((a.D + UK - 1) / UK + 3) / 4;
-  const size_t lds = static_cast<size_t>(up_resident<MX>(a.T, quads) ? quads : kUpWaves) * act_bytes<MX>(a.T);
+  const size_t lds = static_cast<size_t>(RES ? quads : kUpWaves) * act_bytes<MX>(a.T);
   constexpr size_t kStatic = sizeof(MoeTable) + sizeof(float) * kUpWaves * 2 * 16 * 17;
   static_assert(kUpResident + kStatic <= kMaxLds && kUpWaves * act_bytes<MX>(kMoeMaxTokens) + kStatic <= kMaxLds,
                 "k_moe_gate_up's LDS");
-  const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16);
-  const unsigned blocks = static_cast<unsigned>(steps < kMoeBlocks ? steps : kMoeBlocks);
-  hipLaunchKernelGGL((k_moe_gate_up<T, MX>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, ids, weights);
-  const hipError_t e = hipGetLastError();
+  const bool two = !MX && quads >= kUpLongQuads && 2 * (lds + kStatic) <= kMaxLds;
+  const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16), most = two ? 2 * kMoeBlocks : kMoeBlocks;
+  const unsigned blocks = static_cast<unsigned>(steps < most ? steps : most);
+  hipLaunchKernelGGL((k_moe_gate_up<T, MX, V, NT, RES>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, ids, weights);
+  return hipGetLastError();
+}
+
+template <class T, bool MX>
+static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
+  constexpr int UK = WeightFmt<MX>::UK, V = kMoeMaxExperts / 64;
+  const bool few = a.T <= kUpWaves, small = a.E <= 64;
+  hipError_t e;
+  if (!up_resident<MX>(a.T, ((a.D + UK - 1) / UK + 3) / 4)) e = run_up<T, MX, V, 2, false>(a, ids, weights, s);
+  else if (few) e = small ? run_up<T, MX, 1, 1, true>(a, ids, weights, s) : run_up<T, MX, V, 1, true>(a, ids, weights, s);
+  else e = small ? run_up<T, MX, 1, 2, true>(a, ids, weights, s) : run_up<T, MX, V, 2, true>(a, ids, weights, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_moe_down<T, MX>), dim3(a.D / 16), dim3(64 * kDownWaves), 0, s, a, ids, weights);
   return hipGetLastError();

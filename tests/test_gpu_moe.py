@@ -85,6 +85,23 @@ def test_eight_four_and_two_waves_on_a_rows_quads(T, k, fmt):
     check(X, logits, pairs, values, k, True)
 
 
+@pytest.mark.parametrize("T,E,I", [(3, 4, 2064), (1, 2, 2064), (2, 2, 2048)])
+def test_two_workgroups_per_cu(T, E, I):
+    """Long int8 rows of few tokens: more steps than 512 workgroups take once, than 256, and as
+    many as 256."""
+    announce(f"moe T={T} D=3600 I={I} E={E}")
+    X, logits, pairs, values = case(T, 3600, I, E, B16, "int8", T + E)
+    check(X, logits, pairs, values, 2, False)
+
+
+@pytest.mark.parametrize("T", [7, 8, 9])
+def test_many_experts_and_the_edge_of_one_token_per_wave(T):
+    for E in (64, 65, 130):
+        announce(f"moe T={T} D=272 I=80 E={E}")
+        X, logits, pairs, values = case(T, 272, 80, E, F16, "mx4", T + E)
+        check(X, logits, pairs, values, 5, True)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "mx4"])
 def test_masks_ties_and_padding_tokens(fmt):
     X, logits, pairs, values = case(6, 272, 80, 12, F16, fmt, 1)
