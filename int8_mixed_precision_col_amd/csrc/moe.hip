@@ -27,7 +27,7 @@
 //
 // Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
 // time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 165 us, 5.5 TB/s, MX4 94.5 us, 5.0 TB/s;
-// of 2048 x 768 75 and 48 us; 1 token of these 19.3 and 14.9 us, of which 7.5 and 4.0 us are the
+// of 2048 x 768 75 and 48 us; 1 token of these 18.6 and 15.0 us, of which 7.5 and 4.0 us are the
 // bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
@@ -394,7 +394,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const i
   constexpr int UK = WeightFmt<MX>::UK;
   const int ks = (a.I + UK - 1) / UK, quads = (ks + 3) >> 2;
   const int items = passes * quads, per = (items + WAVES - 1) / WAVES;
-  const int begin = min(items, per * wave), end = min(items, begin + per);
+  int begin = min(items, per * wave), end = min(items, begin + per);
+  // With waves for every pass no wave's share crosses into a second pass, whose rows it would
+  // have to wait for again; neighbouring waves, on different SIMDs, take different passes (1
+  // token, 8 of 64 experts of 2048 x 768, int8 19.4 -> 18.6 us, of 4096 x 1280 36.4 -> 35.6; with
+  // neighbours on the same pass, so on two SIMDs, 4 of 32 of 1024 x 512 11.9 -> 13.3).
+  if (passes > 0 && passes <= WAVES) {
+    const int share = WAVES / passes, n = (quads + share - 1) / share, s = wave / passes, p = wave - s * passes;
+    if (n <= per) {
+      begin = p * quads + min(quads, s * n);
+      end = p * quads + min(quads, (s + 1) * n);
+      if (s >= share) begin = end = 0;
+    }
+  }
   const unsigned plane = static_cast<unsigned>(n_lists) * a.I * 2u;  // bytes
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, plane * 2u);
   const int r = lane & 15, g = lane >> 4;
