@@ -194,6 +194,15 @@ __host__ __device__ __forceinline__ bool up_resident(int T, int quads) {
 // 41.2 -> 41.7, and 4 of 60 of 3328 x 1280 23.4 -> 23.4, 30.8 -> 31.8 and 47.0 -> 48.6.
 constexpr int kMoeBlocks = 256, kUpLongQuads = 15;
 
+// What k_moe_gate_up leaves for k_moe_down (with the hidden values), and what its workgroups
+// leave for each other.
+struct MoeLists {
+  int* ids;        // [kMoeMaxLists]
+  float* weights;  // [kMoeMaxLists]
+  int* arrived;    // [kMoeBlocks] zeros
+  float* sums;     // [kMoeBlocks][256]
+};
+
 // Waves that share the quads of a group: a workgroup's steps each cost a turn per quad of a wave
 // and about as much again for the sums' exchange and the hidden values, so the fewest of
 // steps x (1 + turns). Few sharers exchange little and give each wave loads to have in flight
@@ -220,7 +229,7 @@ __device__ __forceinline__ int up_share(int experts, int groups, int quads, int 
 // 8 KB than in 37 (1 token, 8 of 64 experts of 2048 x 768, int8 20.9 -> 19.2 us; 8 tokens of 4096 x
 // 1280, MX4, 79 -> 73 us).
 template <class T, bool MX, int V, int NT, bool RES>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* ids, float* weights) {
+__global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, MoeLists lists) {
   extern __shared__ __attribute__((aligned(16))) char s_x[];  // [quads or waves][act_bytes(T)]
   __shared__ MoeTable table;
   __shared__ float red[kUpWaves][2][16][17];
@@ -239,7 +248,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
   lds_barrier();
   // One workgroup writes what the second launch goes by, all of it from its own view of the
   // logits, so that it is consistent whatever else happens to them meanwhile.
-  router.route(a, lane, table, blockIdx.x == 0 ? ids : nullptr, weights);
+  router.route(a, lane, table, blockIdx.x == 0 ? lists.ids : nullptr, lists.weights);
+  if (!MX && blockIdx.x == 0 && tid < kMoeBlocks) lists.arrived[tid] = 0;
   lds_barrier();
   const MoeOrder order(table, lane);
 
@@ -338,8 +348,11 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, int* i
 // 1280) and gave nothing where 16 fit (int8).
 constexpr int kDownWaves = 16, kDownTokens = 4;
 
-template <class T, bool MX>
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const int* ids, const float* weights) {
+// SPLIT: gridDim.y workgroups share the items of 16 features. Each writes its sums, [T][16], and
+// counts itself in; the last adds them up in order, so the result does not depend on which that
+// is. Nobody waits for another workgroup.
+template <class T, bool MX, bool SPLIT>
+__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeLists lists) {
   constexpr int WAVES = kDownWaves, TOK = kDownTokens, ROWS = 2 * TOK;
   __shared__ __attribute__((aligned(16))) char s_x[WAVES * ROWS * kActStride];
   __shared__ unsigned s_tokens[kMoeMaxExperts];
@@ -354,8 +367,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const i
   int id = -1;
   float weight = 0.0f;
   if (tid < n_lists) {
-    id = ids[tid];
-    weight = weights[tid];
+    id = lists.ids[tid];
+    weight = lists.weights[tid];
   }
   for (int i = tid; i < a.E; i += 64 * WAVES) s_tokens[i] = 0u;
   for (int i = lane; i < kMoeMaxTokens * 17; i += 64) (&total[wave][0][0])[i] = 0.0f;
@@ -393,14 +406,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const i
 
   constexpr int UK = WeightFmt<MX>::UK;
   const int ks = (a.I + UK - 1) / UK, quads = (ks + 3) >> 2;
-  const int items = passes * quads, per = (items + WAVES - 1) / WAVES;
-  int begin = min(items, per * wave), end = min(items, begin + per);
+  const int parts = SPLIT ? gridDim.y : 1, waves = WAVES * parts, at = SPLIT ? blockIdx.y * WAVES + wave : wave;
+  const int items = passes * quads, per = (items + waves - 1) / waves;
+  int begin = min(items, per * at), end = min(items, begin + per);
   // With waves for every pass no wave's share crosses into a second pass, whose rows it would
   // have to wait for again; neighbouring waves, on different SIMDs, take different passes (1
   // token, 8 of 64 experts of 2048 x 768, int8 19.4 -> 18.6 us, of 4096 x 1280 36.4 -> 35.6; with
   // neighbours on the same pass, so on two SIMDs, 4 of 32 of 1024 x 512 11.9 -> 13.3).
-  if (passes > 0 && passes <= WAVES) {
-    const int share = WAVES / passes, n = (quads + share - 1) / share, s = wave / passes, p = wave - s * passes;
+  if (passes > 0 && passes <= waves) {
+    const int share = waves / passes, n = (quads + share - 1) / share, s = at / passes, p = at - s * passes;
     if (n <= per) {
       begin = p * quads + min(quads, s * n);
       end = p * quads + min(quads, (s + 1) * n);
@@ -487,16 +501,34 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, const i
   }
   lds_barrier();
   const int t = tid >> 4, f = tid & 15;
+  float y = 0.0f;
   if (t < a.T) {
-    float y = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) y += total[w][t][f];
-    static_cast<typename T::elem*>(a.Y)[static_cast<size_t>(t) * a.D + blockIdx.x * 16 + f] = T::round(y);
   }
+  if constexpr (SPLIT) {
+    // The sums pass through memory that every XCD sees: written and read as device-scope atomics,
+    // ordered by the count, one release and acquire per workgroup (a fence in every wave took
+    // 30 us).
+    __shared__ bool s_last;
+    float* sums = lists.sums + (static_cast<size_t>(blockIdx.x) * parts) * 256 + tid;
+    if (t < a.T) __hip_atomic_store(sums + blockIdx.y * 256, y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tid == 0)
+      s_last = __hip_atomic_fetch_add(lists.arrived + blockIdx.x, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    __syncthreads();
+    if (!s_last) return;
+    y = 0.0f;
+    if (t < a.T)
+      for (int p = 0; p < parts; ++p) y += __hip_atomic_load(sums + p * 256, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (t < a.T)
+    static_cast<typename T::elem*>(a.Y)[static_cast<size_t>(t) * a.D + blockIdx.x * 16 + f] = T::round(y);
 }
 
 template <class T, bool MX, int V, int NT, bool RES>
-static hipError_t run_up(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
+static hipError_t run_up(const MoeArgs& a, const MoeLists& lists, hipStream_t s) {
   const int n_slots = a.E < a.T * a.k ? a.E : a.T * a.k;
   constexpr int UK = WeightFmt<MX>::UK;
   const int quads = ((a.D + UK - 1) / UK + 3) / 4;
@@ -507,34 +539,57 @@ static hipError_t run_up(const MoeArgs& a, int* ids, float* weights, hipStream_t
   const bool two = !MX && quads >= kUpLongQuads && 2 * (lds + kStatic) <= kMaxLds;
   const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16), most = two ? 2 * kMoeBlocks : kMoeBlocks;
   const unsigned blocks = static_cast<unsigned>(steps < most ? steps : most);
-  hipLaunchKernelGGL((k_moe_gate_up<T, MX, V, NT, RES>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, ids, weights);
+  hipLaunchKernelGGL((k_moe_gate_up<T, MX, V, NT, RES>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, lists);
   return hipGetLastError();
+}
+
+// Workgroups that share 16 features of Y: few features leave CUs idle, the more items of a wave
+// the longer, and the exchange costs 3 to 5 us. int8, at least three items per wave saved (by
+// the most passes that the lists can have): 8 of 64 experts of 2048 x 768, 4 / 8 / 16 tokens 40.8 ->
+// 37.7, 58.0 -> 54.0, 73.6 -> 64.6 us; 4 of 60 of 2048 x 1408, 16 tokens 88.3 -> 76.7; 2 of 16 of
+// 512 x 2048, four workgroups, 4 / 16 tokens 20.8 -> 17.6, 35.6 -> 25.8; with fewer, 2 tokens of 2048
+// x 768 25.7 -> 26.7. An MX4 item is half as long: 16 tokens 48.0 -> 46.2, 49.4 -> 50.8, 8 tokens
+// 38.3 -> 37.2, 38.6 -> 41.6: not worth it.
+static int down_parts(const MoeArgs& a, int quads) {
+  const int parts = a.D <= 16 * kMoeBlocks / 4 ? 4 : a.D <= 16 * kMoeBlocks / 2 ? 2 : 1;
+  const int n = a.T * a.k, most = a.E + n / kDownTokens, passes = n < most ? n : most;
+  const int per = (passes * quads + kDownWaves - 1) / kDownWaves, split = (per + parts - 1) / parts;
+  return per - split >= 3 ? parts : 1;
 }
 
 template <class T, bool MX>
-static hipError_t run(const MoeArgs& a, int* ids, float* weights, hipStream_t s) {
+static hipError_t run(const MoeArgs& a, const MoeLists& lists, hipStream_t s) {
   constexpr int UK = WeightFmt<MX>::UK, V = kMoeMaxExperts / 64;
   const bool few = a.T <= kUpWaves, small = a.E <= 64;
   hipError_t e;
-  if (!up_resident<MX>(a.T, ((a.D + UK - 1) / UK + 3) / 4)) e = run_up<T, MX, V, 2, false>(a, ids, weights, s);
-  else if (few) e = small ? run_up<T, MX, 1, 1, true>(a, ids, weights, s) : run_up<T, MX, V, 1, true>(a, ids, weights, s);
-  else e = small ? run_up<T, MX, 1, 2, true>(a, ids, weights, s) : run_up<T, MX, V, 2, true>(a, ids, weights, s);
+  if (!up_resident<MX>(a.T, ((a.D + UK - 1) / UK + 3) / 4)) e = run_up<T, MX, V, 2, false>(a, lists, s);
+  else if (few) e = small ? run_up<T, MX, 1, 1, true>(a, lists, s) : run_up<T, MX, V, 1, true>(a, lists, s);
+  else e = small ? run_up<T, MX, 1, 2, true>(a, lists, s) : run_up<T, MX, V, 2, true>(a, lists, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_moe_down<T, MX>), dim3(a.D / 16), dim3(64 * kDownWaves), 0, s, a, ids, weights);
+  if constexpr (!MX) {
+    const int parts = down_parts(a, ((a.I + UK - 1) / UK + 3) / 4);
+    if (parts > 1) {
+      hipLaunchKernelGGL((k_moe_down<T, MX, true>), dim3(a.D / 16, parts), dim3(64 * kDownWaves), 0, s, a, lists);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_moe_down<T, MX, false>), dim3(a.D / 16), dim3(64 * kDownWaves), 0, s, a, lists);
   return hipGetLastError();
 }
 
-// Workspace: the lists' ids and weights, then the hidden values.
-size_t moe_workspace(int T, int I, int k) {
-  return kMoeMaxLists * (sizeof(int) + sizeof(float)) + static_cast<size_t>(T) * k * I * 4;
-}
+// Workspace: the lists, the down product's counts and sums, then the hidden values.
+constexpr size_t kMoeListBytes = kMoeMaxLists * (sizeof(int) + sizeof(float)) + kMoeBlocks * (sizeof(int) + 256 * sizeof(float));
+size_t moe_workspace(int T, int I, int k) { return kMoeListBytes + static_cast<size_t>(T) * k * I * 4; }
 
 hipError_t launch_moe(MoeArgs a, void* workspace, int type, bool mx4, hipStream_t s) {
-  int* ids = static_cast<int*>(workspace);
-  float* weights = reinterpret_cast<float*>(ids + kMoeMaxLists);
-  a.h = reinterpret_cast<uint16_t*>(weights + kMoeMaxLists);
-  if (type == kMxF16) return mx4 ? run<F16, true>(a, ids, weights, s) : run<F16, false>(a, ids, weights, s);
-  return mx4 ? run<B16, true>(a, ids, weights, s) : run<B16, false>(a, ids, weights, s);
+  MoeLists l;
+  l.ids = static_cast<int*>(workspace);
+  l.weights = reinterpret_cast<float*>(l.ids + kMoeMaxLists);
+  l.arrived = reinterpret_cast<int*>(l.weights + kMoeMaxLists);
+  l.sums = reinterpret_cast<float*>(l.arrived + kMoeBlocks);
+  a.h = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kMoeListBytes);
+  if (type == kMxF16) return mx4 ? run<F16, true>(a, l, s) : run<F16, false>(a, l, s);
+  return mx4 ? run<B16, true>(a, l, s) : run<B16, false>(a, l, s);
 }
 
 }  // namespace i8mm

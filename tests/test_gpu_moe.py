@@ -94,6 +94,41 @@ def test_two_workgroups_per_cu(T, E, I):
     check(X, logits, pairs, values, 2, False)
 
 
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("T,D,I,E,k", [(16, 1040, 1040, 16, 4), (4, 272, 1040, 8, 4), (9, 2048, 784, 12, 3),
+                                       (16, 1024, 1024, 8, 8), (16, 16, 4112, 4, 2)])
+def test_down_product_of_several_workgroups(T, D, I, E, k, dtype):
+    """int8, few features and many items: two or four workgroups share 16 features."""
+    announce(f"moe T={T} D={D} I={I} E={E} k={k} {dtype}")
+    X, logits, pairs, values = case(T, D, I, E, dtype, "int8", T + D)
+    logits[T // 2] = -float("inf")       # a padding row
+    y = check(X, logits, pairs, values, k, True)
+    lg = logits.cuda()
+    ws = torch.full((moe.workspace_bytes(T, I, k),), 255, dtype=torch.uint8, device="cuda")
+    want, alone = y.clone(), torch.zeros_like(y)
+    for _ in range(3):                   # the workspace's contents do not matter
+        assert torch.equal(moe.moe_layer(X, lg, *pairs, k, workspace=ws)[0], want)
+        ws.fill_(85)
+    off = torch.full_like(lg, -float("inf"))
+    assert torch.equal(moe.moe_layer(X, off, *pairs, k, workspace=ws)[0], alone)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        moe.moe_layer(X, lg, *pairs, k, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        a = moe.moe_layer(X, lg, *pairs, k, workspace=ws)[0]
+        b = moe.moe_layer(X, lg, *pairs, k, workspace=ws)[0]
+    for _ in range(4):
+        a.zero_()
+        b.zero_()
+        g.replay()
+        eager = moe.moe_layer(X, lg, *pairs, k)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want) and torch.equal(eager, want)
+
+
 @pytest.mark.parametrize("T", [7, 8, 9])
 def test_many_experts_and_the_edge_of_one_token_per_wave(T):
     for E in (64, 65, 130):
