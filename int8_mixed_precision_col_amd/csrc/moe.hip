@@ -16,8 +16,8 @@
 // that chose the expert.
 // k_moe_down: a workgroup per 16 output features goes over all chosen experts, its waves
 // sharing the (pass, K quad) items in order (a pass: up to four tokens of one expert), so
-// that the weighted sum over experts needs neither atomics nor a third launch and is the same
-// on every run.
+// that the weighted sum over experts needs no third launch and is the same on every run. With
+// few features several workgroups share 16 of them, and the last one there adds up their sums.
 //
 // The hidden values stay near fp32: they are kept as a bf16 pair, high part and remainder
 // (16 significant bits, the full exponent range, so that no |h| > 65504 turns into an
@@ -26,8 +26,8 @@
 // two sums are added in the end.
 //
 // Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
-// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 165 us, 5.5 TB/s, MX4 94.5 us, 5.0 TB/s;
-// of 2048 x 768 75 and 48 us; 1 token of these 18.6 and 15.0 us, of which 7.5 and 4.0 us are the
+// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 160 us, 5.5 TB/s, MX4 94.5 us, 5.0 TB/s;
+// of 2048 x 768 63 and 48 us; 1 token of these 18.6 and 15.0 us, of which 7.5 and 4.0 us are the
 // bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
