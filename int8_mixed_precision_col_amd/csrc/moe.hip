@@ -26,8 +26,8 @@
 // two sums are added in the end.
 //
 // Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
-// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 160 us, 5.5 TB/s, MX4 94.5 us, 5.0 TB/s;
-// of 2048 x 768 63 and 48 us; 1 token of these 18.6 and 15.0 us, of which 7.5 and 4.0 us are the
+// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 152 us, 5.7 TB/s, MX4 94.5 us, 5.0 TB/s;
+// of 2048 x 768 61 and 46 us; 1 token of these 18.6 and 14.8 us, of which 7.5 and 4.0 us are the
 // bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
@@ -189,7 +189,7 @@ __host__ __device__ __forceinline__ bool up_resident(int T, int quads) {
   return quads * act_bytes<MX>(T) <= kUpResident;
 }
 
-// Workgroups of k_moe_gate_up: one per CU. Two where they fit (int8 takes 124 registers) and a step is long, D of 15 quads (3.6 K) and more: 1 / 2 / 4 tokens, 8 of 64 experts of
+// Workgroups of k_moe_gate_up: one per CU. Two where they fit (int8 takes 126 registers) and a step is long, D of 15 quads (3.6 K) and more: 1 / 2 / 4 tokens, 8 of 64 experts of
 // 4096 x 1280, 36.7 -> 36.4, 53 -> 49 and 85 -> 81 us; but of 2048 x 768 19.3 -> 20.4, 26.5 -> 26.8 and
 // 41.2 -> 41.7, and 4 of 60 of 3328 x 1280 23.4 -> 23.4, 30.8 -> 31.8 and 47.0 -> 48.6.
 constexpr int kMoeBlocks = 256, kUpLongQuads = 15;
@@ -210,8 +210,9 @@ struct MoeLists {
 // 4 / 2 sharers: 16 tokens, 8 of 64 experts of 4096 x 1280, MX4 116 / 100 / 97, int8 172 / 162 /
 // 167; of 2048 x 768, int8 87 / 81 / 77, 4 tokens 45 / 42 / 44, 1 token 21.7 / 20.2 / 23.2; 1
 // token of 4096 x 1280, MX4 28 / 28 / 25. (One: 102, 179, 82, 40, 28.8 and 31.)
+template <bool MX>
 __device__ __forceinline__ int up_share(int experts, int groups, int quads, int blocks) {
-  const int most = quads >= 5 ? 8 : quads >= 3 ? 4 : quads;
+  const int most = quads >= 5 ? 8 : quads >= 3 ? 4 : MX ? quads : 2;  // int8: at most four groups at once
   int best = most, least = 0x7fffffff;
   for (int share = most; share >= 2 || share == most; share >>= 1) {
     const int par = kUpWaves / share, steps = experts * ((groups + par - 1) / par);
@@ -229,10 +230,11 @@ __device__ __forceinline__ int up_share(int experts, int groups, int quads, int 
 // 8 KB than in 37 (1 token, 8 of 64 experts of 2048 x 768, int8 20.9 -> 19.2 us; 8 tokens of 4096 x
 // 1280, MX4, 79 -> 73 us).
 template <class T, bool MX, int V, int NT, bool RES>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, MoeLists lists) {
+__global__ __launch_bounds__(64 * kUpWaves, !MX && RES ? 4 : 2) void k_moe_gate_up(MoeArgs a, MoeLists lists) {
   extern __shared__ __attribute__((aligned(16))) char s_x[];  // [quads or waves][act_bytes(T)]
   __shared__ MoeTable table;
   __shared__ float red[kUpWaves][2][16][17];
+  __shared__ float s_col[128];  // int8: gate and up constants of the step's groups, over 127
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr int UK = WeightFmt<MX>::UK;
   const int ks = (a.D + UK - 1) / UK, quads = (ks + 3) >> 2, groups = a.I / 16;
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, MoeLis
 
   // A step is `par` neighbouring 16-feature groups of one expert, `share` waves on the quads
   // of each.
-  const int share = up_share(order.count(), groups, quads, gridDim.x > kMoeBlocks ? 2 * kMoeBlocks : kMoeBlocks);
+  const int share = up_share<MX>(order.count(), groups, quads, gridDim.x > kMoeBlocks ? 2 * kMoeBlocks : kMoeBlocks);
   const int par = kUpWaves / share;
   const int steps = (groups + par - 1) / par;
   // steps [first, last) of the list are this workgroup's
@@ -290,6 +292,15 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, MoeLis
     const unsigned tokens = __builtin_amdgcn_readfirstlane(table.tokens[expert]);
     const int next_in = in + 1 < steps ? in + 1 : 0;
     const int next_expert = next_in == 0 && step + 1 < n_steps ? order.expert(slot + 1) : expert;
+    // int8: the step's column constants, one per thread. Asked for here, in front of the next
+    // step's weights: loads return in order, so that a wait for them behind those waits for both
+    // (with the down product's: 16 tokens, 8 of 64 experts of 4096 x 1280, 158 -> 152 us).
+    float col = 0.0f;
+    if (!MX && tid < 128) {
+      const int group = min(in * par + ((tid >> 4) & 3), groups - 1);
+      col = static_cast<const float*>(a.s13)[(static_cast<size_t>(expert) * 2 * groups + group) * 16 + (tid & 15) +
+                                             (tid < 64 ? 0 : a.I)];
+    }
     v4f acc[2] = {};
     for (int q = kk; q < quads; q += share) {
       const char* buf = s_x + (RES ? q : wave) * act_bytes<MX>(a.T);
@@ -308,6 +319,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, MoeLis
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[wave][p][4 * (lane >> 4) + e][lane & 15] = acc[p][e];
+    if (!MX && tid < 128) s_col[tid] = __fdiv_rn(col, 127.0f);
     lds_barrier();
     for (int o = tid; o < 256 * par; o += 64 * kUpWaves) {
       const int n = o & 15, t = (o >> 4) & 15, s = o >> 8;
@@ -319,9 +331,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(MoeArgs a, MoeLis
         u += red[s * share + w][1][t][n];
       }
       if constexpr (!MX) {
-        const float* aw = static_cast<const float*>(a.s13) + (static_cast<size_t>(expert) * 2 * groups + group) * 16 + n;
-        g *= __fdiv_rn(aw[0], 127.0f);
-        u *= __fdiv_rn(aw[a.I], 127.0f);
+        g *= s_col[16 * s + n];
+        u *= s_col[64 + 16 * s + n];
       }
       const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
       const __bf16 hi = static_cast<__bf16>(h);
@@ -356,10 +367,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
   constexpr int WAVES = kDownWaves, TOK = kDownTokens, ROWS = 2 * TOK;
   __shared__ __attribute__((aligned(16))) char s_x[WAVES * ROWS * kActStride];
   __shared__ unsigned s_tokens[kMoeMaxExperts];
-  __shared__ uint8_t s_place[kMoeMaxExperts * kMoeMaxTokens], s_pass[kMoeMaxLists];
+  __shared__ uint8_t s_place[kMoeMaxExperts * kMoeMaxTokens];
   __shared__ uint64_t s_first[kMoeMaxLists / 64];
-  __shared__ int s_id[kMoeMaxLists];
   __shared__ float s_w[kMoeMaxLists];
+  // passes: expert, number of tokens, and by token (bytes) the list entry and the token
+  __shared__ __attribute__((aligned(16))) v4i s_pass[kMoeMaxLists];
+  __shared__ __attribute__((aligned(16))) v4f s_share[kMoeMaxLists];  // by token its weight
   __shared__ float total[WAVES][kMoeMaxTokens][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_lists = a.T * a.k;
@@ -381,12 +394,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
     atomicOr(&s_tokens[id], 1u << t_of);
     s_place[id * kMoeMaxTokens + t_of] = static_cast<uint8_t>(tid - t_of * a.k);
   }
-  if (tid < n_lists) {
-    s_id[tid] = id;
-    s_w[tid] = weight;
-  }
+  if (tid < n_lists) s_w[tid] = weight;
   lds_barrier();
-  // Passes: TOK tokens of one expert, each found by the list entry of its first token and kept
+  // Passes: TOK tokens of one expert, each written by the list entry of its first token and kept
   // in that order. A pass is a wave's unit whatever its expert, so that an expert with many
   // tokens does not hold up one wave.
   const int before = id < 0 ? 0 : __builtin_popcount(s_tokens[id] & ((1u << (t_of & 31)) - 1));
@@ -399,8 +409,24 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
     if (i == wave) mine = passes;
     passes += __builtin_popcountll(s_first[i]);
   }
-  if (id >= 0 && before % TOK == 0)
-    s_pass[mine + __builtin_popcountll(starts & ((uint64_t(1) << lane) - 1))] = static_cast<uint8_t>(tid);
+  if (id >= 0 && before % TOK == 0) {
+    static_assert(TOK == 4, "four bytes, four weights");
+    unsigned left = s_tokens[id] & ~((1u << t_of) - 1), entries = 0, tokens = 0;
+    v4f w = {};
+    const int m = min(__builtin_popcount(left), TOK);
+#pragma unroll
+    for (int c = 0; c < TOK; ++c)
+      if (c < m) {
+        const int t = __builtin_ctz(left), entry = t * a.k + s_place[id * kMoeMaxTokens + t];
+        left &= left - 1;
+        entries |= static_cast<unsigned>(entry) << (8 * c);
+        tokens |= static_cast<unsigned>(t) << (8 * c);
+        w[c] = s_w[entry];
+      }
+    const int pass = mine + __builtin_popcountll(starts & ((uint64_t(1) << lane) - 1));
+    s_pass[pass] = v4i{id, m, static_cast<int>(entries), static_cast<int>(tokens)};
+    s_share[pass] = w;
+  }
   lds_barrier();
   passes = __builtin_amdgcn_readfirstlane(passes);
 
@@ -425,53 +451,41 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, plane * 2u);
   const int r = lane & 15, g = lane >> 4;
   WeightQuad<MX> next;
+  float col = 1.0f, col_next = 1.0f;  // int8: the feature's column constant
   auto prefetch = [&](int expert, int q) {
     next.load(a.w2, static_cast<const uint32_t*>(a.s2), static_cast<size_t>(expert) * (a.D / 16) + blockIdx.x, ks, quads,
               q, lane);
   };
-  auto expert_of = [&](int pass) { return __builtin_amdgcn_readfirstlane(s_id[s_pass[pass]]); };
-  int pass = begin / quads, expert = 0;
-  if (begin < end) {
-    expert = expert_of(pass);
-    prefetch(expert, begin - pass * quads);
-  }
+  // the first quad of a wave's share of a pass, in front of it the constant (loads return in order)
+  auto enter = [&](int pass, int q) {
+    const int expert = __builtin_amdgcn_readfirstlane(s_pass[pass][0]);
+    if constexpr (!MX) col_next = static_cast<const float*>(a.s2)[static_cast<size_t>(expert) * a.D + blockIdx.x * 16 + r];
+    prefetch(expert, q);
+  };
+  int pass = begin / quads;
+  if (begin < end) enter(pass, begin - pass * quads);
   for (int i = begin; i < end; ++pass) {
     // items [i, stop) are quads of one pass, the wave's share of it
     const int q0 = i - pass * quads, stop = min(end, (pass + 1) * quads), q1 = stop - pass * quads;
-    const int current = expert;
-    const unsigned t0 = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(s_pass[pass])) / static_cast<unsigned>(a.k);
-    // the pass's tokens: this one and those after it
-    const unsigned tokens = __builtin_amdgcn_readfirstlane(s_tokens[current]) & ~((1u << t0) - 1);
-    const int m = min(__builtin_popcount(tokens), TOK);
     i = stop;
-    auto list_of = [&](int c) {  // list entry of the pass's c-th token
-      unsigned b = tokens;
-      for (int j = 0; j < c; ++j) b &= b - 1;
-      const int t = __builtin_ctz(b);
-      return t * a.k + s_place[current * kMoeMaxTokens + t];
-    };
-    // this lane's rows: byte offsets of rows 2 j + l / 32 in h
+    const v4i p = s_pass[pass];
+    const int expert = __builtin_amdgcn_readfirstlane(p[0]), m = __builtin_amdgcn_readfirstlane(p[1]);
+    const unsigned entries = __builtin_amdgcn_readfirstlane(p[2]), tokens = __builtin_amdgcn_readfirstlane(p[3]);
+    col = col_next;
+    // row 2 c is the high parts of the pass's token c, row 2 c + 1 its remainders: byte offsets in h
+    // of this half wave's
     unsigned off[TOK];
 #pragma unroll
-    for (int j = 0; j < TOK; ++j) {
-      const int row = 2 * j + (lane >> 5);
-      off[j] = row < 2 * m ? static_cast<unsigned>(list_of(row < m ? row : row - m)) * a.I * 2u +
-                                 (row < m ? 0u : plane)
-                           : kOOB;
-    }
+    for (int c = 0; c < TOK; ++c) off[c] = ((entries >> (8 * c)) & 255u) * (a.I * 2u) + (lane < 32 ? 0u : plane);
     // operand rows 0 .. TOK - 1 are the high parts, 8 .. the remainders; the others repeat one
-    const int row = min(r & 7, m - 1) + (r < 8 ? 0 : m);
+    const int row = 2 * min(r & 7, m - 1) + (r >> 3);
     v4f acc[1] = {};
     for (int q = q0; q < q1; ++q) {
       WeightQuad<MX> w[1] = {next};
       ActQuad<MX, ROWS> x;
       x.load(hr, q, a.I, 2 * m, lane, [&](int j) { return off[j >> 1]; });
-      if (q + 1 < q1) {
-        prefetch(expert, q + 1);
-      } else if (i < end) {
-        expert = expert_of(pass + 1);
-        prefetch(expert, 0);
-      }
+      if (q + 1 < q1) prefetch(expert, q + 1);
+      else if (i < end) enter(pass + 1, 0);
       wave_lds_fence();
       x.store_piece(0, buf, 2 * m, lane);
       wave_lds_fence();
@@ -484,19 +498,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
         mma_quad<B16, MX, 1, 2, 4>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
       }
     }
-    // weigh the sums into the tokens'
-    float scale = 1.0f;
-    if constexpr (!MX)
-      scale = __fdiv_rn(static_cast<const float*>(a.s2)[static_cast<size_t>(current) * a.D + blockIdx.x * 16 + r], 127.0f);
+    // weigh the sums into the tokens': lane r of group 0 holds the high parts' sums of the tokens,
+    // of group 2 the remainders'
+    const v4f weights = s_share[pass];
+    const float scale = MX ? 1.0f : __fdiv_rn(col, 127.0f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // rows c (high) and 8 + c (remainder) of one token are 32 lanes apart
-      const float y = acc[0][e] + __shfl_xor(acc[0][e], 32, 64);
-      const int c = 4 * (g & 1) + e;
-      if (g < 2 && c < m) {
-        const int list = list_of(c);
-        total[wave][list / a.k][r] += y * scale * s_w[list];
-      }
+    for (int c = 0; c < TOK; ++c) {
+      const float y = acc[0][c] + __shfl_xor(acc[0][c], 32, 64);
+      if (g == 0 && c < m) total[wave][(tokens >> (8 * c)) & 255u][r] += y * scale * weights[c];
     }
   }
   lds_barrier();
@@ -533,7 +542,7 @@ static hipError_t run_up(const MoeArgs& a, const MoeLists& lists, hipStream_t s)
   constexpr int UK = WeightFmt<MX>::UK;
   const int quads = ((a.D + UK - 1) / UK + 3) / 4;
   const size_t lds = static_cast<size_t>(RES ? quads : kUpWaves) * act_bytes<MX>(a.T);
-  constexpr size_t kStatic = sizeof(MoeTable) + sizeof(float) * kUpWaves * 2 * 16 * 17;
+  constexpr size_t kStatic = sizeof(MoeTable) + sizeof(float) * (kUpWaves * 2 * 16 * 17 + 128);
   static_assert(kUpResident + kStatic <= kMaxLds && kUpWaves * act_bytes<MX>(kMoeMaxTokens) + kStatic <= kMaxLds,
                 "k_moe_gate_up's LDS");
   const bool two = !MX && quads >= kUpLongQuads && 2 * (lds + kStatic) <= kMaxLds;
