@@ -117,9 +117,9 @@ def _need_rows(X: torch.Tensor, name: str, types=_HALF) -> tuple:
 
 def _need_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: int, K: int, like: torch.Tensor, name: str) -> None:
     """A tiled pair of `rows` rows of K elements on `like`'s device: the kernels trust its
-    sizes."""
+    sizes and that it is in device memory (`like` may be the pair itself)."""
     want = _sizes(rows, K)
-    if (codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous()
+    if (binding._on_device(codes) and codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous()
             and scales.is_contiguous() and want[0] and codes.numel() == want[0] and scales.numel() == want[1]
             and codes.get_device() == scales.get_device() == like.get_device()):
         return

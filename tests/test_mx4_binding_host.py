@@ -188,3 +188,24 @@ def test_launch_makes_the_tensors_device_current(monkeypatch):
     with pytest.raises(binding.Int8mmError):
         mx4._launch("mx4_quantize", Tensor(), 7, 8)
     assert seen[-1] == ("exit", 1)
+
+
+def test_cpu_tensors_are_refused_by_every_call(monkeypatch):
+    """With the device predicate as it is: tensors in host memory, alone or all of them, never
+    reach a launch."""
+    launched = []
+    monkeypatch.setattr(mx4, "_launch", lambda name, t, *args: launched.append(name))
+    X, W, q = f16(5, 272), pair(48, 272), pair(5, 272)
+    packed, bytes_ = torch.zeros((48, 144), dtype=torch.uint8), torch.zeros((48, 9), dtype=torch.uint8)
+    calls = {
+        "quantize": lambda: mx4.quantize(X), "prepare_weight": lambda: mx4.prepare_weight(f16(272, 48)),
+        "tile_weight": lambda: mx4.tile_weight(packed, bytes_, 272),
+        "dequantize": lambda: mx4.dequantize(*q, 5, 272), "dequantize, out": lambda: mx4.dequantize(*q, 5, 272, out=X),
+        "matmul": lambda: mx4.matmul(X, *W), "matmul_q": lambda: mx4.matmul_q(*q, 5, 272, *W),
+        "weight_only_matmul": lambda: mx4.weight_only_matmul(X, *W),
+        "moe_layer": lambda: moe.moe_layer(f16(3, 64), torch.zeros(3, 4), pair(4 * 2 * 32, 64), pair(4 * 64, 32), 2),
+    }
+    for name, f in calls.items():
+        with pytest.raises(ValueError):
+            f()
+        assert launched == [], name
