@@ -137,8 +137,7 @@ int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int
  *                 (id -1 and weight 0 past the last chosen expert).
  *   workspace     at least moe_layer_workspace_bytes(T, I, top_k) bytes; its contents do not
  *                 matter. Calls that may run at the same time need workspaces of their own.
- * fp32 sums; the hidden values are kept to 16 significant bits; one rounding of Y. The same
- * inputs give the same bits.
+ * fp32 sums and hidden values; one rounding of Y. The same inputs give the same bits.
  */
 size_t moe_layer_workspace_bytes(int64_t T, int64_t I, int64_t top_k);
 int moe_layer(const void* X, int64_t T, int64_t D, int64_t ldx, int dtype, const void* logits,

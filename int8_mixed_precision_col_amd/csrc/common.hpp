@@ -231,8 +231,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, un
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(bytes),
                                            0x00020000);
 }
-__device__ __forceinline__ v4u buf_load16(__amdgpu_buffer_rsrc_t r, unsigned off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0);
+// `more`: a uniform offset added to `off`; the sum is in range where `off` is.
+__device__ __forceinline__ v4u buf_load16(__amdgpu_buffer_rsrc_t r, unsigned off, unsigned more = 0) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), static_cast<int>(more), 0);
 }
 
 }  // namespace i8mm

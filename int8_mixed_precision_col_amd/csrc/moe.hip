@@ -19,11 +19,10 @@
 // that the weighted sum over experts needs no third launch and is the same on every run. With
 // few features several workgroups share 16 of them, and the last one there adds up their sums.
 //
-// The hidden values stay near fp32: they are kept as a bf16 pair, high part and remainder
-// (16 significant bits, the full exponent range, so that no |h| > 65504 turns into an
-// infinity). The pair costs no instructions in the down product: a pass has four tokens, so
-// rows 0-3 of the 16-row operand hold their high parts and rows 8-11 the remainders, and the
-// two sums are added in the end.
+// The hidden values stay fp32 between the launches, and enter the matrix instructions as three
+// bf16 parts of 8 significant bits, 24 together. The parts cost no matrix instructions: a pass
+// has four tokens, so rows 0-3, 4-7 and 8-11 of the 16-row operand hold their first, second
+// and third parts, and the three sums are added in the end.
 //
 // Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
 // time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 152 us, 5.7 TB/s, MX4 94.5 us, 5.0 TB/s;
@@ -335,13 +334,8 @@ __global__ __launch_bounds__(64 * kUpWaves, !MX && RES ? 4 : 2) void k_moe_gate_
         u *= s_col[64 + 16 * s + n];
       }
       const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
-      const __bf16 hi = static_cast<__bf16>(h);
-      const float rest = h - static_cast<float>(hi);
-      const __bf16 lo = static_cast<__bf16>(fabsf(rest) < __builtin_inff() ? rest : 0.0f);
       const int list = t * a.k + table.place[expert * kMoeMaxTokens + t];
-      const size_t at = static_cast<size_t>(list) * a.I + group * 16 + n;
-      a.h[at] = __builtin_bit_cast(uint16_t, hi);
-      a.h[static_cast<size_t>(a.T * a.k) * a.I + at] = __builtin_bit_cast(uint16_t, lo);
+      a.h[static_cast<size_t>(list) * a.I + group * 16 + n] = h;
     }
     lds_barrier();  // red is read
     slot += next_in == 0;
@@ -350,21 +344,72 @@ __global__ __launch_bounds__(64 * kUpWaves, !MX && RES ? 4 : 2) void k_moe_gate_
   }
 }
 
-// A pass over an expert's quads serves TOK of its tokens (2 TOK rows: high parts and
-// remainders); further ones read its weights again, from a cache. Eight tokens per pass leave
+// A pass over an expert's quads serves TOK of its tokens (kMoeParts TOK rows); further ones read
+// its weights again, from a cache. Eight tokens per pass (measured with two parts each) leave
 // LDS for 8 waves instead of 16: 132 for 114 us (16 tokens, 8 of 64 experts of 2048 x 1280,
 // int8), 112.6 for 111.2 (8 of 32 of 4096 x 1280), 51.8 for 51.0 (4 of 8), 24.3 for 21.9 (one
 // expert), and at best 39.9 for 41.5 (8 tokens, 4 of 8). A load of the next item's h ahead of the
 // products, as the weights', leaves 8 waves too for MX4 (111 for 97 us, 16 tokens of 4096 x
 // 1280) and gave nothing where 16 fit (int8).
 constexpr int kDownWaves = 16, kDownTokens = 4;
+constexpr int kMoeParts = 3;  // bf16 parts of a hidden value
+constexpr float kMoeMost = 0x1p127f;
+
+// The hidden values of one quad for a pass of m tokens, a token's piece (1 KB) per load, split into
+// bf16 parts on the way to the wave's LDS buffer: part p of token c is its row kDownTokens p + c. The
+// parts are cut off (a value's leading 8 significant bits are its upper half), not rounded, and
+// both remainders are exact. Split here, a hidden value is 4 bytes of what a CU takes in; as three bf16
+// planes from the first launch it was 6 (16 tokens, 8 of 64 experts of 4096 x 1280, MX4, 111 against 101
+// us; of 2048 x 768 53.5 against 49).
+template <bool MX>
+struct HiddenQuad {
+  static constexpr int P = ActQuad<MX, 2>::P;
+  v4u raw[P][kDownTokens];
+
+  // off[c]: byte offset of token c's row
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int q, int I, int m, int lane,
+                                       const unsigned (&off)[kDownTokens]) {
+#pragma unroll
+    for (int v = 0; v < P; ++v) {
+      const int k = (P * q + v) * kActPiece + 4 * lane;
+#pragma unroll
+      for (int c = 0; c < kDownTokens; ++c)
+        if (c < m) raw[v][c] = buf_load16(r, k < I ? 4u * k : kOOB, off[c]);
+    }
+  }
+  __device__ __forceinline__ void store_piece(int v, char* buf, int m, int lane) const {
+#pragma unroll
+    for (int c = 0; c < kDownTokens; ++c)
+      if (c < m) {
+        v2u part[kMoeParts];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          unsigned f[2] = {raw[v][c][2 * e], raw[v][c][2 * e + 1]};
+#pragma unroll
+          for (int p = 0; p < kMoeParts; ++p) {
+            part[p][e] = __builtin_amdgcn_perm(f[1], f[0], 0x07060302u);
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              float rest = __builtin_bit_cast(float, f[d]) - __builtin_bit_cast(float, f[d] & 0xffff0000u);
+              // an infinity is all in its first part; the median of NaN and these is finite
+              if (p == 0) rest = __builtin_amdgcn_fmed3f(rest, -kMoeMost, kMoeMost);
+              f[d] = __builtin_bit_cast(unsigned, rest);
+            }
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < kMoeParts; ++p)
+          *reinterpret_cast<v2u*>(buf + (kDownTokens * p + c) * kActStride + 8 * lane) = part[p];
+      }
+  }
+};
 
 // SPLIT: gridDim.y workgroups share the items of 16 features. Each writes its sums, [T][16], and
 // counts itself in; the last adds them up in order, so the result does not depend on which that
 // is. Nobody waits for another workgroup.
 template <class T, bool MX, bool SPLIT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeLists lists) {
-  constexpr int WAVES = kDownWaves, TOK = kDownTokens, ROWS = 2 * TOK;
+  constexpr int WAVES = kDownWaves, TOK = kDownTokens, ROWS = kMoeParts * TOK;
   __shared__ __attribute__((aligned(16))) char s_x[WAVES * ROWS * kActStride];
   __shared__ unsigned s_tokens[kMoeMaxExperts];
   __shared__ uint8_t s_place[kMoeMaxExperts * kMoeMaxTokens];
@@ -447,8 +492,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
       if (s >= share) begin = end = 0;
     }
   }
-  const unsigned plane = static_cast<unsigned>(n_lists) * a.I * 2u;  // bytes
-  const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, plane * 2u);
+  const unsigned plane = static_cast<unsigned>(n_lists) * a.I * 4u;  // bytes
+  const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, plane);
   const int r = lane & 15, g = lane >> 4;
   WeightQuad<MX> next;
   float col = 1.0f, col_next = 1.0f;  // int8: the feature's column constant
@@ -472,39 +517,41 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a, MoeList
     const int expert = __builtin_amdgcn_readfirstlane(p[0]), m = __builtin_amdgcn_readfirstlane(p[1]);
     const unsigned entries = __builtin_amdgcn_readfirstlane(p[2]), tokens = __builtin_amdgcn_readfirstlane(p[3]);
     col = col_next;
-    // row 2 c is the high parts of the pass's token c, row 2 c + 1 its remainders: byte offsets in h
-    // of this half wave's
     unsigned off[TOK];
 #pragma unroll
-    for (int c = 0; c < TOK; ++c) off[c] = ((entries >> (8 * c)) & 255u) * (a.I * 2u) + (lane < 32 ? 0u : plane);
-    // operand rows 0 .. TOK - 1 are the high parts, 8 .. the remainders; the others repeat one
-    const int row = 2 * min(r & 7, m - 1) + (r >> 3);
+    for (int c = 0; c < TOK; ++c) off[c] = ((entries >> (8 * c)) & 255u) * (a.I * 4u);
+    // operand rows TOK p .. are part p of the tokens, those past m and past the parts repeat one
+    const int row = TOK * min(r / TOK, kMoeParts - 1) + min(r % TOK, m - 1);
     v4f acc[1] = {};
     for (int q = q0; q < q1; ++q) {
       WeightQuad<MX> w[1] = {next};
-      ActQuad<MX, ROWS> x;
-      x.load(hr, q, a.I, 2 * m, lane, [&](int j) { return off[j >> 1]; });
+      HiddenQuad<MX> x;
+      x.load(hr, q, a.I, m, lane, off);
+      // The hidden values are here before the next weights are asked for: behind them, with the
+      // number of loads in flight known at run time alone, a wait for them would be one for all
+      // (1 token, 8 of 64 experts of 2048 x 768, int8 18.6 -> 17.9 us; 16 tokens 66.8 -> 65.4).
+      wave_load_fence();
       if (q + 1 < q1) prefetch(expert, q + 1);
       else if (i < end) enter(pass + 1, 0);
       wave_lds_fence();
-      x.store_piece(0, buf, 2 * m, lane);
+      x.store_piece(0, buf, m, lane);
       wave_lds_fence();
       constexpr int HALF = MX ? 2 : 4;
       mma_quad<B16, MX, 1, 0, HALF>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
       if constexpr (MX) {
         wave_lds_fence();
-        x.store_piece(1, buf, 2 * m, lane);
+        x.store_piece(1, buf, m, lane);
         wave_lds_fence();
         mma_quad<B16, MX, 1, 2, 4>(w, acc, [&](int j, int v) { return act_operand<MX>(buf, 0, row, j, v, lane); });
       }
     }
-    // weigh the sums into the tokens': lane r of group 0 holds the high parts' sums of the tokens,
-    // of group 2 the remainders'
+    // weigh the sums into the tokens': lane r of group p holds the sums of the tokens' part p
+    static_assert(TOK == 4 && kMoeParts == 3, "a lane group's four rows are one part");
     const v4f weights = s_share[pass];
     const float scale = MX ? 1.0f : __fdiv_rn(col, 127.0f);
 #pragma unroll
     for (int c = 0; c < TOK; ++c) {
-      const float y = acc[0][c] + __shfl_xor(acc[0][c], 32, 64);
+      const float y = acc[0][c] + (__shfl_xor(acc[0][c], 16, 64) + __shfl_xor(acc[0][c], 32, 64));
       if (g == 0 && c < m) total[wave][(tokens >> (8 * c)) & 255u][r] += y * scale * weights[c];
     }
   }
@@ -596,7 +643,7 @@ hipError_t launch_moe(MoeArgs a, void* workspace, int type, bool mx4, hipStream_
   l.weights = reinterpret_cast<float*>(l.ids + kMoeMaxLists);
   l.arrived = reinterpret_cast<int*>(l.weights + kMoeMaxLists);
   l.sums = reinterpret_cast<float*>(l.arrived + kMoeBlocks);
-  a.h = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kMoeListBytes);
+  a.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMoeListBytes);
   if (type == kMxF16) return mx4 ? run<F16, true>(a, l, s) : run<F16, false>(a, l, s);
   return mx4 ? run<B16, true>(a, l, s) : run<B16, false>(a, l, s);
 }

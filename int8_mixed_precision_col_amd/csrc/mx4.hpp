@@ -161,4 +161,11 @@ __device__ __forceinline__ void wave_lds_fence() {
   asm volatile("" ::: "memory");
 }
 
+// All loads that the wave has asked for are here.
+__device__ __forceinline__ void wave_load_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0 | (0x7 << 4) | (0xF << 8));  // vmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
 }  // namespace i8mm

@@ -88,8 +88,7 @@ struct MoeArgs {
   void* Y;              // [T][D]
   int32_t* ids;         // nullable [T][k]
   float* weights;       // nullable [T][k]
-  uint16_t* h;          // [2][T k][I] bf16: high parts and remainders of the hidden rows
-                        // (set by the launcher)
+  float* h;             // [T k][I]: the hidden rows (set by the launcher)
 };
 size_t moe_workspace(int T, int I, int k);
 hipError_t launch_moe(MoeArgs a, void* workspace, int type, bool mx4, hipStream_t s);

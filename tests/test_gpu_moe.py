@@ -256,3 +256,54 @@ def test_a_decode_step_with_the_operators_together():
     a, b = ref.mx4_round(f64(y)), ref.mx4_round(f64(nxt))
     S = np.abs(a) @ np.abs(b).T
     assert (np.abs(z - a @ b.T) <= S * (5 + 32) * 2.0 ** -23 + np.abs(a @ b.T) * 2.0 ** -8 * 1.01 + 1e-30).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mx4"])
+@pytest.mark.parametrize("T", [1, 3, 16])
+def test_hidden_values_keep_their_24_bits(T, fmt):
+    """Gate rows that all read X[0], up rows that read one element each, and down rows that
+    subtract neighbouring hidden values, which differ in their last fp16 bit: y = silu(X[0])
+    (X[1 + 2 d] - X[2 + 2 d]). What the layer rounds, with s = |silu(X[0])| and hidden values
+    below 2 s: each hidden value twice by half an fp32 step (the column constant's product and
+    the product with silu), so four times 2^-24 of 2 s in a difference; silu, the constants and
+    the sums by a few units that both values share; Y by half a step."""
+    I = 144
+    D = I + 16
+    X = torch.zeros((T, D))
+    g = torch.Generator().manual_seed(T)
+    X[:, 0] = torch.linspace(0.75, 3, T)
+    even = 1 + torch.randint(0, 512, (T, I // 2), generator=g) * 2.0 ** -9
+    X[:, 1:1 + I:2], X[:, 2:2 + I:2] = even + 2.0 ** -10, even
+    X = X.half().cuda()
+    w13, w2 = torch.zeros((2 * I, D)), torch.zeros((D, I))
+    w13[:I, 0] = 1
+    w13[torch.arange(I) + I, torch.arange(I) + 1] = 1
+    d = torch.arange(I // 2)
+    w2[d, 2 * d], w2[d, 2 * d + 1] = 1, -1
+    pairs = tuple(prepared(w.half().cuda(), fmt)[0] for w in (w13, w2))
+    announce(f"moe hidden values T={T} {fmt}")
+    y = f64(moe.moe_layer(X, torch.zeros((T, 1), device="cuda"), *pairs, 1)[0])
+    x = f64(X)
+    s = x[:, :1] / (1 + np.exp(-x[:, :1]))
+    h = s * x[:, 1:1 + I]
+    want = h[:, 0::2] - h[:, 1::2]
+    bound = 4 * 2.0 ** -24 * 2 * s + np.abs(want) * (16 * 2.0 ** -24 + 2.0 ** -11) + 2.0 ** -25
+    # hidden values of 16 bits would not do
+    bf = lambda a: torch.from_numpy(a).float().bfloat16().double().numpy()  # noqa: E731
+    pair = bf(h) + bf(h - bf(h))
+    assert (np.abs(pair[:, 0::2] - pair[:, 1::2] - want) > bound).mean() > 0.3
+    assert (np.abs(y[:, :I // 2] - want) <= bound).all(), (np.abs(y[:, :I // 2] - want) / bound).max()
+    assert int(np.count_nonzero(y[:, I // 2:])) == 0
+
+
+def test_infinite_hidden_values_stay_infinite():
+    """|h| past fp32's range: an infinity of its sign in Y, not a NaN, and only for its token."""
+    D, I = 64, 32
+    w13, w2 = torch.zeros((2 * I, D)), torch.zeros((D, I))
+    w13[0, 0], w13[I, 1], w2[:, 0] = 1, 4, 1
+    X = torch.zeros((3, D))
+    X[:, 0] = 2
+    X[:, 1] = torch.tensor([1.0, 3e38, -3e38])
+    pairs = mx4.prepare_weight(w13.bfloat16().cuda(), 1), mx4.prepare_weight(w2.bfloat16().cuda(), 1)
+    y = moe.moe_layer(X.bfloat16().cuda(), torch.zeros((3, 1), device="cuda"), *pairs, 1)[0].float().cpu()
+    assert bool(torch.isfinite(y[0]).all()) and bool((y[1] == float("inf")).all()) and bool((y[2] == -float("inf")).all())
