@@ -104,9 +104,9 @@ int mx4_matmul_q(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, int
 /*
  * Y [M, N] = X W^T with X as it is, for a few tokens: 1 <= M <= 16 and M ldx < 2^30 (X is
  * read through a buffer resource). fp32 accumulation, one rounding to dtype (MX4_F16 or
- * MX4_BF16). With bf16 X the weight values enter exactly; with fp16 X a value below 2^-23
- * of the largest power of two of its row within 512 consecutive elements is off by at most
- * 2^-25 of that.
+ * MX4_BF16). The weight values enter exactly, however far apart a row's blocks are; but with
+ * fp16 X those of a block of byte 0 (below 2^-124) may count as zeros beside larger ones. A
+ * row of X with an infinity or a NaN gives infinities or NaNs.
  */
 int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype,
                            const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, void* Y,
@@ -137,7 +137,8 @@ int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int
  *                 (id -1 and weight 0 past the last chosen expert).
  *   workspace     at least moe_layer_workspace_bytes(T, I, top_k) bytes; its contents do not
  *                 matter. Calls that may run at the same time need workspaces of their own.
- * fp32 sums and hidden values; one rounding of Y. The same inputs give the same bits.
+ * fp32 sums and hidden values, weight values as in mx4_weight_only_matmul; one rounding of Y.
+ * The same inputs give the same bits.
  */
 size_t moe_layer_workspace_bytes(int64_t T, int64_t I, int64_t top_k);
 int moe_layer(const void* X, int64_t T, int64_t D, int64_t ldx, int dtype, const void* logits,

@@ -42,12 +42,6 @@ __host__ __device__ __forceinline__ int mx_quads(int64_t K) { return (mx_ks(K) +
 // every byte and code).
 __device__ __forceinline__ float mx_scale_operand(unsigned b) { return __builtin_bit_cast(float, b << 23); }
 
-// fp32 of a scale byte: 2^(b - 127), NaN for 255. Byte 0 is the subnormal 2^-127.
-__device__ __forceinline__ float mx_scale(unsigned b) {
-  const unsigned u = b == 0 ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23;
-  return __builtin_bit_cast(float, u);
-}
-
 // The 16-bit element types: F16 (X, Y fp16) and B16 (bf16).
 struct F16 {
   typedef _Float16 elem;
@@ -159,6 +153,13 @@ __device__ __forceinline__ void wave_lds_fence() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0xF | (0x7 << 4) | (0x0 << 8) | (0x3 << 14));  // lgkmcnt(0)
   asm volatile("" ::: "memory");
+}
+
+// The lane's number, worked out where it stands rather than held in a register.
+__device__ __forceinline__ int lane_again() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
 }
 
 // All loads that the wave has asked for are here.

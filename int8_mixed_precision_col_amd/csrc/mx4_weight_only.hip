@@ -32,6 +32,7 @@ __global__ __launch_bounds__(64 * kMxWoWaves, wo_waves(ROWS)) void k_mx_weight_o
   // elements past K are out of the resource's range and read zeros
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.M - 1) * a.ldx + a.K) * 2));
   const int M = a.M, mrow = min(row, M - 1);  // rows past M repeat the last (outputs discarded)
+  __builtin_assume(M >= 1 && M <= ROWS);      // the first rows' loads need no test
   // With one row group the wave's next quad is on its way while this one is multiplied (16 x
   // 4096 x 4096 5.4 -> 5.1 us); with more the registers it takes cost more than it gives (16 x
   // 8192 x 8192, two groups: 10.5 -> 11.7 us).
@@ -40,7 +41,8 @@ __global__ __launch_bounds__(64 * kMxWoWaves, wo_waves(ROWS)) void k_mx_weight_o
   WeightQuad<true> w[RG], next[AHEAD ? RG : 1];
   ActQuad<true, ROWS> x;
   auto load_x = [&](int q) {
-    x.load(xr, q, a.K, M, lane, [&](int i) { return static_cast<unsigned>(i * a.ldx) * 2u; });
+    // the lane made anew: offsets kept from quad to quad would take the registers that fp16 with 2 rows lacks
+    x.load(xr, q, a.K, M, lane_again(), [&](int i) { return static_cast<unsigned>(i * a.ldx) * 2u; });
   };
   auto load_w = [&](auto& to, int q) {
 #pragma unroll

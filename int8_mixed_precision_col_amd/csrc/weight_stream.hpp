@@ -12,9 +12,11 @@
 //
 // int8 codes are exact in fp16 and bf16. MX4 values are exact in bf16 (2 significant bits,
 // the same exponent range). In fp16 a block's power of two may not fit, so each quad is
-// multiplied relative to its row's largest block scale and the fp32 sum is scaled back: a
-// value is then inexact only where it is below 2^-23 of the largest power of two of its
-// row's quad, off by at most 2^-25 of that.
+// multiplied relative to its row's largest block scale, 2^13 for it, and the fp32 sum is scaled
+// back. That holds the blocks down to 2^-26 of the largest, as normal numbers; where a row of the
+// wave has one below that (trained weights have none, but for blocks of zeros), the quad is gone
+// over again for the largest of those. Blocks of byte 0, below 2^-124, are left out of that: no
+// fp16 sum can show them beside larger ones.
 #pragma once
 
 #include "mx4.hpp"
@@ -122,6 +124,64 @@ __device__ __forceinline__ v4u act_operand(const char* buf, int stride, int row,
                                        2 * (UK * (j % PER) + KL * (lane >> 4) + 8 * v));
 }
 
+// The power of two of a row's largest block in fp16 (6 times it is below fp16's largest value) and
+// how many below it are still normal numbers with their smallest code, 0.5.
+constexpr int kMxTop = 13, kMxWindow = kMxTop + 14 - 1;
+
+// The smallest byte of s that is not 0, less 1 (65535 if all are 0).
+__device__ __forceinline__ unsigned mx_least_byte(unsigned s) {
+  typedef unsigned short v2s __attribute__((ext_vector_type(2)));
+  const v2s one = {1, 1};
+  const v2s a = __builtin_bit_cast(v2s, s & 0x00ff00ffu) - one, b = __builtin_bit_cast(v2s, (s >> 8) & 0x00ff00ffu) - one;
+  const v2s m = __builtin_elementwise_min(a, b);
+  return min(static_cast<unsigned>(m[0]), static_cast<unsigned>(m[1]));
+}
+// The largest byte of s that is more than kMxWindow below ref (0 if none is).
+__device__ __forceinline__ unsigned mx_next_byte(unsigned s, int ref) {
+  int most = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int b = static_cast<int>((s >> (8 * j)) & 255u);
+    if (b + kMxWindow < ref) most = max(most, b);
+  }
+  return static_cast<unsigned>(most);
+}
+
+// What a sum of products relative to block byte ref is multiplied by: NaN for 255, which makes the
+// row's outputs NaN whatever else they add up.
+__device__ __forceinline__ float mx_back(int ref) {
+  return ref == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, ref - 127 - kMxTop);
+}
+
+// acc += X_quad W_quad^T in fp16, the blocks by windows of powers of two: of what is left in each row
+// (lane l: l % 16) the largest one, ref, and kMxWindow below it. Hardly ever run, and kept small.
+template <class T, class X>
+__device__ __forceinline__ void mma_quad_spread(const WeightQuad<true>& w, v4f& acc, int ref, X x) {
+  for (;;) {
+    v4f part = {};
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const int j = i >> 2, v = i & 3;
+      v4u unit = w.w[0];
+#pragma unroll
+      for (int u = 1; u < 4; ++u)
+        if (j == u) unit = w.w[u];
+      const unsigned codes = v < 2 ? (v ? unit[1] : unit[0]) : (v == 2 ? unit[2] : unit[3]);
+      const unsigned b = (w.s >> (8 * j)) & 255u, below = static_cast<unsigned>(ref) - b;
+      // 2^-126, so zeros in fp16, for blocks above ref or below the window
+      const float s = mx_scale_operand(below <= kMxWindow ? 127 + kMxTop - below : 1u);
+      part = T::mfma(x(j, v), mx_values8<T>(codes, s), part);
+    }
+    const float back = mx_back(ref);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = ref < 0 ? acc[e] : __builtin_fmaf(part[e], back, acc[e]);
+    // each turn takes ref down by more than the window; -1: nothing is left of the row
+    const int next = static_cast<int>(max_over_groups(mx_next_byte(w.s, ref)));
+    ref = next > 0 ? next : -1;
+    if (__ballot(ref >= 0) == 0) break;
+  }
+}
+
 // acc[r] += X_quad W_quad[r]^T for RG row groups of the weight that share the activations
 // x(j, v): 16-byte part v of unit j (the int8 column constants are left to the caller).
 // J0, J1: of units J0 .. J1 - 1 alone (MX4 in fp16: all four, its reference is theirs).
@@ -140,44 +200,54 @@ __device__ __forceinline__ void mma_quad(const WeightQuad<MX> (&w)[RG], v4f (&ac
         acc[r] = T::mfma(x1, v4u{h2[0], h2[1], h3[0], h3[1]}, acc[r]);
       }
     }
-  } else {
-    unsigned ref[RG];
-    v4f part[RG];
-#pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      if constexpr (!T::bf) {
-        const unsigned t = pk_max_u16(w[r].s & 0x00ff00ffu, (w[r].s >> 8) & 0x00ff00ffu);
-        ref[r] = max_over_groups(max(t & 0xffffu, t >> 16));
-        part[r] = v4f{};
-      } else {
-        part[r] = acc[r];
-      }
-    }
+  } else if constexpr (T::bf) {
 #pragma unroll
     for (int j = J0; j < J1; ++j) {
       float s[RG];
 #pragma unroll
-      for (int r = 0; r < RG; ++r) {
-        const unsigned b = (w[r].s >> (8 * j)) & 255u;
-        // fp16: 2^(b - ref), at least the smallest normal; NaN for a NaN block
-        s[r] = mx_scale_operand(T::bf || b == 255u ? b : static_cast<unsigned>(max(static_cast<int>(127 + b - ref[r]), 1)));
-      }
+      for (int r = 0; r < RG; ++r) s[r] = mx_scale_operand((w[r].s >> (8 * j)) & 255u);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const v4u xv = x(j, v);
 #pragma unroll
-        for (int r = 0; r < RG; ++r) part[r] = T::mfma(xv, mx_values8<T>(w[r].w[j][v], s[r]), part[r]);
+        for (int r = 0; r < RG; ++r) acc[r] = T::mfma(xv, mx_values8<T>(w[r].w[j][v], s[r]), acc[r]);
       }
     }
+  } else {
+    int ref[RG];  // byte of the largest block of lane l's row (l % 16)
+    bool spread = false;
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
-      if constexpr (!T::bf) {
-        const float back = mx_scale(ref[r]);
+      const unsigned t = pk_max_u16(w[r].s & 0x00ff00ffu, (w[r].s >> 8) & 0x00ff00ffu);
+      ref[r] = static_cast<int>(max_over_groups(max(t & 0xffffu, t >> 16)));
+      spread |= static_cast<int>(mx_least_byte(w[r].s)) + 1 + kMxWindow < ref[r];
+    }
+    if (__builtin_expect(__ballot(spread) == 0, 1)) {
+      v4f part[RG] = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float s[RG];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          const int b = static_cast<int>((w[r].s >> (8 * j)) & 255u);
+          s[r] = mx_scale_operand(static_cast<unsigned>(max(127 + kMxTop + b - ref[r], 1)));
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const v4u xv = x(j, v);
+#pragma unroll
+          for (int r = 0; r < RG; ++r) part[r] = T::mfma(xv, mx_values8<T>(w[r].w[j][v], s[r]), part[r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        const float back = mx_back(ref[r]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[r][e] = __builtin_fmaf(part[r][e], back, acc[r][e]);
-      } else {
-        acc[r] = part[r];
       }
+    } else {
+#pragma unroll
+      for (int r = 0; r < RG; ++r) mma_quad_spread<T>(w[r], acc[r], ref[r], x);
     }
   }
 }

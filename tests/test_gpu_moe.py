@@ -307,3 +307,18 @@ def test_infinite_hidden_values_stay_infinite():
     pairs = mx4.prepare_weight(w13.bfloat16().cuda(), 1), mx4.prepare_weight(w2.bfloat16().cuda(), 1)
     y = moe.moe_layer(X.bfloat16().cuda(), torch.zeros((3, 1), device="cuda"), *pairs, 1)[0].float().cpu()
     assert bool(torch.isfinite(y[0]).all()) and bool((y[1] == float("inf")).all()) and bool((y[2] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("T,D,I,E,k", [(1, 528, 32, 4, 2), (6, 1040, 48, 6, 3), (16, 4224, 32, 3, 2)])
+def test_mx4_blocks_far_below_others(T, D, I, E, k, dtype):
+    """Gate and up rows whose blocks lie up to 2^80 apart, X zero where they are largest: the
+    oracle's bound, which knows no loss, holds. X in LDS and read by the waves."""
+    from tests.test_gpu_mx4 import spread_weight
+    announce(f"moe spread blocks T={T} D={D} I={I} E={E} {dtype}")
+    X, logits, pairs, values = case(T, D, I, E, dtype, "mx4", T + D)
+    W, wv, far = spread_weight(E * 2 * I, D, T + D, 80)
+    X[:, far] = 0
+    wv = wv.reshape(E, 2 * I, D)
+    assert np.abs(np.einsum("eid,td->tei", wv, f64(X))).max() < 2000
+    check(X, logits, (W, pairs[1]), (wv, values[1]), k, True)

@@ -354,3 +354,66 @@ def test_quantize_once_for_three_weights():
         wv = mx4.dequantize(*W, w.shape[0], 1040, F32)
         a, b = f64(xv), f64(wv)
         check_sum(mx4.matmul_q(*q, 77, 1040, *W, dtype=B16), a @ b.T, np.abs(a) @ np.abs(b).T, B16, 9 + 32)
+
+
+def spread_weight(N, K, seed, at_most):
+    """Tiled pair and values of N rows whose blocks' powers of two lie up to 2^at_most apart: in
+    every 512 elements a few blocks far above the others (row n: by n % at_most), and the others
+    24 bits apart. Also the columns of the far blocks."""
+    g = torch.Generator().manual_seed(seed)
+    nb = (K + 31) // 32
+    packed = torch.randint(0, 256, (N, 16 * nb), generator=g, dtype=torch.uint8)
+    if K % 32:
+        packed[:, -8:] = 0
+    scales = torch.randint(100, 124, (N, nb), generator=g)
+    far = torch.rand((nb,), generator=g) < 0.25
+    far[0] = True
+    scales[:, far] = 123 + (torch.arange(N) % at_most)[:, None]
+    scales = scales.to(torch.uint8)
+    codes = np.stack((packed.numpy() & 15, packed.numpy() >> 4), -1).reshape(N, -1)[:, :K]
+    return mx4.tile_weight(packed.cuda(), scales.cuda(), K), ref.mx4_values(codes, scales.numpy()), \
+        far.repeat_interleave(32)[:K]
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("M,K,N", [(1, 528, 128), (4, 1040, 128), (16, 2064, 112), (12, 1040, 4208), (16, 528, 16496)])
+def test_weight_only_small_blocks_beside_far_larger_ones(M, K, N, dtype):
+    """X is zero where the weight is largest, so that what is left of every sum comes from blocks
+    far below: nothing of them is lost. (A block more than 26 powers of two below the
+    largest one left takes another pass; each pass over 512 elements is one more rounding.)"""
+    announce(f"mx4.weight_only_matmul spread blocks {M}x{K}x{N} {dtype}")
+    W, wv, far = spread_weight(N, K, K + N, 100)
+    x = rows(M, K, dtype, M, 2)
+    x[:, far] = 0
+    xv = f64(x)
+    want, S = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    assert np.abs(want).max() < 30000 and (np.abs(want) > 2.0 ** -14).mean() > 0.95
+    check_sum(mx4.weight_only_matmul(x, *W), want, S, dtype, K // 4 + 32 + 10 * -(-K // 512))
+
+
+def test_weight_only_subnormal_activations():
+    """fp16 X down to its smallest values against weights that bring the sums back."""
+    M, K, N = 5, 1040, 48
+    x, w = rows(M, K, F16, 1, 2).float() * 2.0 ** -20, rows(N, K, B16, 2, 2) * 2.0 ** 16
+    x = x.half()
+    assert int(((x.abs() < 2.0 ** -14) & (x != 0)).sum()) > K
+    W, wv, xv = mx4.prepare_weight(w, 1), ref.mx4_round(f64(w)), f64(x)
+    want = xv @ wv.T
+    announce("mx4.weight_only_matmul subnormal X")
+    check_sum(mx4.weight_only_matmul(x, *W), want, np.abs(xv) @ np.abs(wv).T, F16, K // 4 + 32)
+
+
+def test_weight_only_nan_blocks_and_values_beside_spread_blocks():
+    """NaN blocks, and an infinity or a NaN in X, in rows that take several passes."""
+    M, K, N = 6, 1040, 64
+    W, wv, far = spread_weight(N, K, 3, 60)
+    x = rows(M, K, F16, 4, 2)
+    x[:, far] = 0
+    near = int((~far).nonzero()[3])
+    x[1, near], x[4, near] = float("inf"), float("nan")
+    W[1].view(-1)[:4] = 255                    # feature 0, block 0 of the first four units
+    announce("mx4.weight_only_matmul spread blocks, not finite")
+    y = mx4.weight_only_matmul(x, *W).cpu()
+    assert bool(torch.isnan(y[:, 0]).all())
+    assert torch.isfinite(y[:, 1:]).all(1).tolist() == [True, False, True, True, False, True]
+    assert not torch.isfinite(y[1]).any() and bool(torch.isnan(y[4]).all())
