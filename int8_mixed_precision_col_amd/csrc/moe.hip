@@ -188,10 +188,12 @@ __host__ __device__ __forceinline__ bool up_resident(int T, int quads) {
   return quads * act_bytes<MX>(T) <= kUpResident;
 }
 
-// Workgroups of k_moe_gate_up: one per CU. Two where they fit (int8 takes 126 registers) and a step is long, D of 15 quads (3.6 K) and more: 1 / 2 / 4 tokens, 8 of 64 experts of
-// 4096 x 1280, 36.7 -> 36.4, 53 -> 49 and 85 -> 81 us; but of 2048 x 768 19.3 -> 20.4, 26.5 -> 26.8 and
-// 41.2 -> 41.7, and 4 of 60 of 3328 x 1280 23.4 -> 23.4, 30.8 -> 31.8 and 47.0 -> 48.6.
-constexpr int kMoeBlocks = 256, kUpLongQuads = 15;
+// Workgroups of k_moe_gate_up: one per CU. Two for each (they fit with int8 weights and X in LDS, in
+// 126 registers) gain nothing that a rule could go by: of 8 of 64 experts with I = 768 / 1280, one
+// against two, 2 tokens of D = 2048 24.8 / 25.8, 39.5 / 40.3 us, 3328 33.6 / 33.4, 47.8 / 48.5, 4096
+// 36.0 / 35.4, 53.9 / 50.3, 5120 49.0 / 49.8, 73.1 / 76.6, 7168 56.4 / 56.5, 88.0 / 83.1; 4 tokens of
+// 4096 53.3 / 49.9, 84.3 / 80.8, 5120 74.3 / 78.1, 108.8 / 107.6.
+constexpr int kMoeBlocks = 256;
 
 // What k_moe_gate_up leaves for k_moe_down (with the hidden values), and what its workgroups
 // leave for each other.
@@ -210,12 +212,12 @@ struct MoeLists {
 // 167; of 2048 x 768, int8 87 / 81 / 77, 4 tokens 45 / 42 / 44, 1 token 21.7 / 20.2 / 23.2; 1
 // token of 4096 x 1280, MX4 28 / 28 / 25. (One: 102, 179, 82, 40, 28.8 and 31.)
 template <bool MX>
-__device__ __forceinline__ int up_share(int experts, int groups, int quads, int blocks) {
+__device__ __forceinline__ int up_share(int experts, int groups, int quads) {
   const int most = quads >= 5 ? 8 : quads >= 3 ? 4 : MX ? quads : 2;  // int8: at most four groups at once
   int best = most, least = 0x7fffffff;
   for (int share = most; share >= 2 || share == most; share >>= 1) {
     const int par = kUpWaves / share, steps = experts * ((groups + par - 1) / par);
-    const int cost = (steps + blocks - 1) / blocks * (1 + (quads + share - 1) / share);
+    const int cost = (steps + kMoeBlocks - 1) / kMoeBlocks * (1 + (quads + share - 1) / share);
     if (cost < least) {
       least = cost;
       best = share;
@@ -229,7 +231,7 @@ __device__ __forceinline__ int up_share(int experts, int groups, int quads, int 
 // 8 KB than in 37 (1 token, 8 of 64 experts of 2048 x 768, int8 20.9 -> 19.2 us; 8 tokens of 4096 x
 // 1280, MX4, 79 -> 73 us).
 template <class T, bool MX, int V, int NT, bool RES>
-__global__ __launch_bounds__(64 * kUpWaves, !MX && RES ? 4 : 2) void k_moe_gate_up(MoeArgs a, MoeLists lists) {
+__global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_gate_up(MoeArgs a, MoeLists lists) {
   extern __shared__ __attribute__((aligned(16))) char s_x[];  // [quads or waves][act_bytes(T)]
   __shared__ MoeTable table;
   __shared__ float red[kUpWaves][2][16][17];
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(64 * kUpWaves, !MX && RES ? 4 : 2) void k_moe_gate_
 
   // A step is `par` neighbouring 16-feature groups of one expert, `share` waves on the quads
   // of each.
-  const int share = up_share<MX>(order.count(), groups, quads, gridDim.x > kMoeBlocks ? 2 * kMoeBlocks : kMoeBlocks);
+  const int share = up_share<MX>(order.count(), groups, quads);
   const int par = kUpWaves / share;
   const int steps = (groups + par - 1) / par;
   // steps [first, last) of the list are this workgroup's
@@ -592,9 +594,8 @@ static hipError_t run_up(const MoeArgs& a, const MoeLists& lists, hipStream_t s)
   constexpr size_t kStatic = sizeof(MoeTable) + sizeof(float) * (kUpWaves * 2 * 16 * 17 + 128);
   static_assert(kUpResident + kStatic <= kMaxLds && kUpWaves * act_bytes<MX>(kMoeMaxTokens) + kStatic <= kMaxLds,
                 "k_moe_gate_up's LDS");
-  const bool two = !MX && quads >= kUpLongQuads && 2 * (lds + kStatic) <= kMaxLds;
-  const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16), most = two ? 2 * kMoeBlocks : kMoeBlocks;
-  const unsigned blocks = static_cast<unsigned>(steps < most ? steps : most);
+  const int64_t steps = static_cast<int64_t>(n_slots) * (a.I / 16);
+  const unsigned blocks = static_cast<unsigned>(steps < kMoeBlocks ? steps : kMoeBlocks);
   hipLaunchKernelGGL((k_moe_gate_up<T, MX, V, NT, RES>), dim3(blocks), dim3(64 * kUpWaves), lds, s, a, lists);
   return hipGetLastError();
 }
