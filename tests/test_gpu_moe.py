@@ -322,3 +322,74 @@ def test_mx4_blocks_far_below_others(T, D, I, E, k, dtype):
     wv = wv.reshape(E, 2 * I, D)
     assert np.abs(np.einsum("eid,td->tei", wv, f64(X))).max() < 2000
     check(X, logits, (W, pairs[1]), (wv, values[1]), k, True)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mx4"])
+def test_most_experts_and_longest_lists(fmt):
+    """16 tokens of 16 experts each out of 512: 256 list entries, nearly as many experts."""
+    T, D, I, E, k = 16, 48, 16, 512, 16
+    announce(f"moe T={T} E={E} k={k} {fmt}")
+    X, logits, pairs, values = case(T, D, I, E, F16, fmt, 21)
+    check(X, logits, pairs, values, k, True)
+    logits[:] = -float("inf")
+    logits[torch.arange(T).repeat_interleave(k), torch.arange(T * k) * 2 + 1] = 1.0  # every expert has one token
+    check(X, logits, pairs, values, k, False)
+
+
+def test_lists_are_optional_in_the_c_call():
+    X, logits, pairs, _ = case(5, 272, 80, 8, F16, "mx4", 22)
+    lg = logits.cuda()
+    want = moe.moe_layer(X, lg, *pairs, 2)[0]
+    y = torch.zeros_like(X)
+    work = torch.empty(moe.workspace_bytes(5, 80, 2), dtype=torch.uint8, device="cuda")
+    announce("moe_layer without lists")
+    mx4._launch("moe_layer", X, X.data_ptr(), 5, 272, 272, 0, lg.data_ptr(), 8, 2, 2, 1, 1, pairs[0][0].data_ptr(),
+                pairs[0][1].data_ptr(), pairs[1][0].data_ptr(), pairs[1][1].data_ptr(), 80, y.data_ptr(), None, None,
+                work.data_ptr(), work.numel())
+    assert torch.equal(y, want)
+
+
+def test_on_a_stream_of_its_own_behind_the_inputs():
+    """Captured twice in one graph beside an MX4 product that shares no buffer; replayed with eager
+    calls of both between the replays."""
+    X, logits, pairs, _ = case(9, 528, 144, 12, B16, "mx4", 23)
+    lg = logits.cuda()
+    W = mx4.prepare_weight((torch.randn((272, 528), generator=torch.Generator().manual_seed(1)) * 0.05).to(B16).cuda(), 1)
+
+    def step(x):
+        y = moe.moe_layer(x, lg, *pairs, 3)[0]
+        return y, mx4.matmul(moe.moe_layer(y, lg, *pairs, 3)[0], *W)
+    want = step(X)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(X)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(X)
+    for _ in range(4):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        eager = step(X)
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want, eager):
+            assert torch.equal(a, b) and torch.equal(c, b)
+
+
+def test_one_experts_rows_are_a_weight_of_their_own():
+    """What a prompt of more than 16 tokens uses: the products on one expert's slice of the prepared
+    weights, both formats, as on the expert prepared alone."""
+    E, I, D, e = 4, 48, 272, 2
+    g = torch.Generator().manual_seed(31)
+    w13 = (torch.randn((E * 2 * I, D), generator=g) * 0.05).half().cuda()
+    X = torch.randn((40, D), generator=g).half().cuda()
+    part = slice(e * 2 * I // 16, (e + 1) * 2 * I // 16)
+    announce("one expert's slice")
+    rows_ = w13[e * 2 * I:(e + 1) * 2 * I].contiguous()
+    codes, scales = mx4.prepare_weight(w13, 1)
+    assert torch.equal(mx4.matmul(X, codes[part], scales[part]), mx4.matmul(X, *mx4.prepare_weight(rows_, 1)))
+    Wq, aw = binding.prepare_weight(w13, 1)
+    assert torch.equal(binding.mixed_matmul(X, Wq[part], aw[e * 2 * I:(e + 1) * 2 * I]),
+                       binding.mixed_matmul(X, *binding.prepare_weight(rows_, 1)))

@@ -417,3 +417,27 @@ def test_weight_only_nan_blocks_and_values_beside_spread_blocks():
     assert bool(torch.isnan(y[:, 0]).all())
     assert torch.isfinite(y[:, 1:]).all(1).tolist() == [True, False, True, True, False, True]
     assert not torch.isfinite(y[1]).any() and bool(torch.isnan(y[4]).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 1040, 144), (16, 528, 48), (30, 1040, 272), (64, 2064, 144), (200, 1040, 272),
+                                   (70, 8208, 144)])
+def test_matmul_of_opposite_scales(M, K, N):
+    """Blocks from 2^-100 to 2^100 against blocks that bring the products back: neither scale is
+    applied alone. And both at an end: zeros, or infinities."""
+    announce(f"mx4.matmul opposite scales {M}x{K}x{N}")
+    g = torch.Generator().manual_seed(K)
+    x, w = rows(M, K, B16, M, 1), rows(N, K, B16, N, 1)
+    e = torch.randint(-100, 101, (K // 16 + 1,), generator=g).repeat_interleave(32)[:K].cuda()
+    x, w = x * torch.exp2(e.float()).to(B16), w * torch.exp2(-e.float()).to(B16)
+    xv, wv = ref.mx4_round(f64(x)), ref.mx4_round(f64(w))
+    W = mx4.prepare_weight(w, 1)
+    want, S = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    check_sum(mx4.matmul(x, *W), want, S, B16, -(-K // 128) + 32)
+    check_sum(mx4.matmul_q(*mx4.quantize(x), M, K, *W, dtype=B16), want, S, B16, -(-K // 128) + 32)
+    if M <= 16:
+        check_sum(mx4.weight_only_matmul(x, *W), f64(x) @ wv.T, np.abs(f64(x)) @ np.abs(wv).T, B16, K // 4 + 32)
+    one = torch.ones((M, K), dtype=B16, device="cuda")
+    for s in (-120, 120):
+        v = one * 2.0 ** s
+        y = mx4.matmul(v, *mx4.prepare_weight(v[:1].expand(N, K).contiguous(), 1)).float()
+        assert bool((y == (0.0 if s < 0 else float("inf"))).all())
