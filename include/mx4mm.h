@@ -135,6 +135,10 @@ int mx4_weight_only_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int
  *   Y             out, [T, D] contiguous, dtype.
  *   ids, weights  out, nullable: int32 and fp32 [T, top_k], the lists in descending order
  *                 (id -1 and weight 0 past the last chosen expert).
+ *                 One expert's row groups are a prepared weight by themselves (2 I and D are
+ *                 multiples of 16): more than 16 tokens go through here 16 at a time, or, a
+ *                 prompt's, through the products (mx4_matmul, int8_mixed_matmul) expert by
+ *                 expert on the rows of X that chose it.
  *   workspace     at least moe_layer_workspace_bytes(T, I, top_k) bytes; its contents do not
  *                 matter. Calls that may run at the same time need workspaces of their own.
  * fp32 sums and hidden values, weight values as in mx4_weight_only_matmul; one rounding of Y.

@@ -25,8 +25,8 @@
 // and third parts, and the three sums are added in the end.
 //
 // Measured (us per layer in graphs over rotated weights; bytes of the chosen experts over that
-// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 152 us, 5.7 TB/s, MX4 94.5 us, 5.0 TB/s;
-// of 2048 x 768 61 and 46 us; 1 token of these 18.6 and 14.8 us, of which 7.5 and 4.0 us are the
+// time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 165 us, 5.4 TB/s, MX4 102 us, 4.6 TB/s;
+// of 2048 x 768 65 and 49.5 us; 1 token of these 17.9 and 15.0 us, of which 7.5 and 4.0 us are the
 // bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
@@ -208,9 +208,10 @@ struct MoeLists {
 // and about as much again for the sums' exchange and the hidden values, so the fewest of
 // steps x (1 + turns). Few sharers exchange little and give each wave loads to have in flight
 // over a step's end; many leave fewer features to the last step. Measured, us per layer at 8 /
-// 4 / 2 sharers: 16 tokens, 8 of 64 experts of 4096 x 1280, MX4 116 / 100 / 97, int8 172 / 162 /
-// 167; of 2048 x 768, int8 87 / 81 / 77, 4 tokens 45 / 42 / 44, 1 token 21.7 / 20.2 / 23.2; 1
-// token of 4096 x 1280, MX4 28 / 28 / 25. (One: 102, 179, 82, 40, 28.8 and 31.)
+// 4 / 2 sharers: 16 tokens, 8 of 64 experts of 4096 x 1280, MX4 116 / 104 / 106, int8 171 / 171 /
+// 171 (chosen by cost 167); of 2048 x 768, int8 70 / 65.5 / 64.6, 4 tokens 39.7 / 37.6 / 38.7, 1 token
+// 19.8 / 18.6 / 21.4; 1 token of 4096 x 1280, MX4 26.1 / 25.7 / 24.1. (One, with the hidden values in two
+// parts: 102 and 179 for the first two, where two sharers took 97 and 167.)
 template <bool MX>
 __device__ __forceinline__ int up_share(int experts, int groups, int quads) {
   const int most = quads >= 5 ? 8 : quads >= 3 ? 4 : MX ? quads : 2;  // int8: at most four groups at once
@@ -601,12 +602,13 @@ static hipError_t run_up(const MoeArgs& a, const MoeLists& lists, hipStream_t s)
 }
 
 // Workgroups that share 16 features of Y: few features leave CUs idle, the more items of a wave
-// the longer, and the exchange costs 3 to 5 us. int8, at least three items per wave saved (by
-// the most passes that the lists can have): 8 of 64 experts of 2048 x 768, 4 / 8 / 16 tokens 40.8 ->
-// 37.7, 58.0 -> 54.0, 73.6 -> 64.6 us; 4 of 60 of 2048 x 1408, 16 tokens 88.3 -> 76.7; 2 of 16 of
-// 512 x 2048, four workgroups, 4 / 16 tokens 20.8 -> 17.6, 35.6 -> 25.8; with fewer, 2 tokens of 2048
-// x 768 25.7 -> 26.7. An MX4 item is half as long: 16 tokens 48.0 -> 46.2, 49.4 -> 50.8, 8 tokens
-// 38.3 -> 37.2, 38.6 -> 41.6: not worth it.
+// the longer; the exchange costs 1 us and about another per 64 workgroups. int8, at least three items per
+// wave saved (by the most passes that the lists can have). One workgroup against the split taken: 8 of 64
+// experts of 2048 x 768, 4 / 8 / 16 tokens 37.7 / 37.3, 51.8 / 48.0, 68.3 / 63.4 us; 4 of 60 of 2048 x 1408, 16
+// tokens 89.5 / 78.5; 2 of 16 of 512 x 2048, four workgroups, 4 / 16 tokens 19.3 / 17.2, 34.0 / 24.4, but 8 tokens
+// of 1024 x 1024 19.9 / 22.1; with fewer saved, 2 tokens of 2048 x 768 24.8 / 26.8. Over 125 layers of 256 to
+// 2048 features the choice is 0.7% from the best of one, two and four. An MX4 item is half as long (with hidden
+// values in two parts): 16 tokens 48.0 / 46.2, 49.4 / 50.8, 8 tokens 38.3 / 37.2, 38.6 / 41.6: not worth it.
 static int down_parts(const MoeArgs& a, int quads) {
   const int parts = a.D <= 16 * kMoeBlocks / 4 ? 4 : a.D <= 16 * kMoeBlocks / 2 ? 2 : 1;
   const int n = a.T * a.k, most = a.E + n / kDownTokens, passes = n < most ? n : most;

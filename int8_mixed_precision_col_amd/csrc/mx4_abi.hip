@@ -11,7 +11,7 @@ namespace {
 constexpr int64_t kMaxK = int64_t(1) << 20;
 constexpr int64_t kMaxInt8K = 133144;  // the int8 operators' own limit
 constexpr int64_t kMaxMN = int64_t(1) << 24;
-constexpr int64_t kMaxElements = int64_t(1) << 36;  // grid sizes stay below 2^31 threads
+constexpr int64_t kMaxElements = int64_t(1) << 36;  // grids stay below 2^32 threads (quantizing 2^24 x 4096: 2^31)
 constexpr int64_t kMaxFew = 16;
 constexpr int64_t kMaxBuffer = int64_t(1) << 30;    // elements behind a buffer resource
 

@@ -8,7 +8,8 @@
 // With few enough rows X is quantized on the way and the call is one launch: a wave loads a
 // row's whole quad at once (1 KB, a lane holds 8 elements and four lanes a block), and the codes
 // and scale bytes go through LDS into operand order. Loading 16-bit X in operand order instead
-// takes 16 gathers per quad whatever the number of rows (8 x 4096 x 4096: 6.7 against 4.4 us).
+// takes 16 gathers per quad whatever the number of rows (8 x 4096 x 4096: 6.7 us; rows through LDS took it
+// to 4.9, and more workgroups per CU to 4.4).
 #include "mx4.hpp"
 #include "mx4_launch.hpp"
 
@@ -167,8 +168,10 @@ static hipError_t run(const MxGemmArgs& a, const void* X, int64_t ldx, int type,
   return hipGetLastError();
 }
 
-// Row groups per workgroup where one workgroup fills a CU, by its registers or by the work on X
-// that each repeats: as many as make one round of workgroups, up to 4. Measured per call (HIP
+// Row groups per workgroup where each workgroup does much over again that all do (quantizing X, or
+// reading 64 rows of it): as many as make one round of workgroups over the CUs, up to 4, although with one
+// group two fit a CU (X quantized by each wave for its own quads: 113 registers and 35 KB; two and
+// four groups, 136 and 185 registers, one). Measured per call (HIP
 // graphs over rotated weights, fp16, K x N, RG = 1 / 2 / 4): M = 16, X quantized on the way, 4096 x
 // 4096 6.3 / 6.2 / 7.7 us, 4096 x 6144 8.5 / 6.8 / 7.9, 8192 x 8192 14.8 / 11.5 / 13.2, 4096 x
 // 10240 11.6 / 11.3 / 8.6, 12288 x 12288 28.9 / 25.5 / 20.1; M = 64, X tiled, 4096 x 4096 6.2 /

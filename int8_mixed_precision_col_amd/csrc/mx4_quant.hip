@@ -108,7 +108,9 @@ hipError_t launch_mx_quantize_cols(const void* W, int K, int N, int type, uint8_
 }
 
 // Row-major packed codes and scale bytes -> the tiled layout; same lane mapping as
-// k_mx_quantize. Codes past K (the second half of a last, half-full block) become 0.
+// k_mx_quantize. Codes past K (the second half of a last, half-full block) become 0. Once per
+// checkpoint weight: 12288 x 49152 (K x N) 171 us, 3.7 TB/s read and written, 4096 x 16384 20.7, 4096 x
+// 4096 6.0 (a large copy: 4.9 TB/s; a lane moves 4 bytes at a time).
 __global__ __launch_bounds__(256) void k_mx_tile(const uint8_t* packed, const uint8_t* bytes, int K,
                                                  uint8_t* codes, uint32_t* scales) {
   const int lane = threadIdx.x & 63, r = 4 * (threadIdx.x >> 6) + (lane >> 4), c = lane & 15;

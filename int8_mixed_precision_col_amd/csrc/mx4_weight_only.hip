@@ -29,7 +29,7 @@ __global__ __launch_bounds__(64 * kMxWoWaves, wo_waves(ROWS)) void k_mx_weight_o
   const int ks = mx_ks(a.K), quads = mx_quads(a.K), groups = a.N / 16;
   const int g0 = blockIdx.x * RG;
   char* buf = s_x + wave * act_bytes<true>(a.M);
-  // elements past K are out of the resource's range and read zeros
+  // what ActQuad leaves out, elements past K among it, is out of the resource's range and reads zeros
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, static_cast<unsigned>(((a.M - 1) * a.ldx + a.K) * 2));
   const int M = a.M, mrow = min(row, M - 1);  // rows past M repeat the last (outputs discarded)
   __builtin_assume(M >= 1 && M <= ROWS);      // the first rows' loads need no test

@@ -51,6 +51,10 @@ def moe_layer(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple
     format. Lists are in descending order of the logits, ties to the lower index; past the
     last expert that is on, id is -1 and weight 0. renormalize: weights sum to 1 over the
     chosen experts, otherwise they are the softmax over all of them.
+
+    More than 16 tokens: 16 at a time, or, for a prompt, each expert's tokens through ``mx4.matmul``
+    or ``binding.mixed_matmul`` on its part of the prepared weights (of gate_up the row groups
+    e * 2 I / 16 up to (e + 1) * 2 I / 16 of codes and scales; int8 constants by row).
     """
     T, D, ld, dt = mx4._need_rows(X, "X")
     if not isinstance(logits, torch.Tensor) or logits.dtype not in mx4.DTYPES or logits.dim() != 2:
