@@ -28,6 +28,7 @@
 // time): 16 tokens, 8 of 64 experts of 4096 x 1280, int8 165 us, 5.4 TB/s, MX4 102 us, 4.6 TB/s;
 // of 2048 x 768 65 and 49.5 us; 1 token of these 17.9 and 15.0 us, of which 7.5 and 4.0 us are the
 // bytes at 5 TB/s and the rest two chains of launch, routing or tables, first loads and join.
+#include "moe_keys.hpp"
 #include "mx4_launch.hpp"
 #include "weight_stream.hpp"
 
@@ -35,26 +36,6 @@ namespace i8mm {
 
 constexpr int kMoeMaxLists = kMoeMaxTokens * kMoeMaxTopK;
 constexpr int kMoeExpertWords = kMoeMaxExperts / 32;
-
-__device__ __forceinline__ float moe_logit(const void* p, int type, int64_t i) {
-  if (type == kMxF32) return static_cast<const float*>(p)[i];
-  if (type == kMxF16) return static_cast<float>(static_cast<const _Float16*>(p)[i]);
-  return static_cast<float>(static_cast<const __bf16*>(p)[i]);
-}
-
-// Order-preserving map of fp32 to unsigned: -inf to 0 (an expert that is off), any NaN to
-// the greatest.
-__device__ __forceinline__ unsigned moe_key(float v) {
-  const unsigned b = __builtin_bit_cast(unsigned, v);
-  if (v != v) return 0xffffffffu;
-  if (b == 0xff800000u) return 0u;
-  const unsigned z = b == 0x80000000u ? 0u : b;  // -0 ties with +0
-  return z ^ (z >> 31 ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float moe_unkey(unsigned k) {
-  if (k == 0xffffffffu) return __builtin_nanf("");
-  return __builtin_bit_cast(float, k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
-}
 
 // The chosen experts of all tokens, in LDS: a bit per expert that some token chose, and per
 // expert the mask of its tokens and its place in each one's list. The experts are used in

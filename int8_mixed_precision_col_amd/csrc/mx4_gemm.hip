@@ -16,124 +16,11 @@
 //    need: a row's fragment (and, at the end of a quad, its scale dword) is read again in
 //    place as soon as the row's products are issued, and only the activation side, which
 //    every row uses, is held twice.
-#include "gemm_kernel.hpp"
 #include "gemm_tiles.hpp"
-#include "mx4.hpp"
+#include "mx4_gemm_kernel.hpp"
 #include "mx4_launch.hpp"
 
 namespace i8mm {
-
-#define I8MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
-
-template <class C>
-__device__ __forceinline__ char* scale_buf() {
-  __shared__ __attribute__((aligned(1024))) char buf[(C::TN + C::TM) / 16 * 256];
-  return buf;
-}
-
-template <class C>
-struct MxBlock {
-  static constexpr int NQ = C::AI + C::BI;              // code DMAs of a wave per slab
-  static constexpr int SI = (C::TN + C::TM) / 64;       // scale DMAs of the tile per quad
-  static_assert(SI <= C::NW, "one scale DMA per wave");
-  const MxGemmArgs& g;
-  // uniform bases (the tile's first row groups) and this lane's offsets from them
-  const uint8_t *a_base, *b_base, *s_base;
-  unsigned a_off[C::AI], b_off[C::BI], s_off;
-  int ks, quads;
-  int wave, lane, rn0, rm0;
-  v4f acc[C::BN][C::BM];
-  v4i a[C::BN], b[C::BM];
-  unsigned sa[C::BN], sb[C::BM];
-
-  // One DMA instruction (q < AI: weights, else activations) of slab kt into stage S. Slabs
-  // past K repeat the last one: those of a last, partial quad are multiplied, but under the
-  // layout's padding scales of both sides, 2^-254 together, and add nothing in fp32.
-  template <int S>
-  __device__ __forceinline__ void issue_one(int kt, int q) {
-    const size_t step = static_cast<size_t>(min(kt, ks - 1)) * kUnitBytes;
-    char* base = stage_buf<C, S>();
-    if (q < C::AI)
-      dma16<0>(a_base + step + a_off[q], I8MM_LDS(base + (q * C::NW + wave) * 1024));
-    else
-      dma16<0>(b_base + step + b_off[q - C::AI], I8MM_LDS(base + C::A_BYTES + ((q - C::AI) * C::NW + wave) * 1024));
-  }
-  template <int S>
-  __device__ __forceinline__ void issue(int kt) {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) issue_one<S>(kt, q);
-  }
-  // The quad's scales. Waves past the last instruction repeat one of them (the same bytes to
-  // the same place), so that every wave has the same number of loads in flight.
-  __device__ __forceinline__ void issue_scales(int quad) {
-    dma16<0>(s_base + static_cast<size_t>(min(quad, quads - 1)) * 256 + s_off,
-             I8MM_LDS(scale_buf<C>() + (wave % SI) * 1024));
-  }
-
-  template <int S>
-  __device__ __forceinline__ v4i frag_a(int i) const {
-    return *reinterpret_cast<const v4i*>(stage_buf<C, S>() + lds_off<C::BK>(rn0 + i * 16, lane >> 4));
-  }
-  template <int S>
-  __device__ __forceinline__ v4i frag_b(int j) const {
-    return *reinterpret_cast<const v4i*>(stage_buf<C, S>() + C::A_BYTES + lds_off<C::BK>(rm0 + j * 16, lane >> 4));
-  }
-  // rn0 and rm0 are this lane's rows: their group's dwords start at row / 16
-  __device__ __forceinline__ unsigned scale_a(int i) const {
-    return reinterpret_cast<const unsigned*>(scale_buf<C>())[((rn0 >> 4) + i) * 64 + lane];
-  }
-  __device__ __forceinline__ unsigned scale_b(int j) const {
-    return reinterpret_cast<const unsigned*>(scale_buf<C>())[(C::TN / 16 + (rm0 >> 4) + j) * 64 + lane];
-  }
-
-  template <int SEL>
-  static __device__ __forceinline__ v4f mma(const v4i& w, const v4i& x, const v4f& c, unsigned sw, unsigned sx) {
-    const v8i A = {w[0], w[1], w[2], w[3]}, B = {x[0], x[1], x[2], x[3]};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, SEL, static_cast<int>(sw), SEL,
-                                                            static_cast<int>(sx));
-  }
-
-  // Slab kt, whose operands are in registers, with the refill of stage CUR by slab kt + 4
-  // (in front of the first slab of a quad its scales) and the reads of slab kt + 1 spread
-  // between the products. In flight at the wait, and not waited for: slabs kt + 2 and
-  // kt + 3, and the scales issued between them and slab kt + 1.
-  template <int CUR>
-  __device__ __forceinline__ void step(int kt) {
-    constexpr int NX = (CUR + 1) % 4;
-    constexpr int EVERY = C::BN * C::BM / NQ > 0 ? C::BN * C::BM / NQ : 1;
-    wait_and_barrier<2 * NQ + (CUR == 1 || CUR == 2 ? 1 : 0)>();
-    if constexpr (CUR == 0) issue_scales((kt >> 2) + 1);
-    v4i nb[C::BM];
-    unsigned nsb[C::BM];
-#pragma unroll
-    for (int j = 0; j < C::BM; ++j) {
-      nb[j] = frag_b<NX>(j);
-      if constexpr (CUR == 3) nsb[j] = scale_b(j);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < C::BN; ++i) {
-#pragma unroll
-      for (int j = 0; j < C::BM; ++j) {
-        acc[i][j] = mma<CUR>(a[i], b[j], acc[i][j], sa[i], sb[j]);
-        const int at = i * C::BM + j;
-        if (at % EVERY == EVERY - 1 && at / EVERY < NQ) {
-          __builtin_amdgcn_sched_barrier(0);
-          issue_one<CUR>(kt + 4, at / EVERY);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      a[i] = frag_a<NX>(i);
-      if constexpr (CUR == 3) sa[i] = scale_a(i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int j = 0; j < C::BM; ++j) {
-      b[j] = nb[j];
-      if constexpr (CUR == 3) sb[j] = nsb[j];
-    }
-  }
-};
 
 // 16x16 accumulator layout: lane l, register e holds row m = l % 16, feature 4 (l / 16) + e.
 // Each wave rounds its part of the tile into a slice of the ring and stores whole row
@@ -181,7 +68,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
   static_assert(C::STAGES == 4, "a quad of slabs is one turn of the ring");
   int tn, tm;
   tile_of(blockIdx.x, gridDim.x, tiles_m, group_m, tn, tm);
-  MxBlock<C> b{g};
+  MxBlock<C, false> b;
   const int tid = threadIdx.x, vw = tid >> 6;
   b.lane = tid & 63;
   b.wave = __builtin_amdgcn_readfirstlane(vw);
@@ -208,7 +95,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
   {
     // scale DMA w: groups 4 w .. 4 w + 3 of the tile (weights first), 16 lanes each
     static_assert(C::TN % 64 == 0, "a scale DMA serves one operand");
-    const int sw = b.wave % MxBlock<C>::SI, first = 4 * sw - C::TN / 16;
+    const int sw = b.wave % MxBlock<C, false>::SI, first = 4 * sw - C::TN / 16;
     const bool w = first < 0;
     b.s_base = reinterpret_cast<const uint8_t*>(w ? g.Ws : g.Xs) +
                static_cast<size_t>(w ? n0 / 16 : m0 / 16) * b.quads * 256;
@@ -227,7 +114,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
   b.template issue<1>(4 * q0 + 1);
   b.template issue<2>(4 * q0 + 2);
   b.template issue<3>(4 * q0 + 3);
-  wait_and_barrier<3 * MxBlock<C>::NQ>();  // scales 0 and slab 0 landed
+  wait_and_barrier<3 * MxBlock<C, false>::NQ>();  // scales 0 and slab 0 landed
 #pragma unroll
   for (int j = 0; j < C::BM; ++j) {
     b.b[j] = b.template frag_b<0>(j);
@@ -281,8 +168,6 @@ __global__ __launch_bounds__(256) void k_mx_gemm_join(MxGemmArgs g, int tiles, i
   for (int e = 0; e < 4; ++e) out[e] = T::round(sum[e]);
   *reinterpret_cast<v4t*>(static_cast<typename T::elem*>(g.Y) + static_cast<size_t>(m) * g.ldy + n) = out;
 }
-
-#undef I8MM_LDS
 
 // 256 x 256, 128 x 256 and 128 x 128 (features x rows) tiles of 8 waves, 4-stage rings.
 using MxL = GemmCfg<256, 256, 64, 2, 4, 4>;

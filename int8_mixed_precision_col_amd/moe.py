@@ -1,15 +1,19 @@
-"""A mixture-of-experts layer for a few tokens (moe_layer in include/mx4mm.h): routing, gate
-and up products, SiLU, down product and the weighted sum over experts in two launches, with
-expert weights in int8 (``binding.prepare_weight`` / ``tile_weight``) or MX4
-(``mx4.prepare_weight`` / ``tile_weight``)."""
+"""A mixture-of-experts layer, with expert weights in int8 (``binding.prepare_weight`` /
+``tile_weight``) or MX4 (``mx4.prepare_weight`` / ``tile_weight``).
+
+For a few tokens ``moe_layer`` (include/mx4mm.h): routing, gate and up products, SiLU, down
+product and the weighted sum over experts in two launches. For any number of tokens
+``moe_prompt`` and its parts (include/groupmm.h): ``route``, ``grouped_matmul`` and ``combine``.
+"""
 
 from __future__ import annotations
 
 import functools
+from typing import NamedTuple
 
 import torch
 
-from . import binding, mx4
+from . import binding, groups, mx4
 from .binding import _need_shape
 
 
@@ -52,9 +56,7 @@ def moe_layer(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple
     last expert that is on, id is -1 and weight 0. renormalize: weights sum to 1 over the
     chosen experts, otherwise they are the softmax over all of them.
 
-    More than 16 tokens: 16 at a time, or, for a prompt, each expert's tokens through ``mx4.matmul``
-    or ``binding.mixed_matmul`` on its part of the prepared weights (of gate_up the row groups
-    e * 2 I / 16 up to (e + 1) * 2 I / 16 of codes and scales; int8 constants by row).
+    More than 16 tokens: ``moe_prompt``, which quantizes the activations, or 16 at a time.
     """
     T, D, ld, dt = mx4._need_rows(X, "X")
     if not isinstance(logits, torch.Tensor) or logits.dtype not in mx4.DTYPES or logits.dim() != 2:
@@ -85,3 +87,134 @@ def moe_layer(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple
                 down[1].data_ptr(), I, out.data_ptr(), ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(),
                 workspace.numel())
     return out, ids, weights
+
+
+class Routing(NamedTuple):
+    """What ``route`` gives: each token's experts and their weights, and the order of the rows of
+    a product grouped by expert."""
+    ids: torch.Tensor       # int32 [T, top_k], -1 past the last expert that is on
+    weights: torch.Tensor   # fp32 [T, top_k]
+    offsets: torch.Tensor   # int32 [E + 1]: expert e has rows offsets[e] up to offsets[e + 1]
+    rows: torch.Tensor      # int32 [T * top_k]: the token of each row, -1 behind the last
+    slots: torch.Tensor     # int32 [T, top_k]: the row of each token and place, -1 for none
+
+
+@functools.lru_cache(maxsize=1024)
+def _route_workspace_bytes(T: int, E: int) -> int:
+    return int(groups.lib().moe_route_workspace_bytes(T, E))
+
+
+@functools.lru_cache(maxsize=1024)
+def grouped_workspace_bytes(M: int, K: int, P: int, E: int, N: int, weight_format: int, max_outliers: int = 256) -> int:
+    """What ``grouped_matmul`` needs for X [M, K], P rows of the product and E experts of N features
+    (0 on bad shapes); weight_format 0: int8, 1: MX4."""
+    return int(groups.lib().moe_grouped_workspace_bytes(M, K, P, E, N, weight_format, max_outliers))
+
+
+def route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> Routing:
+    """Routing of T tokens from their router logits [T, E] (fp16, bf16 or fp32; -inf: the expert is
+    off; E <= 512, top_k <= 16): lists as in ``moe_layer``, and the pairs of token and expert in
+    order of expert and then token. The same inputs give the same order."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in mx4.DTYPES or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D fp16, bf16 or fp32 tensor")
+    T, E = logits.shape
+    if not logits.is_contiguous() or not binding._on_device(logits):
+        _need_shape(logits, logits.dtype, (T, E), logits.device, "logits")
+    if not (1 <= top_k <= min(E, 16) and 1 <= T <= 1 << 24 and E <= 512):
+        raise ValueError(f"bad shape for route: T={T} E={E} top_k={top_k}")
+    nbytes = _route_workspace_bytes(T, E)
+    i32 = torch.int32
+    r = Routing(logits.new_empty((T, top_k), dtype=i32), logits.new_empty((T, top_k), dtype=torch.float32),
+                logits.new_empty((E + 1,), dtype=i32), logits.new_empty((T * top_k,), dtype=i32),
+                logits.new_empty((T, top_k), dtype=i32))
+    ws = mx4._scratch(None, nbytes, logits)
+    groups.launch("moe_route", logits, logits.data_ptr(), T, E, mx4.DTYPES[logits.dtype], top_k, int(renormalize),
+                  r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
+                  0 if ws is None else ws.data_ptr(), nbytes)
+    return r
+
+
+def grouped_matmul(X: torch.Tensor, weight: tuple, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                   gated: bool = False, threshold: float = 6.0, max_outliers: int | None = None,
+                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Products grouped by expert with ragged sizes: row p of Y, offsets[e] <= p < offsets[e + 1],
+    is the product of row rows[p] of X [M, K] (row p without rows) with expert e's part of `weight`,
+    one prepared weight of E * N output features. Y is [P, N] in X's type, or, gated (N: gate
+    features, then as many up features), silu(gate) * up [P, N / 2].
+
+    MX4 weights: fp16 or bf16 X, rounded to MX4 as in ``mx4.matmul``. int8 weights: fp16 X,
+    decomposed as in ``binding.mixed_matmul`` (outlier columns are those of the whole of X; more than
+    max_outliers of them, without one any number up to 8192, give NaN).
+    offsets int32 [E + 1] ascending from 0 and rows int32 [P] are on the GPU and stay there
+    (``route`` makes both). Rows of Y behind offsets[E], and rows whose index is outside X, are zeros.
+    """
+    M, K, ld, dt = mx4._need_rows(X, "X")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be an int32 tensor [E + 1]")
+    E = offsets.shape[0] - 1
+    groups.need_vector(offsets, torch.int32, (E + 1,), X, "offsets")
+    P = M
+    if rows is not None:
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            raise ValueError("rows must be an int32 tensor [P]")
+        P = rows.shape[0]
+        groups.need_vector(rows, torch.int32, (P,), X, "rows")
+    fmt, features = _rows(weight, "weight")
+    step = 32 if gated else 16
+    if features % (step * E):
+        raise ValueError(f"weight has {features} output features: not E = {E} times a multiple of {step}")
+    N = features // E
+    if not fmt and (X.dtype is not torch.float16 or ld != K):
+        raise ValueError("int8 weights take contiguous fp16 X")
+    _need_pair(weight, fmt, features, K, X, "weight")
+    width = N // 2 if gated else N
+    if out is None:
+        out = X.new_empty((P, width))
+    else:
+        _need_shape(out, X.dtype, (P, width), X.device, "out")
+    most = min(K, 8192)
+    max_outliers = most if max_outliers is None else min(max_outliers, most)
+    nbytes = grouped_workspace_bytes(M, K, P, E, N, fmt, max_outliers)
+    if nbytes == 0:
+        raise ValueError(f"bad shape for grouped_matmul: M={M} K={K} P={P} E={E} N={N} max_outliers={max_outliers}")
+    workspace = mx4._scratch(workspace, nbytes, X)
+    groups.launch("moe_grouped_matmul", X, X.data_ptr(), M, K, ld, dt, fmt, weight[0].data_ptr(), weight[1].data_ptr(),
+                  E, N, offsets.data_ptr(), 0 if rows is None else rows.data_ptr(), P, int(gated), float(threshold),
+                  max_outliers, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def combine(P: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y [T, D] in P's type: Y[t] = sum over j of weights[t, j] P[slots[t, j]], slots int32 and weights
+    fp32 [T, top_k] as from ``route``; a slot that is no row of P adds nothing."""
+    _need_shape(P, P.dtype, tuple(P.shape), P.device, "P")
+    if P.dim() != 2 or P.dtype not in mx4._HALF or P.shape[1] % 16:
+        raise ValueError(f"P must be fp16 or bf16 [rows, D], D a multiple of 16, got {P.dtype} {tuple(P.shape)}")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise ValueError("slots must be an int32 tensor [T, top_k]")
+    T, k = slots.shape
+    groups.need_vector(slots, torch.int32, (T, k), P, "slots")
+    groups.need_vector(weights, torch.float32, (T, k), P, "weights")
+    n, D = P.shape
+    if out is None:
+        out = P.new_empty((T, D))
+    else:
+        _need_shape(out, P.dtype, (T, D), P.device, "out")
+    groups.launch("moe_combine", P, P.data_ptr(), n, D, mx4.DTYPES[P.dtype], slots.data_ptr(), weights.data_ptr(), T, k,
+                  out.data_ptr())
+    return out
+
+
+def moe_prompt(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple, top_k: int,
+               renormalize: bool = True, threshold: float = 6.0, max_outliers: int | None = None,
+               out: torch.Tensor | None = None):
+    """(Y [T, D], ids, weights) as ``moe_layer``, for any number of tokens: ``route``, the gated
+    product of gate_up, the product of down and ``combine``. The activations are quantized like the
+    weights (MX4, or int8 with fp16 outlier columns, threshold and max_outliers as in
+    ``grouped_matmul``), and the hidden values and each expert's outputs are rounded to X's type
+    between the launches, where ``moe_layer`` keeps both in 16 bits or more."""
+    r = route(logits, top_k, renormalize)
+    h = grouped_matmul(X, gate_up, r.offsets, r.rows, True, threshold, max_outliers)
+    p = grouped_matmul(h, down, r.offsets, None, False, threshold, max_outliers)
+    return combine(p, r.slots, r.weights, out), r.ids, r.weights

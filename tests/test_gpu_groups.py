@@ -1,0 +1,405 @@
+"""GPU tests of the operators whose rows have weights of their own (routing, products grouped by
+expert, the weighted sum back to tokens, low-rank adapters) against the float64 oracle. Bounds
+are derived in ``oracle/groups_oracle.py``; the output's own rounding is half a step of its type."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from int8_mixed_precision_col_amd import binding, lora, moe, mx4
+from oracle import groups_oracle as ref
+from oracle import mx4_oracle
+from tests.gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+F16, B16, F32 = torch.float16, torch.bfloat16, torch.float32
+TINY = {F16: 2.0 ** -25, B16: 2.0 ** -134}  # half the smallest subnormal
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(y, want, bound):
+    y, eps, tiny = f64(y), torch.finfo(y.dtype).eps / 2, TINY[y.dtype]
+    bound = bound + (np.abs(want) + bound) * eps + tiny
+    assert y.shape == want.shape and np.isfinite(y).all()
+    worst = (np.abs(y - want) / bound).max()
+    assert worst <= 1, worst
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+# ---- routing ----
+
+def check_route(logits, k, renorm):
+    r = moe.route(logits, k, renormalize=renorm)
+    ids, weights = mx4_oracle.moe_route(f64(logits), k, renorm)
+    offsets, rows, slots = ref.group_order(ids, logits.shape[1])
+    for got, want in ((r.ids, ids), (r.offsets, offsets), (r.rows, rows), (r.slots, slots)):
+        assert got.dtype == torch.int32 and np.array_equal(got.cpu().numpy(), want)
+    assert np.abs(f64(r.weights) - weights).max() <= 1e-6
+    again = moe.route(logits, k, renormalize=renorm)
+    assert all(torch.equal(a, b) for a, b in zip(r, again))
+    return r
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (3, 65, 4), (17, 10, 3), (63, 128, 2), (64, 129, 16), (65, 64, 8),
+                                   (200, 257, 5), (1000, 512, 16), (64 * 257 + 3, 7, 2), (5000, 3, 3)])
+def test_route(T, E, k):
+    announce(f"route T={T} E={E} k={k}")
+    x = torch.randn((T, E), generator=gen(T + E))
+    x[torch.rand((T, E), generator=gen(E)) < 0.2] = -float("inf")
+    if T > 1:
+        x[T // 2] = -float("inf")      # a token without experts
+        x[T - 1] = 1.0                 # all tied
+    for dtype in (F32, F16, B16):
+        check_route(x.to(dtype).cuda(), k, T % 2 == 0)
+
+
+def test_route_every_token_off_and_all_to_one_expert():
+    announce("route, nothing on and one expert")
+    for T in (5, 300):
+        r = check_route(torch.full((T, 9), -float("inf"), device="cuda"), 4, True)
+        assert int(r.offsets.abs().max()) == 0 and bool((r.rows == -1).all()) and bool((r.weights == 0).all())
+        x = torch.full((T, 9), -float("inf"), device="cuda")
+        x[:, 4] = 1.0
+        check_route(x, 3, False)
+
+
+def test_route_of_nan_and_infinity():
+    announce("route of NaN and +inf")
+    x = torch.randn((70, 12), generator=gen(1))
+    x[3, 5], x[4, 7], x[66, 0] = float("nan"), float("inf"), float("nan")
+    r = moe.route(x.cuda(), 3)
+    ids, _ = mx4_oracle.moe_route(x.double().numpy(), 3, True)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    for t in (3, 4, 66):
+        assert bool(torch.isnan(r.weights[t]).any())
+
+
+# ---- products grouped by expert ----
+
+def weights_of(E, N, K, fmt, dtype, seed):
+    """(prepared pair, values or codes and constants) of E experts' weights."""
+    w = (torch.randn((E * N, K), generator=gen(seed)) * 0.05).to(dtype)
+    if fmt == "mx4":
+        return mx4.prepare_weight(w.cuda(), 1), mx4_oracle.mx4_round(f64(w)).reshape(E, N, K)
+    q, a = oracle.prepare_weight(w.numpy().T.copy())
+    return binding.prepare_weight(w.cuda(), 1), (q.reshape(E, N, K), a.reshape(E, N))
+
+
+def activations(M, K, dtype, seed, outliers=2):
+    x = torch.randn((M, K), generator=gen(seed))
+    for j in torch.randint(0, K, (outliers,), generator=gen(seed + 1)).tolist():
+        x[:, j] = 20 * torch.sign(x[:, j]) + x[:, j]
+    return x.to(dtype).cuda()
+
+
+def want_grouped(x, values, fmt, offsets, rows, P, gated, threshold=6.0):
+    if fmt == "mx4":
+        return ref.grouped_mx4(f64(x), values, offsets, rows, P, gated)
+    return ref.grouped_int8(x.cpu().numpy(), *values, threshold, offsets, rows, P, gated)
+
+
+def offsets_of(sizes):
+    return np.concatenate(([0], np.cumsum(sizes)))
+
+
+def check_grouped(x, weight, values, fmt, sizes, rows, P, gated, **kw):
+    offsets = offsets_of(sizes)
+    width = weight[0].shape[0] * 16 // len(sizes) // (2 if gated else 1)
+    guard = torch.full((P * width + 64,), 3.0, dtype=x.dtype, device="cuda")
+    y = moe.grouped_matmul(x, weight, i32(offsets), None if rows is None else i32(rows), gated,
+                           out=guard[:P * width].view(P, width), **kw)
+    close(y, *want_grouped(x, values, fmt, offsets, rows, P, gated))
+    assert bool((guard[P * width:] == 3.0).all())
+    assert int(torch.count_nonzero(y[offsets[-1]:])) == 0
+    return y
+
+
+GROUPED = [  # sizes, tokens, K, N
+    ([1], 1, 16, 32), ([0, 1, 0], 5, 48, 32), ([3, 0, 16, 17, 1], 9, 1040, 96), ([64, 65, 63], 40, 528, 160),
+    ([130, 7, 0, 129], 100, 144, 288), ([0, 0, 700, 3], 333, 272, 544), ([257, 255], 512, 656, 800),
+    ([1000, 0, 13, 300], 600, 2064, 288), ([0, 0], 4, 64, 64),
+]
+
+
+@pytest.mark.parametrize("fmt,dtype", [("mx4", F16), ("mx4", B16), ("int8", F16)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("sizes,T,K,N", GROUPED)
+def test_grouped(sizes, T, K, N, gated, fmt, dtype):
+    announce(f"grouped {sizes} T={T} K={K} N={N} gated={gated} {fmt} {dtype}")
+    x = activations(T, K, dtype, T + K)
+    weight, values = weights_of(len(sizes), N, K, fmt, dtype, K + N)
+    n = sum(sizes)
+    P = n + 37  # rows behind the last expert's
+    rows = np.full(P, -1)
+    rows[:n] = torch.randint(0, T, (n,), generator=gen(n)).numpy()
+    y = check_grouped(x, weight, values, fmt, sizes, rows, P, gated)
+    assert torch.equal(y, moe.grouped_matmul(x, weight, i32(offsets_of(sizes)), i32(rows), gated))  # the same bits
+    # rows in order already, some of them behind the last expert's
+    if n <= T:
+        check_grouped(x, weight, values, fmt, sizes, None, T, gated)
+
+
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+@pytest.mark.parametrize("E,n", [(64, 40), (3, 1500), (2, 64)])
+def test_grouped_each_tile_shape(E, n, fmt):
+    """Many experts of a few rows; many rows of few experts; both with empty experts."""
+    announce(f"grouped E={E} rows={n} {fmt}")
+    g = gen(E + n)
+    sizes = torch.randint(0, 2 * n // E + 2, (E,), generator=g).numpy()
+    x, (weight, values) = activations(50, 272, F16, n), weights_of(E, 160, 272, fmt, F16, E)
+    P = int(sizes.sum())
+    rows = torch.randint(0, 50, (P,), generator=g).numpy()
+    check_grouped(x, weight, values, fmt, sizes, rows, P, False)
+
+
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+def test_grouped_rows_out_of_range_are_zeros_and_offsets_stay_inside(fmt):
+    announce(f"grouped, rows and offsets out of range, {fmt}")
+    x, (weight, values) = activations(20, 144, F16, 3), weights_of(3, 64, 144, fmt, F16, 4)
+    rows = np.array([0, -1, 20, 1 << 30, -(1 << 31), 19, 7, 3])
+    y = check_grouped(x, weight, values, fmt, [3, 2, 3], rows, 8, False)
+    assert int(torch.count_nonzero(y[1:5])) == 0
+    for bad in ([0, 9, -5, 8], [8, 0, 8, 0], [-(1 << 31), 1 << 30, 1 << 30, (1 << 31) - 1], [5, 5, 2, 2]):
+        guard = torch.full((8 * 64 + 64,), 3.0, dtype=F16, device="cuda")
+        moe.grouped_matmul(x, weight, i32(bad), i32(rows), out=guard[:512].view(8, 64))
+        torch.cuda.synchronize()
+        assert bool((guard[512:] == 3.0).all())
+
+
+def test_grouped_nonfinite_rows_and_weights():
+    announce("grouped mx4, non-finite blocks")
+    x = activations(30, 272, F16, 5)
+    x[4, 100] = float("inf")
+    w = (torch.randn((3 * 48, 272), generator=gen(6)) * 0.05).half().cuda()
+    w[48 + 5, 200] = float("nan")
+    rows = np.arange(30)[::-1].copy()
+    y = moe.grouped_matmul(x, mx4.prepare_weight(w, 1), i32([0, 10, 20, 30]), i32(rows))
+    bad = torch.zeros((30, 48), dtype=torch.bool)
+    bad[25], bad[10:20, 5] = True, True
+    assert torch.equal(torch.isnan(y).cpu(), bad)
+    assert bool(torch.isfinite(y[~bad.cuda()]).all())
+
+
+def test_grouped_int8_without_and_with_many_outliers():
+    announce("grouped int8, outlier columns")
+    (weight, values), rows = weights_of(3, 96, 528, "int8", F16, 8), np.arange(90) % 40
+    for outliers in (0, 1, 16, 40):
+        check_grouped(activations(40, 528, F16, 9, outliers), weight, values, "int8", [30, 0, 60], rows, 90, True)
+    x = activations(40, 528, F16, 9, 40)
+    y = moe.grouped_matmul(x, weight, i32([0, 30, 30, 80]), i32(rows), max_outliers=8)
+    assert bool(torch.isnan(y[:80]).all()) and int(torch.count_nonzero(y[80:])) == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+def test_grouped_strided_rows(dtype):
+    announce(f"grouped mx4, strided X {dtype}")
+    big = activations(70, 400, dtype, 10)
+    x = big[:, 64:64 + 272]
+    weight, _ = weights_of(4, 64, 272, "mx4", dtype, 11)
+    off, rows = i32([0, 20, 20, 90, 100]), i32(np.arange(100) % 70)
+    assert torch.equal(moe.grouped_matmul(x, weight, off, rows), moe.grouped_matmul(x.contiguous(), weight, off, rows))
+
+
+# ---- back to tokens ----
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("T,k,D", [(1, 1, 16), (7, 3, 1040), (33, 16, 4112), (200, 8, 2048), (5, 2, 48), (9, 11, 8208)])
+def test_combine(T, k, D, dtype):
+    announce(f"combine T={T} k={k} D={D} {dtype}")
+    n = max(1, T * k - 3)
+    p = torch.randn((n, D), generator=gen(T)).to(dtype)
+    p[0] = float("nan")                # a row that no token has
+    slots = torch.randint(1 if n > 1 else 0, n, (T, k), generator=gen(k)) if n > 1 else torch.full((T, k), -1)
+    slots[torch.rand((T, k), generator=gen(D)) < 0.2] = -1
+    slots[0, 0] = n                    # past the last row
+    w = torch.randn((T, k), generator=gen(2))
+    y = moe.combine(p.cuda(), slots.int().cuda(), w.cuda())
+    close(y, *ref.combine(f64(p), slots.numpy(), w.double().numpy()))
+
+
+# ---- the layer ----
+
+@pytest.mark.parametrize("fmt,dtype", [("mx4", F16), ("mx4", B16), ("int8", F16)])
+@pytest.mark.parametrize("T,D,I,E,k", [(1, 64, 32, 3, 2), (37, 272, 144, 10, 3), (300, 528, 272, 5, 2)])
+def test_layer(T, D, I, E, k, fmt, dtype):
+    """The parts after each other, each against the oracle on what the one before gave, and
+    moe_prompt the same bits."""
+    announce(f"moe_prompt T={T} D={D} I={I} E={E} k={k} {fmt} {dtype}")
+    x = activations(T, D, dtype, T)
+    gu, gu_values = weights_of(E, 2 * I, D, fmt, dtype, D)
+    dn, dn_values = weights_of(E, D, I, fmt, dtype, I)
+    logits = torch.randn((T, E), generator=gen(E))
+    logits[torch.rand((T, E), generator=gen(k)) < 0.3] = -float("inf")
+    logits[0] = -float("inf")          # a padding row
+    r = check_route(logits.cuda(), k, True)
+    offsets, rows = r.offsets.cpu().numpy(), r.rows.cpu().numpy()
+    h = moe.grouped_matmul(x, gu, r.offsets, r.rows, gated=True)
+    close(h, *want_grouped(x, gu_values, fmt, offsets, rows, T * k, True))
+    p = moe.grouped_matmul(h, dn, r.offsets)
+    close(p, *want_grouped(h, dn_values, fmt, offsets, None, T * k, False))
+    y = moe.combine(p, r.slots, r.weights)
+    close(y, *ref.combine(f64(p), r.slots.cpu().numpy(), f64(r.weights)))
+    assert int(torch.count_nonzero(y[0])) == 0
+    whole, ids, weights = moe.moe_prompt(x, logits.cuda(), gu, dn, k)
+    assert torch.equal(whole, y) and torch.equal(ids, r.ids) and torch.equal(weights, r.weights)
+
+
+# ---- adapters ----
+
+def lora_case(M, K, N, R, S, dtype, seed, ranked):
+    g = gen(seed)
+    t = dict(Y=torch.randn((M, N), generator=g).to(dtype), X=torch.randn((M, K), generator=g).to(dtype),
+             A=(torch.randn((S, R, K), generator=g) / K ** 0.5).to(dtype),
+             B=(torch.randn((S, N, R), generator=g) / R ** 0.5).to(dtype),
+             ids=torch.randint(-1, S, (M,), generator=g).int(), scales=torch.randn(S, generator=g), ranks=None)
+    if ranked:
+        t["ranks"] = torch.randint(0, R + 1, (S,), generator=g).int()
+        t["ranks"][0] = 0
+        for a in range(S):             # what lies beyond a rank is not looked at
+            t["A"][a, t["ranks"][a]:] = float("nan")
+            t["B"][a, :, t["ranks"][a]:] = float("inf")
+    return {k: v if v is None else v.cuda() for k, v in t.items()}
+
+
+def want_lora(t):
+    return ref.lora(f64(t["Y"]), f64(t["X"]), np.nan_to_num(f64(t["A"])), f64(t["B"]), t["ids"].cpu().numpy(),
+                    None if t["scales"] is None else f64(t["scales"]),
+                    None if t["ranks"] is None else t["ranks"].cpu().numpy(), t["X"].dtype == B16)
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("M,K,N,R,S", [
+    (1, 16, 16, 8, 1), (1, 4096, 272, 16, 3), (8, 1040, 528, 16, 20), (17, 144, 4112, 24, 2), (64, 528, 144, 64, 5),
+    (65, 528, 144, 64, 5), (64, 2064, 48, 128, 64), (200, 272, 1040, 40, 1), (333, 1040, 528, 72, 9),
+    (1000, 144, 80, 104, 1000), (700, 4112, 272, 96, 3), (2050, 64, 64, 8, 2), (130, 48, 16, 120, 1024)])
+def test_lora(M, K, N, R, S, dtype):
+    announce(f"lora M={M} K={K} N={N} R={R} S={S} {dtype}")
+    for ranked in (False, True):
+        t = lora_case(M, K, N, R, S, dtype, M + K + ranked, ranked)
+        guard = torch.full((M * N + 64,), 3.0, dtype=dtype, device="cuda")
+        y = lora.apply(**t, out=guard[:M * N].view(M, N))
+        close(y, *want_lora(t))
+        assert bool((guard[M * N:] == 3.0).all())
+        none = (t["ids"] < 0).nonzero().squeeze(1)
+        assert torch.equal(y[none], t["Y"][none])
+        assert torch.equal(y, lora.apply(**t))                       # the same bits
+        inplace = t["Y"].clone()
+        assert lora.apply(**{**t, "Y": inplace}, out=inplace) is inplace and torch.equal(inplace, y)
+    t["scales"] = None
+    close(lora.apply(**t), *want_lora(t))
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("M", [1, 40, 150])
+def test_lora_strided_and_ids_out_of_range(M, dtype):
+    announce(f"lora strided M={M} {dtype}")
+    t = lora_case(M, 272, 144, 16, 4, dtype, M, False)
+    t["ids"][M // 2] = 4
+    t["ids"][0] = -(1 << 31)
+    t["ids"][M - 1] = 1 << 30
+    want = lora.apply(**t)
+    assert torch.equal(want[M // 2], t["Y"][M // 2]) and torch.equal(want[M - 1], t["Y"][M - 1])
+    xb, yb, ob = (torch.full((M, w), float("nan"), dtype=dtype, device="cuda") for w in (400, 200, 176))
+    xb[:, 64:336], yb[:, 8:152] = t["X"], t["Y"]
+    got = lora.apply(**{**t, "X": xb[:, 64:336], "Y": yb[:, 8:152]}, out=ob[:, 16:160])
+    assert torch.equal(got, want)
+    assert bool(torch.isnan(ob[:, :16]).all()) and bool(torch.isnan(ob[:, 160:]).all())
+
+
+@pytest.mark.parametrize("M", [5, 100])
+def test_lora_wide_ranges_in_fp16(M):
+    """V's rows far above and below what fp16 holds: each has a power of two of its own."""
+    announce(f"lora, rows of very different sizes, M={M}")
+    t = lora_case(M, 1040, 272, 32, 2, F16, M, False)
+    t["ids"] = (torch.arange(M) % 2).int().cuda()
+    t["X"] = (t["X"].float() * torch.exp2((torch.arange(M) % 25 - 14).float()).cuda()[:, None]).half()
+    t["A"] = (t["A"].float() * 256).half()
+    t["B"] = (t["B"].float() / 4096).half()
+    close(lora.apply(**t), *want_lora(t))
+
+
+# ---- streams, graphs, large operands ----
+
+def test_streams_and_calls_at_once():
+    announce("grouped operators on two streams")
+    x = activations(300, 528, F16, 20)
+    gu, _ = weights_of(6, 288, 528, "mx4", F16, 21)
+    dn, _ = weights_of(6, 528, 144, "mx4", F16, 22)
+    logits = torch.randn((300, 6), generator=gen(23)).cuda()
+    t = lora_case(200, 272, 528, 16, 5, F16, 24, False)
+    want = moe.moe_prompt(x, logits, gu, dn, 2)[0], lora.apply(**t)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            a = moe.moe_prompt(x, logits, gu, dn, 2)[0]
+        with torch.cuda.stream(s2):
+            b, c = lora.apply(**t), moe.moe_prompt(x, logits, gu, dn, 2)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(c, want[0])
+
+
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+@pytest.mark.parametrize("T", [20, 150])
+def test_graph_capture_and_replay(T, fmt):
+    """The layer and adapters beside it in one graph, with routing that changes between replays."""
+    announce(f"graph T={T} {fmt}")
+    x, logits = activations(T, 272, F16, 30), torch.randn((T, 6), generator=gen(31)).cuda()
+    gu, _ = weights_of(6, 288, 272, fmt, F16, 32)
+    dn, _ = weights_of(6, 272, 144, fmt, F16, 33)
+    t = lora_case(T, 272, 272, 16, 5, F16, 34, False)
+    t["X"] = x
+
+    def step():
+        y = moe.moe_prompt(x, logits, gu, dn, 3)[0]
+        return y, lora.apply(**{**t, "Y": y})
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    for seed in range(4):
+        x.copy_(activations(T, 272, F16, 40 + seed))
+        logits.copy_(torch.randn((T, 6), generator=gen(50 + seed)).cuda())
+        logits[seed] = -float("inf")
+        t["ids"].copy_(torch.randint(-1, 5, (T,), generator=gen(60 + seed)).int())
+        for o in got:
+            o.zero_()
+        graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_grouped_offsets_beyond_32_bits():
+    """Over 4 GB of expert weights and over 4 GB of outputs: the last expert's rows are right."""
+    E, N, K = 1024, 4112, 2048
+    announce(f"grouped mx4 with {E} x {N} x {K} weights")
+    codes = torch.zeros((E * N // 16, K // 128, 16, 64), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((E * N // 16, K // 512, 64, 4), dtype=torch.uint8, device="cuda")
+    assert codes.numel() > 1 << 32
+    w, values = weights_of(1, N, K, "mx4", B16, 70)
+    codes[-(N // 16):], scales[-(N // 16):] = w
+    x = activations(4, K, B16, 71)
+    n = 700000
+    offsets = np.concatenate((np.zeros(E), [n]))
+    rows = np.arange(n) % 4
+    y = moe.grouped_matmul(x, (codes, scales), i32(offsets), i32(rows))
+    assert y.numel() > 1 << 31
+    close(y[-4:], *ref.grouped_mx4(f64(x), values, [0, 4], None, 4, False))
+    assert torch.equal(y[:4], y[-4:]) and torch.equal(y[n // 2:n // 2 + 4], y[-4:])
