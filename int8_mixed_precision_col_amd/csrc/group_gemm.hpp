@@ -1,6 +1,6 @@
 // What the products with a weight per group of rows share (mx4_grouped.hip, int8_grouped.hip).
 //
-// A workgroup takes a row tile of the table (group.hpp) and TN features of that group's weight.
+// A workgroup takes a row tile and TN features of its group's weight.
 // The rows of a tile are any rows of X: each lane of the DMA that fills the ring brings 16 bytes
 // of the row that its place holds, so the rows are gathered on their way into LDS and the K loop
 // is the ungrouped product's. gated: a tile's 16-row groups of the weight are gate and up in
@@ -13,6 +13,11 @@
 
 namespace i8mm {
 
+// A tile's group (-1: rows behind the last group's), its first row and its rows, 1 .. TM.
+struct RowTile {
+  int group, first, rows;
+};
+
 // 16-row group of the group's weight behind place v of a tile whose first output feature is n0.
 // Past the last feature it is the last one's (those outputs are not stored).
 template <bool GATED>
@@ -22,31 +27,65 @@ __device__ __forceinline__ int weight_group(int v, int n0, int N) {
 }
 
 // Row of X behind row r of a tile; M, a row of zeros, where there is none.
-__device__ __forceinline__ int source_row(const GroupShape& g, const int4& tile, int r) {
-  if (r >= tile.z) return g.M;
-  const int p = tile.y + r;
+__device__ __forceinline__ int source_row(const GroupShape& g, const RowTile& tile, int r) {
+  if (r >= tile.rows) return g.M;
+  const int p = tile.first + r;
   const int s = g.rows ? g.rows[p] : p;
   return s >= 0 && s < g.M ? s : g.M;
 }
 
 template <class C, bool GATED>
-__device__ __forceinline__ void zero_tile(const GroupShape& g, const int4& tile, int n0) {
+__device__ __forceinline__ void zero_tile(const GroupShape& g, const RowTile& tile, int n0) {
   constexpr int OUT = GATED ? C::TN / 2 : C::TN;
   const int N = GATED ? g.N / 2 : g.N;
-  for (int t = threadIdx.x; t < tile.z * (OUT / 8); t += C::NT) {
+  for (int t = threadIdx.x; t < tile.rows * (OUT / 8); t += C::NT) {
     const int n = n0 + t % (OUT / 8) * 8;
-    if (n < N) *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.Y) + static_cast<size_t>(tile.y + t / (OUT / 8)) * N + n) = v4u{};
+    if (n < N) *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.Y) + static_cast<size_t>(tile.first + t / (OUT / 8)) * N + n) = v4u{};
   }
 }
 
-// The tile of workgroup b (false: none); table and order as in tile_of, over the tiles that
-// there are.
-__device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, int4& tile, int& tn) {
-  const int tiles_m = g.table[0].x, blocks = tiles_n * tiles_m;
+// The row tile and feature tile of this workgroup (false: there is none for it), in the order of
+// tile_of over the tiles that there are. Row tiles never cross a group's border; the rows behind
+// the last group are a group of their own, -1. Every wave works it out for itself: the groups' rows,
+// 64 groups at a time, their tiles and sums of these (a table made by a launch of its own costs 2.3
+// us, and looking it up as long a chain of loads). Offsets that do not ascend give some tiles, at
+// most g.tiles_most, with all rows in [0, P).
+template <class C>
+__device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, RowTile& tile, int& tn) {
+  const int lane = threadIdx.x & 63, chunks = g.G / 64 + 1;  // of the G + 1 groups
+  auto rows_of = [&](int e, int& first) {
+    first = e <= g.G ? group_first(g.offsets, e, g.P) : g.P;
+    return max((e < g.G ? group_first(g.offsets, e + 1, g.P) : g.P) - first, 0);
+  };
+  int sums = 0, first = 0, rows = 0, upto = 0;  // lane c: the tiles of chunk c
+  for (int c = 0; c < chunks; ++c) {
+    rows = rows_of(64 * c + lane, first);
+    upto = wave_prefix_sum((rows + C::TM - 1) / C::TM);
+    const int sum = __builtin_amdgcn_readlane(upto, 63);
+    if (lane == c) sums = sum;
+  }
+  const int chunk_upto = wave_prefix_sum(sums);
+  const int tiles_m = min(__builtin_amdgcn_readlane(chunk_upto, 63), g.tiles_most), blocks = tiles_n * tiles_m;
   if (static_cast<int>(blockIdx.x) >= blocks) return false;
-  int tm;
-  tile_of(blockIdx.x, blocks, tiles_m, min(tiles_m, 8), tn, tm);
-  tile = g.table[1 + tm];
+  // each XCD (workgroup number mod 8) takes a contiguous run of the tiles
+  const int xcd = blockIdx.x & 7, extra = blocks & 7;
+  int at = static_cast<int>(blockIdx.x >> 3) + xcd * (blocks >> 3) + min(xcd, extra);
+  // the run goes through the groups, all features of one after the other
+  const int chunk = __builtin_ctzll(__ballot(chunk_upto > at / tiles_n));
+  at -= __builtin_amdgcn_readlane(chunk_upto - sums, chunk) * tiles_n;
+  if (chunks > 1) {
+    rows = rows_of(64 * chunk + lane, first);
+    upto = wave_prefix_sum((rows + C::TM - 1) / C::TM);
+  }
+  const int e = __builtin_ctzll(__ballot(upto > at / tiles_n)), n = __builtin_amdgcn_readlane(rows, e);
+  const int tiles = (n + C::TM - 1) / C::TM;
+  at -= (__builtin_amdgcn_readlane(upto, e) - tiles) * tiles_n;
+  const int band = at / (8 * tiles_n), in = at - band * 8 * tiles_n, high = min(tiles - 8 * band, 8);
+  const int tm = 8 * band + in % high;
+  tn = in / high;
+  tile.group = 64 * chunk + e < g.G ? 64 * chunk + e : -1;
+  tile.first = __builtin_amdgcn_readlane(first, e) + tm * C::TM;
+  tile.rows = min(n - tm * C::TM, C::TM);
   return true;
 }
 
@@ -56,7 +95,7 @@ __device__ __forceinline__ float silu_up(float g, float u) { return __fdiv_rn(g,
 // bytes per lane. 16 x 16 accumulator layout: lane l, register e holds row m = l % 16, feature
 // 4 (l / 16) + e; value(i, j, e) is that of block (i, j).
 template <class C, class T, bool GATED, class F>
-__device__ __forceinline__ void store_tile(const GroupShape& g, const int4& tile, int n0, int wn, int wm, int lane,
+__device__ __forceinline__ void store_tile(const GroupShape& g, const RowTile& tile, int n0, int wn, int wm, int lane,
                                            F value) {
   typedef typename T::elem v4t __attribute__((ext_vector_type(4)));
   constexpr int WF = GATED ? C::WTN / 2 : C::WTN;  // output features of a wave
@@ -83,14 +122,13 @@ __device__ __forceinline__ void store_tile(const GroupShape& g, const int4& tile
     const int r = t * RPI + lane / CH;
     const v4u v = *reinterpret_cast<const v4u*>(ys + r * RB + 16 * (c ^ swizzle(r)));
     const int m = wm * C::WTM + r;
-    if (m < tile.z && n < N)
-      *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.Y) + static_cast<size_t>(tile.y + m) * N + n) = v;
+    if (m < tile.rows && n < N)
+      *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.Y) + static_cast<size_t>(tile.first + m) * N + n) = v;
   }
 }
 
-// 256 x 256, 128 x 256, 128 x 128 (features x rows) on 8 waves, 128 x 64 on 4; 4-stage rings.
+// 256 x 256 and 128 x 128 (features x rows) on 8 waves, 128 x 64 on 4; 4-stage rings.
 using GroupL = GemmCfg<256, 256, 64, 2, 4, 4>;
-using GroupM = GemmCfg<128, 256, 64, 2, 4, 4>;
 using GroupS = GemmCfg<128, 128, 64, 2, 4, 4>;
 using GroupT = GemmCfg<128, 64, 64, 2, 2, 4>;
 

@@ -36,9 +36,6 @@ struct CombineArgs {
 };
 hipError_t launch_combine(const CombineArgs& a, int type, hipStream_t s);
 
-// The table of row tiles (group.hpp) for tiles of tm rows.
-hipError_t launch_group_tiles(const int32_t* offsets, int G, int P, int tm, int4* table, hipStream_t s);
-
 // Rows of X [M][ldx] to MX4, row by row, and one row M of zeros behind them.
 struct GroupQuantArgs {
   const void* X;
@@ -49,14 +46,15 @@ struct GroupQuantArgs {
 };
 hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t s);
 
-// Shared by both weight formats: P rows, row p of tile's group e against that group's N rows of
-// the weight.
+// Shared by both weight formats: P rows, row p of group e (offsets[e] <= p < offsets[e + 1]) against
+// that group's N rows of the weight.
 struct GroupShape {
   int M, K, N, P;         // rows of X, of K; output features per group; rows of Y
   int gated;              // N is gate features, then as many up features
   const int32_t* rows;    // [P] rows of X, or null: row p
-  const int4* table;
-  int tiles_most;         // of the table
+  const int32_t* offsets; // [G + 1]
+  int G;
+  int tiles_most;         // row tiles that there can be
   void* Y;                // [P][gated ? N / 2 : N]
 };
 struct MxGroupArgs : GroupShape {
@@ -67,10 +65,10 @@ struct MxGroupArgs : GroupShape {
 struct Int8GroupArgs : GroupShape {
   GemmArgs q;             // Xq, a_x, Xo, o_stride, idx, count, max_outliers of X; Wq, a_w of all groups
 };
-// Tile shapes (features x rows): 256 x 256, 128 x 256, 128 x 128, 128 x 64.
-enum class GroupTile { L, M, S, T };
+// Tile shapes (features x rows): 256 x 256, 128 x 128, 128 x 64.
+enum class GroupTile { L, S, T };
 int group_tile_rows(GroupTile t);
-GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t N);
+GroupTile pick_group_tile(int64_t P, int64_t groups, bool int8);
 hipError_t launch_mx_grouped(const MxGroupArgs& a, GroupTile t, int type, hipStream_t s);
 hipError_t launch_int8_grouped(const Int8GroupArgs& a, GroupTile t, hipStream_t s);
 

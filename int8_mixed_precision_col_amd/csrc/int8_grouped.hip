@@ -12,7 +12,7 @@ namespace i8mm {
 // weight's features by weight_group.
 template <class C, bool GATED>
 __device__ __forceinline__ void int8_group_epilogue(const Int8GroupArgs& g, const GemmArgs& q, v4i (&acc)[C::BN][C::BM],
-                                                    const int4& tile, int n0, int wn, int wm, int lane, int tid) {
+                                                    const RowTile& tile, int n0, int wn, int wm, int lane, int tid) {
   constexpr int OS = 24;  // staged row stride in halves (16 columns + 8 of padding)
   static_assert((C::TN + C::TM) * 8 + (C::TN + C::TM) * OS * 2 <= C::STAGE, "staging fits a stage");
   char* base = stage_buf<C, 0>();
@@ -85,18 +85,18 @@ __device__ __forceinline__ void int8_group_epilogue(const Int8GroupArgs& g, cons
 
 template <class C, bool GATED>
 __global__ __launch_bounds__(C::NT) void k_int8_grouped(Int8GroupArgs g, int tiles_n) {
-  int4 tile;
+  RowTile tile;
   int tn;
-  if (!group_tile_of(g, tiles_n, tile, tn)) return;
+  if (!group_tile_of<C>(g, tiles_n, tile, tn)) return;
   const int n0 = tn * (GATED ? C::TN / 2 : C::TN);
-  if (tile.x < 0) {
+  if (tile.group < 0) {
     zero_tile<C, GATED>(g, tile, n0);
     return;
   }
   const int ks = unit_ks(g.K);
   GemmArgs q = g.q;
-  q.Wq += static_cast<size_t>(tile.x) * (g.N / 16) * ks * kUnitBytes;
-  q.a_w += static_cast<size_t>(tile.x) * g.N;
+  q.Wq += static_cast<size_t>(tile.group) * (g.N / 16) * ks * kUnitBytes;
+  q.a_w += static_cast<size_t>(tile.group) * g.N;
   GemmBlock<C> b{q};
   const int tid = threadIdx.x, vw = tid >> 6;
   b.lane = tid & 63;
@@ -158,7 +158,6 @@ static hipError_t run(const Int8GroupArgs& g, hipStream_t s) {
 
 hipError_t launch_int8_grouped(const Int8GroupArgs& g, GroupTile t, hipStream_t s) {
   if (t == GroupTile::L) return run<GroupL>(g, s);
-  if (t == GroupTile::M) return run<GroupM>(g, s);
   if (t == GroupTile::S) return run<GroupS>(g, s);
   return run<GroupT>(g, s);
 }

@@ -84,6 +84,14 @@ struct MxBlock {
                                                             static_cast<int>(sx));
   }
 
+  // A slab's part of a wave that multiplies nothing: the same waits, barriers and loads.
+  template <int CUR>
+  __device__ __forceinline__ void bring(int kt) {
+    wait_and_barrier<2 * NQ + (CUR == 1 || CUR == 2 ? 1 : 0)>();
+    if constexpr (CUR == 0) issue_scales((kt >> 2) + 1);
+    issue<CUR>(kt + 4);
+  }
+
   // Slab kt, whose operands are in registers, with the refill of stage CUR by slab kt + 4
   // (in front of the first slab of a quad its scales) and the reads of slab kt + 1 spread
   // between the products. In flight at the wait, and not waited for: slabs kt + 2 and

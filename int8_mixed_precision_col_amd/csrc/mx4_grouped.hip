@@ -49,11 +49,11 @@ template <class C, class T, bool GATED>
 __global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n) {
   static_assert(C::STAGES == 4, "a quad of slabs is one turn of the ring");
   typedef MxBlock<C, true> Block;
-  int4 tile;
+  RowTile tile;
   int tn;
-  if (!group_tile_of(g, tiles_n, tile, tn)) return;
+  if (!group_tile_of<C>(g, tiles_n, tile, tn)) return;
   const int n0 = tn * (GATED ? C::TN / 2 : C::TN);
-  if (tile.x < 0) {
+  if (tile.group < 0) {
     zero_tile<C, GATED>(g, tile, n0);
     return;
   }
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n
   b.rm0 = (vw / C::WGN) * C::WTM + (b.lane & 15);
   b.ks = mx_ks(g.K);
   b.quads = mx_quads(g.K);
-  const size_t first_group = static_cast<size_t>(tile.x) * (g.N / 16);
+  const size_t first_group = static_cast<size_t>(tile.group) * (g.N / 16);
   b.a_base = g.Wc + first_group * b.ks * kUnitBytes;
   b.b_base = g.Xc;
   // slot p of a stage holds row p / CPR, chunk (p % CPR) ^ swz(row)
@@ -116,11 +116,21 @@ __global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n
     b.a[i] = b.template frag_a<0>(i);
     b.sa[i] = b.scale_a(i);
   }
-  for (int kt = 0; kt < 4 * b.quads; kt += 4) {
-    b.template step<0>(kt);
-    b.template step<1>(kt + 1);
-    b.template step<2>(kt + 2);
-    b.template step<3>(kt + 3);
+  // a wave whose rows are behind the tile's last only brings its share of the operands
+  if (wm * C::WTM < tile.rows) {
+    for (int kt = 0; kt < 4 * b.quads; kt += 4) {
+      b.template step<0>(kt);
+      b.template step<1>(kt + 1);
+      b.template step<2>(kt + 2);
+      b.template step<3>(kt + 3);
+    }
+  } else {
+    for (int kt = 0; kt < 4 * b.quads; kt += 4) {
+      b.template bring<0>(kt);
+      b.template bring<1>(kt + 1);
+      b.template bring<2>(kt + 2);
+      b.template bring<3>(kt + 3);
+    }
   }
   // no DMA may still be writing this block's LDS when it is reused or the block exits
   __builtin_amdgcn_s_waitcnt(0);
@@ -148,7 +158,6 @@ static hipError_t run(const MxGroupArgs& g, int type, hipStream_t s) {
 
 hipError_t launch_mx_grouped(const MxGroupArgs& g, GroupTile t, int type, hipStream_t s) {
   if (t == GroupTile::L) return run<GroupL>(g, type, s);
-  if (t == GroupTile::M) return run<GroupM>(g, type, s);
   if (t == GroupTile::S) return run<GroupS>(g, type, s);
   return run<GroupT>(g, type, s);
 }
