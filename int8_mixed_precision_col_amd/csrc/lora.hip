@@ -12,6 +12,7 @@
 //
 // Rows in order: up to 64 rows every workgroup orders for itself by comparing the ids (no launch);
 // beyond, one workgroup sorts them first (k_lora_order).
+#include "gemm_kernel.hpp"
 #include "group.hpp"
 #include "group_launch.hpp"
 #include "mx4.hpp"
@@ -20,28 +21,54 @@
 namespace i8mm {
 
 constexpr int kLoraFew = 64;  // rows that each workgroup orders by itself
-constexpr int kLoraWaves = 4;
+constexpr int kLoraWaves = 8;
+// Parts of K at most, their sums loaded together: of few rows, where workgroups are few, and of many
+// (us per call with 2 / 4 / 8: 8 x 4096 x 4096 of rank 16 8.5 / 7.5 / 7.1, 3333 x 4096 x 11008 of rank 64
+// 70.8 / 64.7 / 70.9).
+constexpr int kLoraFewSplits = 8, kLoraSplits = 4;
 
 // ---- rows by adapter ----
 
 // Counting sort of ids into S adapters and, last, the rows without one; stable. 16 waves each take
-// a stretch of the rows and count it, then place it, 64 rows at a time; then the table of tiles.
+// a stretch of the rows, 64 at a time: lanes of equal group find each other by a ballot per bit of
+// the group's number, so no order depends on atomics. Counts, their sums, places; then the table of
+// tiles.
 constexpr int kOrderWaves = 16, kOrderThreads = 64 * kOrderWaves;
+constexpr int kOrderBatch = 4;  // chunks of 64 rows whose ids are asked for together
 __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int most) {
   extern __shared__ int lds[];
   const int G = a.S + 1, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int* next = lds;                  // [wave][G]: rows, then the next place
+  int* next = lds + wave * G;          // this wave's rows of each group, then their next place
   int* first = lds + kOrderWaves * G;  // [G + 1]
   __shared__ int wave_sums[kOrderWaves];
-  const int chunks = (a.M + 63) / 64, per = (chunks + kOrderWaves - 1) / kOrderWaves;
+  const int per = ((a.M + 63) / 64 + kOrderWaves - 1) / kOrderWaves;
   const int m0 = min(wave * per * 64, a.M), m1 = min(m0 + per * 64, a.M);
-  for (int i = tid; i < kOrderWaves * G; i += kOrderThreads) next[i] = 0;
-  __syncthreads();
-  auto group_of = [&](int m) {
-    const int id = a.ids[m];
-    return id >= 0 && id < a.S ? id : a.S;
+  const int bits = 32 - __builtin_clz(a.S);
+  for (int g = lane; g < G; g += 64) next[g] = 0;
+  wave_lds_fence();
+  auto each_chunk = [&](auto use) {
+    for (int c0 = m0; c0 < m1; c0 += 64 * kOrderBatch) {
+      int id[kOrderBatch];
+#pragma unroll
+      for (int i = 0; i < kOrderBatch; ++i) id[i] = a.ids[min(c0 + 64 * i + lane, a.M - 1)];
+#pragma unroll
+      for (int i = 0; i < kOrderBatch; ++i) {
+        const int m = c0 + 64 * i + lane;
+        if (m - lane >= m1) break;
+        const int g = id[i] >= 0 && id[i] < a.S ? id[i] : a.S;
+        unsigned long long same = __ballot(m < m1);
+        for (int b = 0; b < bits; ++b) {
+          const unsigned long long set = __ballot(g >> b & 1);
+          same &= g >> b & 1 ? set : ~set;
+        }
+        if (m < m1) use(m, g, same, __builtin_popcountll(same & ((1ull << lane) - 1ull)));
+        wave_lds_fence();
+      }
+    }
   };
-  for (int m = m0 + lane; m < m1; m += 64) atomicAdd(&next[wave * G + group_of(m)], 1);
+  each_chunk([&](int, int g, unsigned long long same, int rank) {
+    if (rank == 0) next[g] += __builtin_popcountll(same);
+  });
   __syncthreads();
   // exclusive sums: over the groups (a thread has one or two, G <= 1025), within one over the waves
   int run = 0;
@@ -49,7 +76,7 @@ __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int mo
     const int g = g0 + tid;
     int n = 0;
     if (g < G)
-      for (int w = 0; w < kOrderWaves; ++w) n += next[w * G + g];
+      for (int w = 0; w < kOrderWaves; ++w) n += lds[w * G + g];
     int upto = wave_prefix_sum(n);
     if (lane == 63) wave_sums[wave] = upto;
     __syncthreads();
@@ -62,8 +89,8 @@ __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int mo
       int at = run + upto - n;
       first[g] = at;
       for (int w = 0; w < kOrderWaves; ++w) {
-        const int c = next[w * G + g];
-        next[w * G + g] = at;
+        const int c = lds[w * G + g];
+        lds[w * G + g] = at;
         at += c;
       }
     }
@@ -71,27 +98,11 @@ __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int mo
     __syncthreads();
   }
   if (tid == 0) first[G] = a.M;
-  __syncthreads();
-  for (int c0 = m0; c0 < m1; c0 += 64) {
-    const int m = c0 + lane;
-    const bool on = m < m1;
-    const int g = on ? group_of(m) : -1;
-    // the lanes of equal group: rank among them, and the last one moves the group's next place on
-    unsigned long long left = __ballot(on);
-    while (left) {
-      const int who = __builtin_ctzll(left);
-      const int lead = __builtin_amdgcn_readlane(g, who);
-      const unsigned long long same = __ballot(g == lead);
-      if (g == lead) {
-        const int rank = __builtin_popcountll(same & ((1ull << lane) - 1ull));
-        a.order[next[wave * G + lead] + rank] = m;
-      }
-      wave_lds_fence();
-      if (lane == who) next[wave * G + lead] += __builtin_popcountll(same);
-      wave_lds_fence();
-      left &= ~same;
-    }
-  }
+  each_chunk([&](int m, int g, unsigned long long same, int rank) {
+    const int at = next[g];
+    a.order[at + rank] = m;
+    if (rank == 0) next[g] = at + __builtin_popcountll(same);
+  });
   __syncthreads();
   // the rows without an adapter are the table's group -1
   make_group_tiles<kOrderThreads>(first, a.S, a.M, kLoraRows, most, a.table);
@@ -122,8 +133,8 @@ __device__ __forceinline__ bool lora_tile(const LoraArgs& a, int b, int* row_of,
     t.rows = __builtin_popcountll(mine);
     if (tid < 64 && (mine >> lane & 1)) row_of[__builtin_popcountll(mine & ((1ull << lane) - 1ull))] = lane;
   } else {
-    if (b >= a.table[0].x) return false;
-    const int4 e = a.table[1 + b];
+    const int4 head = a.table[0], e = a.table[1 + b];  // on their way together
+    if (b >= head.x) return false;
     t.adapter = e.x;
     t.rows = e.z;
     if (tid < e.z) row_of[tid] = a.order[e.y + tid];
@@ -138,198 +149,408 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& a, int adapter) {
 
 // ---- V = A X over a part of K ----
 
-// RB: blocks of 16 ranks. The waves share the part's K in steps of 32; each lane loads 16 bytes of
-// a row, in the order of the matrix instruction's operand: rows l % 16, elements 8 (l / 16) .. + 7.
-template <class T, int RB>
-__global__ __launch_bounds__(64 * kLoraWaves) void k_lora_shrink(LoraArgs a) {
-  __shared__ int row_of[kLoraRows];
-  __shared__ __attribute__((aligned(16))) float red[kLoraWaves][kLoraRows][20];
-  LoraTile tile;
-  if (!lora_tile(a, blockIdx.x, row_of, tile) || tile.adapter < 0) return;
+// RB: blocks of 16 ranks. The waves share the part's K in steps of 64, so that the row pieces
+// they ask for are whole 128-byte lines: lane l has row l % 16, elements 16 (l / 16) .. + 15 of the
+// step, the first 8 for one matrix instruction and the others for the next (both operands take K
+// in this order, so it does not matter which element is where). No load
+// is under a condition (the compiler waits for one at once): rows behind the tile's last are the
+// last one, and what lies behind K is the row's last 8 elements against zeros in A.
+template <class T, int RB, int J>
+__device__ __forceinline__ void lora_shrink(const LoraArgs& a, const LoraTile& tile, int rank, const int* row_of,
+                                            float (&red)[kLoraWaves][kLoraRows][36]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int steps = (a.K + 31) / 32, split = blockIdx.y, splits = gridDim.y;
+  const int steps = (a.K + 63) / 64, split = blockIdx.y, splits = gridDim.y;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * split / splits);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits);
-  const int rank = lora_rank(a, tile.adapter);
-  const uint16_t *x[4], *w[RB];
+  const uint16_t *x[J], *w[RB];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    x[j] = static_cast<const uint16_t*>(a.X) + static_cast<int64_t>(row_of[min(16 * j + l16, tile.rows - 1)]) * a.ldx + 8 * lq;
+  for (int j = 0; j < J; ++j)
+    x[j] = static_cast<const uint16_t*>(a.X) + static_cast<int64_t>(row_of[min(16 * j + l16, tile.rows - 1)]) * a.ldx;
 #pragma unroll
   for (int i = 0; i < RB; ++i)
     w[i] = static_cast<const uint16_t*>(a.A) +
-           (static_cast<int64_t>(tile.adapter) * a.R + min(16 * i + l16, max(rank - 1, 0))) * a.K + 8 * lq;
-  v4f acc[RB][4];
+           (static_cast<int64_t>(tile.adapter) * a.R + min(16 * i + l16, max(rank - 1, 0))) * a.K;
+  v4f acc[RB][J];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{};
-  const int blocks = (tile.rows + 15) / 16;
+    for (int j = 0; j < J; ++j) acc[i][j] = v4f{};
   for (int s = s0 + wave; s < s1; s += kLoraWaves) {
-    const int k = 32 * s;
-    const bool in = k + 8 * lq < a.K;
-    v4u xv[4], wv[RB];
+    v4u xv[2][J], wv[2][RB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      xv[j] = v4u{};
-      if (j < blocks && in) xv[j] = *reinterpret_cast<const v4u*>(x[j] + k);
+    for (int h = 0; h < 2; ++h) {
+      const int k = min(64 * s + 16 * lq + 8 * h, a.K - 8);
+#pragma unroll
+      for (int j = 0; j < J; ++j) xv[h][j] = *reinterpret_cast<const v4u*>(x[j] + k);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) wv[h][i] = *reinterpret_cast<const v4u*>(w[i] + k);
+    }
+    if (64 * s + 64 > a.K) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned keep = 64 * s + 16 * lq + 8 * h < a.K ? ~0u : 0u;
+#pragma unroll
+        for (int i = 0; i < RB; ++i) wv[h][i] &= keep;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      wv[i] = v4u{};
-      if (in) wv[i] = *reinterpret_cast<const v4u*>(w[i] + k);
-    }
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+      for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < blocks) acc[i][j] = T::mfma(wv[i], xv[j], acc[i][j]);
+        for (int j = 0; j < J; ++j) acc[i][j] = T::mfma(wv[h][i], xv[h][j], acc[i][j]);
   }
-  // lane l holds row 16 j + l % 16, ranks 16 i + 4 (l / 16) .. + 3: the waves' sums through LDS
+  // lane l holds row 16 j + l % 16, ranks 16 i + 4 (l / 16) .. + 3: the waves' sums through LDS, 32
+  // ranks at a time
   const int R16 = 16 * RB;
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    if (i > 0) __syncthreads();
+  for (int i0 = 0; i0 < RB; i0 += 2) {
+    if (i0 > 0) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < blocks) *reinterpret_cast<v4f*>(&red[wave][16 * j + l16][4 * lq]) = acc[i][j];
+    for (int i = i0; i < i0 + 2 && i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j) *reinterpret_cast<v4f*>(&red[wave][16 * j + l16][16 * (i - i0) + 4 * lq]) = acc[i][j];
     __syncthreads();
-    const int r = tid >> 2, c = 4 * (tid & 3);
-    if (r < tile.rows) {
+    const int r = tid >> 3, c = 4 * (tid & 7), at = 16 * i0 + c;
+    if (r < tile.rows && at < R16) {
       v4f sum = *reinterpret_cast<const v4f*>(&red[0][r][c]);
 #pragma unroll
       for (int v = 1; v < kLoraWaves; ++v) sum += *reinterpret_cast<const v4f*>(&red[v][r][c]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = 16 * i + c + e < rank ? sum[e] : 0.0f;
-      *reinterpret_cast<v4f*>(a.part + (static_cast<int64_t>(split) * a.M + row_of[r]) * R16 + 16 * i + c) = sum;
+      for (int e = 0; e < 4; ++e) sum[e] = at + e < rank ? sum[e] : 0.0f;
+      *reinterpret_cast<v4f*>(a.part + (static_cast<int64_t>(split) * a.M + row_of[r]) * R16 + at) = sum;
     }
   }
 }
 
+template <class T, int RB>
+__global__ __launch_bounds__(64 * kLoraWaves) void k_lora_shrink(LoraArgs a) {
+  __shared__ int row_of[kLoraRows];
+  __shared__ __attribute__((aligned(16))) float red[kLoraWaves][kLoraRows][36];
+  LoraTile tile;
+  if (!lora_tile(a, blockIdx.x, row_of, tile) || tile.adapter < 0) return;
+  const int rank = lora_rank(a, tile.adapter);
+  if (tile.rows <= 16) lora_shrink<T, RB, 1>(a, tile, rank, row_of, red);
+  else if (tile.rows <= 32) lora_shrink<T, RB, 2>(a, tile, rank, row_of, red);
+  else lora_shrink<T, RB, 4>(a, tile, rank, row_of, red);
+}
+
 // ---- out = Y + scale B V ----
 
-// A workgroup takes a tile's rows and `span` features, its waves 32 of them at a time: two
-// blocks of 16 of B's rows, taken so that a lane ends with 8 consecutive features of a row.
-// KS: steps of 32 ranks.
-template <class T, int KS>
-__global__ __launch_bounds__(64 * kLoraWaves) void k_lora_expand(LoraArgs a, int span) {
-  typedef typename T::elem elem;
-  typedef elem v8e __attribute__((ext_vector_type(8)));
-  typedef elem v4e __attribute__((ext_vector_type(4)));
-  constexpr int LR = 32 * KS + 8;  // padded row of V in LDS
-  __shared__ int row_of[kLoraRows];
-  __shared__ __attribute__((aligned(16))) elem v[2][kLoraRows][LR];
-  __shared__ float row_scale[kLoraRows];
-  LoraTile tile;
-  if (!lora_tile(a, blockIdx.x, row_of, tile)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.y * span, n1 = min(n0 + span, a.N);
-  const uint16_t* Y = static_cast<const uint16_t*>(a.Y);
-  uint16_t* out = static_cast<uint16_t*>(a.out);
-  const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
-  if (rank == 0) {
-    if (Y == out) return;
-    const int per = (n1 - n0) / 8;
-    for (int t = tid; t < tile.rows * per; t += 64 * kLoraWaves) {
-      const int64_t m = row_of[t / per];
-      const int n = n0 + t % per * 8;
-      *reinterpret_cast<v4u*>(out + m * a.ldo + n) = *reinterpret_cast<const v4u*>(Y + m * a.ldy + n);
+// For up to kLoraFew rows. Features n0 .. n1 of a tile's rows, 32 at a time for each wave: two blocks
+// of 16 of B's rows, straight from memory, taken so that a lane ends with 8 consecutive features of a
+// row. The next 32 features' Y and B are on their way while these are multiplied and stored, and the
+// first ones' while V is put together. No load or store is under a condition, or the compiler would
+// wait for all of them where it needs one: rows behind the tile's last are the last one and
+// features behind n1 the last 8, and such lanes compute and store the same values again. KS: steps
+// of 32 ranks, J: blocks of 16 rows.
+template <class T, int KS, int J>
+struct LoraExpand {
+  typedef typename T::elem v8e __attribute__((ext_vector_type(8)));
+  const LoraArgs& a;
+  const uint16_t* B;
+  int last_row, n1, rank, l16, lq;
+  const uint16_t* y_row[J];
+  uint16_t* o_row[J];
+  struct Operands {
+    v4u y[J], b[2][KS];
+  };
+
+  __device__ __forceinline__ LoraExpand(const LoraArgs& a_, const LoraTile& tile, int rank_, const int* row_of, int n1_)
+      : a(a_), last_row(tile.rows - 1), n1(n1_), rank(rank_) {
+    const int lane = threadIdx.x & 63;
+    l16 = lane & 15;
+    lq = lane >> 4;
+    B = static_cast<const uint16_t*>(a.B) + static_cast<int64_t>(tile.adapter) * a.N * a.R;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int64_t m = row_of[min(16 * j + l16, last_row)];
+      y_row[j] = static_cast<const uint16_t*>(a.Y) + m * a.ldy;
+      o_row[j] = static_cast<uint16_t*>(a.out) + m * a.ldo;
     }
-    return;
   }
-  const int R16 = (a.R + 15) & ~15;
-  // V: four threads to a row, each 4 ranks of every 16
-  {
-    const int r = tid >> 2, c = 4 * (tid & 3);
-    v4f sum[2 * KS];
-    float most = 0.0f;
+  // first of the 8 features of lane group g
+  __device__ __forceinline__ int feature(int n, int g) const { return min(n + 8 * g, n1 - 8); }
+  __device__ __forceinline__ void load(Operands& o, int n) const {
 #pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) {
-      sum[i] = v4f{};
-      if (r < tile.rows && 16 * i < R16) {
-        const float* p = a.part + static_cast<int64_t>(row_of[r]) * R16 + 16 * i + c;
-        for (int s = 0; s < a.splits; ++s) sum[i] += *reinterpret_cast<const v4f*>(p + static_cast<int64_t>(s) * a.M * R16);
-      }
+    for (int j = 0; j < J; ++j) o.y[j] = *reinterpret_cast<const v4u*>(y_row[j] + feature(n, lq));
+    // row l % 16 of block h is feature 4 h + l % 4 of lane group l % 16 / 4
 #pragma unroll
-      for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(sum[i][e]));
-    }
-    float up = 1.0f, down = 1.0f;
-    if constexpr (!T::bf) {
-      most = fmaxf(most, __shfl_xor(most, 1, 64));
-      most = fmaxf(most, __shfl_xor(most, 2, 64));
-      // the row's largest to [2^14, 2^15)
-      const int e = most > 0.0f && most < __builtin_inff() ? 14 - ilogbf(most) : 0;
-      up = ldexpf(1.0f, min(max(e, -126), 126));
-      down = ldexpf(1.0f, -min(max(e, -126), 126));
-    }
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) {
-      v4e hi, lo;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float f = sum[i][e] * up;
-        hi[e] = T::round(f);
-        lo[e] = T::round(f - static_cast<float>(hi[e]));
-      }
-      *reinterpret_cast<v4e*>(&v[0][r][16 * i + c]) = hi;
-      *reinterpret_cast<v4e*>(&v[1][r][16 * i + c]) = lo;
-    }
-    if ((tid & 3) == 0) row_scale[r] = down * (a.scales ? a.scales[tile.adapter] : 1.0f);
+      for (int s = 0; s < KS; ++s)
+        o.b[h][s] = *reinterpret_cast<const v4u*>(B + static_cast<int64_t>(feature(n, l16 >> 2) + 4 * h + (l16 & 3)) * a.R +
+                                                  min(32 * s + 8 * lq, a.R - 8));
   }
-  __syncthreads();
-  const int blocks = (tile.rows + 15) / 16;
-  const uint16_t* B = static_cast<const uint16_t*>(a.B) + static_cast<int64_t>(tile.adapter) * a.N * a.R;
-  for (int n = n0 + 32 * wave; n < n1; n += 32 * kLoraWaves) {
-    const int at = n + 8 * lq;  // this lane's output features
-    v4u y[4];
+  template <int LR>
+  __device__ __forceinline__ void multiply(Operands& o, int n, const typename T::elem (&v)[2][kLoraRows][LR],
+                                           const float* row_scale) const {
+    if (rank < 32 * KS) {  // ranks past this adapter's may hold anything
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] = v4u{};
-      if (16 * j + l16 < tile.rows && at < n1)
-        y[j] = *reinterpret_cast<const v4u*>(Y + static_cast<int64_t>(row_of[16 * j + l16]) * a.ldy + at);
-    }
-    // row l % 16 of block h is feature 8 (l % 16 / 4) + 4 h + l % 4
-    v4u b[2][KS];
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int f = min(n + 8 * (l16 >> 2) + 4 * h + (l16 & 3), a.N - 1);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int k = 32 * s + 8 * lq;
-        b[h][s] = v4u{};
-        if (k < rank) b[h][s] = *reinterpret_cast<const v4u*>(B + static_cast<int64_t>(f) * a.R + k);
-        // ranks past this adapter's may hold anything
-        if (k < rank && k + 8 > rank) {
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            b[h][s][d] &= (k + 2 * d < rank ? 0xffffu : 0u) | (k + 2 * d + 1 < rank ? 0xffff0000u : 0u);
+        for (int d = 0; d < 4; ++d) {
+          const int k = 32 * s + 8 * lq + 2 * d;
+          const unsigned keep = (k < rank ? 0xffffu : 0u) | (k + 1 < rank ? 0xffff0000u : 0u);
+          o.b[0][s][d] &= keep;
+          o.b[1][s][d] &= keep;
         }
-      }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= blocks) break;
+    for (int j = 0; j < J; ++j) {
+      const int r = min(16 * j + l16, last_row);
+      __builtin_amdgcn_sched_barrier(0);  // V is read for 16 rows at a time: all of it does not fit the registers
       v4f acc[2] = {v4f{}, v4f{}};
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const v4u x = *reinterpret_cast<const v4u*>(&v[p][16 * j + l16][32 * s + 8 * lq]);
-          acc[0] = T::mfma(b[0][s], x, acc[0]);
-          acc[1] = T::mfma(b[1][s], x, acc[1]);
+          const v4u x = *reinterpret_cast<const v4u*>(&v[p][r][32 * s + 8 * lq]);
+          acc[0] = T::mfma(o.b[0][s], x, acc[0]);
+          acc[1] = T::mfma(o.b[1][s], x, acc[1]);
         }
-      if (16 * j + l16 < tile.rows && at < n1) {
-        const float sc = row_scale[16 * j + l16];
-        const v8e old = __builtin_bit_cast(v8e, y[j]);
-        v8e o;
+      const float sc = row_scale[r];
+      const v8e old = __builtin_bit_cast(v8e, o.y[j]);
+      v8e out;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = T::round(__builtin_fmaf(sc, acc[e >> 2][e & 3], static_cast<float>(old[e])));
-        *reinterpret_cast<v8e*>(out + static_cast<int64_t>(row_of[16 * j + l16]) * a.ldo + at) = o;
-      }
+      for (int e = 0; e < 8; ++e) out[e] = T::round(__builtin_fmaf(sc, acc[e >> 2][e & 3], static_cast<float>(old[e])));
+      *reinterpret_cast<v8e*>(o_row[j] + feature(n, lq)) = out;
     }
   }
+};
+
+// V of the tile's rows: LPR lanes to a row, 4 ranks each; the parts of K together.
+template <class T, int KS, int THREADS, int SPLITS, int LR>
+__device__ __forceinline__ void lora_gather_v(const LoraArgs& a, const LoraTile& tile, const int* row_of,
+                                              typename T::elem (&v)[2][kLoraRows][LR], float* row_scale) {
+  typedef typename T::elem v4e __attribute__((ext_vector_type(4)));
+  constexpr int LPR = KS == 1 ? 8 : KS == 2 ? 16 : 32, RPP = THREADS / LPR;
+  const int c = 4 * (threadIdx.x % LPR), R16 = (a.R + 15) & ~15;
+  for (int r = threadIdx.x / LPR; r < tile.rows; r += RPP) {
+    const float* p = a.part + static_cast<int64_t>(row_of[r]) * R16 + min(c, R16 - 4);
+    v4f part[SPLITS], sum = v4f{};
+#pragma unroll
+    for (int i = 0; i < SPLITS; ++i)
+      part[i] = *reinterpret_cast<const v4f*>(p + static_cast<int64_t>(min(i, a.splits - 1)) * a.M * R16);
+#pragma unroll
+    for (int i = 0; i < SPLITS; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += i < a.splits && c < R16 ? part[i][e] : 0.0f;
+    float up = 1.0f, down = 1.0f;
+    if constexpr (!T::bf) {
+      float most = fmaxf(fmaxf(fabsf(sum[0]), fabsf(sum[1])), fmaxf(fabsf(sum[2]), fabsf(sum[3])));
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+      // the row's largest to [2^14, 2^15)
+      const int e = most > 0.0f && most < __builtin_inff() ? 14 - ilogbf(most) : 0;
+      up = ldexpf(1.0f, min(max(e, -126), 126));
+      down = ldexpf(1.0f, -min(max(e, -126), 126));
+    }
+    v4e hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float f = sum[e] * up;
+      hi[e] = T::round(f);
+      lo[e] = T::round(f - static_cast<float>(hi[e]));
+    }
+    if (c < 32 * KS) {
+      *reinterpret_cast<v4e*>(&v[0][r][c]) = hi;
+      *reinterpret_cast<v4e*>(&v[1][r][c]) = lo;
+    }
+    if (c == 0) row_scale[r] = down * (a.scales ? a.scales[tile.adapter] : 1.0f);
+  }
+}
+
+// Rows without an adapter: out is Y.
+template <int THREADS>
+__device__ __forceinline__ void lora_copy_rows(const LoraArgs& a, const LoraTile& tile, const int* row_of, int n0, int n1) {
+  if (a.Y == a.out) return;
+  const int per = (n1 - n0) / 8;
+  for (int t = threadIdx.x; t < tile.rows * per; t += THREADS) {
+    const int64_t m = row_of[t / per];
+    const int n = n0 + t % per * 8;
+    *reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.out) + m * a.ldo + n) =
+        *reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(a.Y) + m * a.ldy + n);
+  }
+}
+
+// A workgroup takes a tile's rows and `span` features.
+template <class T, int KS, int J, int LR>
+__device__ __forceinline__ void lora_expand(const LoraArgs& a, const LoraTile& tile, int rank, const int* row_of,
+                                            typename T::elem (&v)[2][kLoraRows][LR], float* row_scale, int n0, int n1) {
+  constexpr int step = 32 * kLoraWaves;
+  const LoraExpand<T, KS, J> e(a, tile, rank, row_of, n1);
+  int n = n0 + 32 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  typename LoraExpand<T, KS, J>::Operands x, y;
+  e.load(x, n);
+  lora_gather_v<T, KS, 64 * kLoraWaves, kLoraFewSplits>(a, tile, row_of, v, row_scale);
+  lds_barrier();
+  for (; n < n1; n += 2 * step) {
+    e.load(y, n + step);
+    e.multiply(x, n, v, row_scale);
+    if (n + step >= n1) break;
+    e.load(x, n + 2 * step);
+    e.multiply(y, n + step, v, row_scale);
+  }
+}
+
+template <class T, int KS>
+__global__ __launch_bounds__(64 * kLoraWaves) void k_lora_expand(LoraArgs a, int span) {
+  constexpr int LR = 32 * KS + 8;  // padded row of V in LDS
+  __shared__ int row_of[kLoraRows];
+  __shared__ __attribute__((aligned(16))) typename T::elem v[2][kLoraRows][LR];
+  __shared__ float row_scale[kLoraRows];
+  LoraTile tile;
+  if (!lora_tile(a, blockIdx.x, row_of, tile)) return;
+  const int n0 = blockIdx.y * span, n1 = min(n0 + span, a.N);
+  const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
+  if (rank == 0) {
+    lora_copy_rows<64 * kLoraWaves>(a, tile, row_of, n0, n1);
+    return;
+  }
+  if (tile.rows <= 16) lora_expand<T, KS, 1>(a, tile, rank, row_of, v, row_scale, n0, n1);
+  else if (tile.rows <= 32) lora_expand<T, KS, 2>(a, tile, rank, row_of, v, row_scale, n0, n1);
+  else lora_expand<T, KS, 4>(a, tile, rank, row_of, v, row_scale, n0, n1);
+}
+
+// For more than kLoraFew rows. A tile's rows share B: each of four waves has 16 of the rows,
+// with their V in registers, and B comes 128 features at a time through LDS (two buffers, filled by
+// DMA), read by all four. Of eight blocks of 16 of its rows, block h has the features 8 c + h, so that
+// a lane has 8 consecutive features of four rows and 16 lanes together 256 contiguous bytes of a row.
+// Y is asked for two steps ahead, and nothing is under a condition, as above.
+constexpr int kStagedWaves = 4;
+template <class T, int KS>
+struct LoraStaged {
+  typedef typename T::elem v8e __attribute__((ext_vector_type(8)));
+  static constexpr int CPR = 4 * KS, ROWS = 128, BYTES = ROWS * CPR * 16;  // 16-byte pieces of a staged row
+  static constexpr int DMAS = BYTES / 1024 / kStagedWaves;
+  const LoraArgs& a;
+  const uint16_t* B;
+  int n1, rank, wave, lane, l16, lq;
+
+  // Row 16 h + c of the buffer is feature 8 c + h, its piece p at p ^ swizzle(c): the 16 rows of a
+  // fragment read then lie in different banks.
+  static __device__ __forceinline__ int swizzle(int c) { return KS == 4 ? c : KS == 2 ? (c >> 1) & 7 : (c >> 2) & 3; }
+  // first of the 8 features of column c (the last 8 behind n1)
+  __device__ __forceinline__ int feature(int n, int c) const { return min(n + 8 * c, n1 - 8); }
+
+  // this wave's share of B's rows for features n .. n + 127; pieces past the adapter's rank are zeros
+  __device__ __forceinline__ void bring(char* buf, int n) const {
+#pragma unroll
+    for (int i = 0; i < DMAS; ++i) {
+      const int at = (i * kStagedWaves + wave) * 64 + lane, r = at / CPR, c = r & 15, p = (at % CPR) ^ swizzle(c);
+      const void* src = 8 * p < rank ? static_cast<const void*>(B + static_cast<int64_t>(feature(n, c) + (r >> 4)) * a.R + 8 * p)
+                                     : static_cast<const void*>(kZero16);
+      dma16<0>(src, (__attribute__((address_space(3))) void*)(buf + (i * kStagedWaves + wave) * 1024));
+    }
+  }
+  __device__ __forceinline__ v4u piece(const char* buf, int h, int s) const {
+    v4u b = *reinterpret_cast<const v4u*>(buf + ((16 * h + l16) * CPR + ((4 * s + lq) ^ swizzle(l16))) * 16);
+    if (rank & 7) {  // the adapter's last piece: ranks past its own may hold anything
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int k = 32 * s + 8 * lq + 2 * d;
+        b[d] &= (k < rank ? 0xffffu : 0u) | (k + 1 < rank ? 0xffff0000u : 0u);
+      }
+    }
+    return b;
+  }
+};
+
+template <class T, int KS>
+__global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraArgs a, int span) {
+  typedef LoraStaged<T, KS> Staged;
+  typedef typename Staged::v8e v8e;
+  constexpr int LR = 32 * KS + 8;  // padded row of V in LDS
+  __shared__ int row_of[kLoraRows];
+  __shared__ __attribute__((aligned(16))) typename T::elem v[2][kLoraRows][LR];
+  __shared__ float row_scale[kLoraRows];
+  __shared__ __attribute__((aligned(1024))) char buf0[Staged::BYTES];
+  __shared__ __attribute__((aligned(1024))) char buf1[Staged::BYTES];
+  LoraTile tile;
+  if (!lora_tile(a, blockIdx.x, row_of, tile)) return;
+  const int n0 = blockIdx.y * span, n1 = min(n0 + span, a.N);
+  const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
+  if (rank == 0) {
+    lora_copy_rows<64 * kStagedWaves>(a, tile, row_of, n0, n1);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Staged st{a, static_cast<const uint16_t*>(a.B) + static_cast<int64_t>(tile.adapter) * a.N * a.R, n1, rank,
+                  wave, lane, lane & 15, lane >> 4};
+  st.bring(buf0, n0);
+  const uint16_t* y_row[4];
+  uint16_t* o_row[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t m = row_of[min(16 * wave + 4 * st.lq + e, tile.rows - 1)];
+    y_row[e] = static_cast<const uint16_t*>(a.Y) + m * a.ldy;
+    o_row[e] = static_cast<uint16_t*>(a.out) + m * a.ldo;
+  }
+  auto load_y = [&](v4u (&y)[4], int n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const v4u*>(y_row[e] + st.feature(n, st.l16));
+  };
+  v4u y0[4], y1[4];
+  load_y(y0, n0);
+  load_y(y1, n0 + 128);
+  lora_gather_v<T, KS, 64 * kStagedWaves, kLoraSplits>(a, tile, row_of, v, row_scale);
+  wait_and_barrier<0>();
+  if (16 * wave >= tile.rows) {  // no rows: only its share of B
+    for (int n = n0; n < n1; n += 256) {
+      if (n > n0) wait_and_barrier<0>();
+      st.bring(buf1, n + 128);
+      if (n + 128 >= n1) break;
+      wait_and_barrier<0>();
+      st.bring(buf0, n + 256);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    return;
+  }
+  v4u x[2][KS];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      x[p][s] = *reinterpret_cast<const v4u*>(&v[p][min(16 * wave + st.l16, tile.rows - 1)][32 * s + 8 * st.lq]);
+  float sc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sc[e] = row_scale[min(16 * wave + 4 * st.lq + e, tile.rows - 1)];
+  auto step = [&](const char* buf, char* other, v4u (&y)[4], int n) {
+    st.bring(other, n + 128);
+    asm volatile("" ::: "memory");  // what is asked for from here on comes after B's share: the next wait counts on it
+    v4f acc[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) acc[h] = v4f{};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const v4u b = st.piece(buf, h, s);
+        acc[h] = T::mfma(x[0][s], b, acc[h]);
+        acc[h] = T::mfma(x[1][s], b, acc[h]);
+      }
+    v8e out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const v8e old = __builtin_bit_cast(v8e, y[e]);
+#pragma unroll
+      for (int h = 0; h < 8; ++h) out[e][h] = T::round(__builtin_fmaf(sc[e], acc[h][e], static_cast<float>(old[h])));
+    }
+    load_y(y, n + 256);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<v8e*>(o_row[e] + st.feature(n, st.l16)) = out[e];
+  };
+  for (int n = n0; n < n1; n += 256) {
+    // B's share of this step was asked for before the last step's 4 loads and 4 stores
+    if (n > n0) wait_and_barrier<8>();
+    step(buf0, buf1, y0, n);
+    if (n + 128 >= n1) break;
+    wait_and_barrier<8>();
+    step(buf1, buf0, y1, n + 128);
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // no DMA may still be writing this workgroup's LDS
 }
 
 // Tiles of the rows, as many as there may be.
@@ -339,9 +560,10 @@ static int64_t lora_tiles(int64_t M, int64_t S) {
 }
 
 int lora_splits(int64_t M, int64_t K, int64_t S) {
-  const int64_t by_tiles = 1024 / lora_tiles(M, S), by_k = K / 256;
+  const int64_t by_tiles = 512 / lora_tiles(M, S), by_k = K / (64 * kLoraWaves);
   const int64_t n = by_tiles < by_k ? by_tiles : by_k;
-  return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+  const int64_t most = M <= kLoraFew ? kLoraFewSplits : kLoraSplits;
+  return static_cast<int>(n < 1 ? 1 : n > most ? most : n);
 }
 
 template <class T>
@@ -366,11 +588,22 @@ static hipError_t lora(const LoraArgs& a, hipStream_t s) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // features per workgroup: whole rounds of its waves, about four workgroups per CU
-  constexpr int round = 32 * kLoraWaves;
-  const int64_t want = (static_cast<int64_t>(a.N) * tiles + 1023) / 1024;
-  const int span = static_cast<int>((want + round - 1) / round * round);
+  // features per workgroup: as many workgroups as the GPU holds, two to three per CU
+  const bool few = a.M <= kLoraFew;
+  const int round = few ? 32 * kLoraWaves : 128;
+  const int64_t per = (few ? 512 : 768) / tiles < 1 ? 1 : (few ? 512 : 768) / tiles;
+  const int span = static_cast<int>(((a.N + per - 1) / per + round - 1) / round * round);
   const dim3 expand(tiles, (a.N + span - 1) / span);
+  if (!few) {
+    const dim3 staged(64 * kStagedWaves);
+    switch ((a.R + 31) / 32) {
+      case 1: hipLaunchKernelGGL((k_lora_expand_staged<T, 1>), expand, staged, 0, s, a, span); break;
+      case 2: hipLaunchKernelGGL((k_lora_expand_staged<T, 2>), expand, staged, 0, s, a, span); break;
+      case 3: hipLaunchKernelGGL((k_lora_expand_staged<T, 3>), expand, staged, 0, s, a, span); break;
+      default: hipLaunchKernelGGL((k_lora_expand_staged<T, 4>), expand, staged, 0, s, a, span); break;
+    }
+    return hipGetLastError();
+  }
   switch ((a.R + 31) / 32) {
     case 1: hipLaunchKernelGGL((k_lora_expand<T, 1>), expand, threads, 0, s, a, span); break;
     case 2: hipLaunchKernelGGL((k_lora_expand<T, 2>), expand, threads, 0, s, a, span); break;
