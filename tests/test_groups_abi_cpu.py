@@ -33,8 +33,8 @@ def test_header_binding_and_exports_agree(L):
 
 def test_sizes(L):
     assert L.moe_route_workspace_bytes(64, 512) == 0
-    assert L.moe_route_workspace_bytes(65, 512) >= 2 * 512 * 4
-    assert L.moe_route_workspace_bytes(1 << 24, 512) >= 256 * 512 * 4
+    assert L.moe_route_workspace_bytes(65, 512) >= 2 * 512 * 2
+    assert L.moe_route_workspace_bytes(1 << 24, 512) >= 256 * 512 * 2
     for bad in [(0, 8), (8, 0), (8, 513), ((1 << 24) + 1, 8), (-1, 8)]:
         assert L.moe_route_workspace_bytes(*bad) == 0
     # codes and scales of X and a row of zeros
