@@ -16,12 +16,11 @@ __host__ __device__ __forceinline__ int64_t group_tiles_most(int64_t rows, int64
 // First row of group g, from ascending offsets [G + 1]; whatever they hold, it is in [0, P].
 __device__ __forceinline__ int group_first(const int* offsets, int g, int P) { return min(max(offsets[g], 0), P); }
 
-// Makes the table of groups 0 .. G - 1 and of the rows behind them, for tiles of tm rows; one
-// workgroup of NT threads. Offsets that do not ascend give some table of at most `most` tiles,
-// with every row in [0, P).
+// Tiles of tm rows before each of the groups 0 .. G (group G: the rows behind the others) and, at G +
+// 1, of all: in LDS, by a workgroup of NT threads. Offsets that do not ascend give some numbers.
+typedef int GroupTilesBefore[kMaxGroupsOfRows + 2];
 template <int NT>
-__device__ __forceinline__ void make_group_tiles(const int* offsets, int G, int P, int tm, int most, int4* table) {
-  __shared__ int first[kMaxGroupsOfRows + 2];  // tiles before group g
+__device__ __forceinline__ void count_group_tiles(const int* offsets, int G, int P, int tm, GroupTilesBefore& first) {
   __shared__ int part[NT / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int per = (G + NT) / NT;  // consecutive groups of a thread, of G + 1
@@ -39,18 +38,72 @@ __device__ __forceinline__ void make_group_tiles(const int* offsets, int G, int 
     if (g == G) first[G + 1] = at;
   }
   __syncthreads();
+}
+
+// The group that tile t < first[G + 1] is of.
+__device__ __forceinline__ int group_of_tile(const GroupTilesBefore& first, int G, int t) {
+  int lo = 0, hi = G;  // the group g with first[g] <= t < first[g + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// {group, first row, rows, 0} of tile number `in` of group g, for tiles of tm rows.
+__device__ __forceinline__ int4 group_tile(const int* offsets, int G, int P, int g, int in, int tm) {
+  const int row = group_first(offsets, g, P) + in * tm;
+  const int end = g < G ? group_first(offsets, g + 1, P) : P;
+  return make_int4(g < G ? g : -1, row, min(tm, end - row), 0);
+}
+
+// Makes the table of groups 0 .. G - 1 and of the rows behind them, for tiles of tm rows; one
+// workgroup of NT threads. Offsets that do not ascend give some table of at most `most` tiles,
+// with every row in [0, P).
+template <int NT>
+__device__ __forceinline__ void make_group_tiles(const int* offsets, int G, int P, int tm, int most, int4* table) {
+  __shared__ GroupTilesBefore first;
+  count_group_tiles<NT>(offsets, G, P, tm, first);
   const int tiles = min(first[G + 1], most);
-  if (tid == 0) table[0] = make_int4(tiles, 0, 0, 0);
-  for (int t = tid; t < tiles; t += NT) {
-    int lo = 0, hi = G;  // the group g with first[g] <= t < first[g + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    const int row = group_first(offsets, lo, P) + (t - first[lo]) * tm;
-    const int end = lo < G ? group_first(offsets, lo + 1, P) : P;
-    table[1 + t] = make_int4(lo < G ? lo : -1, row, min(tm, end - row), 0);
+  if (threadIdx.x == 0) table[0] = make_int4(tiles, 0, 0, 0);
+  for (int t = threadIdx.x; t < tiles; t += NT) {
+    const int g = group_of_tile(first, G, t);
+    table[1 + t] = group_tile(offsets, G, P, g, t - first[g], tm);
+  }
+}
+
+// The order in which workgroups take row tiles and feature tiles. Each XCD (workgroup number mod 8)
+// takes a contiguous run of the products; the run goes through the groups, all tiles_n feature
+// tiles of one after the other, up to 8 row tiles of the group for each, so that workgroups that
+// run together share the weight's slabs and the rows' in their XCD's L2.
+__device__ __forceinline__ int group_order(int bid, int blocks) {
+  const int xcd = bid & 7, extra = blocks & 7;
+  return (bid >> 3) + xcd * (blocks >> 3) + min(xcd, extra);
+}
+// Number `in` of a group's products, of `tiles` row tiles: its row tile and feature tile.
+__device__ __forceinline__ void group_product(int in, int tiles, int tiles_n, int& tm, int& tn) {
+  const int band = in / (8 * tiles_n), left = in - band * 8 * tiles_n, high = min(tiles - 8 * band, 8);
+  tm = 8 * band + left % high;
+  tn = left / high;
+}
+
+// Part `part` of `parts` of the table of that order: entry 0 {products}, entry 1 + b {group, first
+// row, rows, feature tile} of workgroup b. At most tiles_n * most products.
+template <int NT>
+__device__ __forceinline__ void make_group_order(const int* offsets, int G, int P, int rows, int tiles_n, int most,
+                                                 int4* table, int part, int parts) {
+  __shared__ GroupTilesBefore first;
+  count_group_tiles<NT>(offsets, G, P, rows, first);
+  const int blocks = tiles_n * min(first[G + 1], most);
+  if (part == 0 && threadIdx.x == 0) table[0] = make_int4(blocks, 0, 0, 0);
+  for (int b = part * NT + threadIdx.x; b < blocks; b += parts * NT) {
+    const int at = group_order(b, blocks), g = group_of_tile(first, G, at / tiles_n);
+    int tm, tn;
+    group_product(at - first[g] * tiles_n, first[g + 1] - first[g], tiles_n, tm, tn);
+    int4 t = group_tile(offsets, G, P, g, tm, rows);
+    t.w = tn;
+    table[1 + b] = t;
   }
 }
 

@@ -42,17 +42,24 @@ bool bad_grouped(int64_t M, int64_t K, int64_t P, int64_t E, int64_t N, int form
   return (M + 1) * row >= kMaxOffset || N * row >= kMaxOffset;
 }
 
-// What X is quantized to.
+// What X is quantized to and, MX4, the order of the products.
 struct GroupedLayout {
-  size_t scales = 0, total = 0;
+  i8mm::GroupTile tile;
+  int tiles_n, tiles_most;
+  size_t scales = 0, table = 0, total = 0;
 };
-GroupedLayout grouped_layout(int64_t M, int64_t K, int format, int64_t max_outliers) {
+GroupedLayout grouped_layout(int64_t M, int64_t K, int64_t P, int64_t E, int64_t N, int format, int64_t max_outliers) {
   GroupedLayout L;
+  L.tile = i8mm::pick_group_tile(P, E, format == 0);
+  const int64_t features = i8mm::group_tile_features(L.tile);
+  L.tiles_n = int((N + features - 1) / features);
+  L.tiles_most = int(i8mm::group_tiles_most(P, E, i8mm::group_tile_rows(L.tile)));
   if (format == 0) {
     L.total = round256(int8_quant_state_bytes(M, K, max_outliers));
   } else {
     L.scales = round256(size_t(M + 1) * i8mm::mx_ks(K) * i8mm::kUnitK);
-    L.total = L.scales + round256(size_t(M + 1) * i8mm::mx_quads(K) * 16);
+    L.table = L.scales + round256(size_t(M + 1) * i8mm::mx_quads(K) * 16);
+    L.total = L.table + round256((1 + size_t(L.tiles_n) * L.tiles_most) * sizeof(int4));
   }
   return L;
 }
@@ -104,7 +111,7 @@ size_t moe_grouped_workspace_bytes(int64_t M, int64_t K, int64_t P, int64_t E, i
                                    int64_t max_outliers) {
   return bad_grouped(M, K, P, E, N, weight_format, max_outliers)
              ? 0
-             : grouped_layout(M, K, weight_format, max_outliers).total;
+             : grouped_layout(M, K, P, E, N, weight_format, max_outliers).total;
 }
 
 int moe_grouped_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dtype, int weight_format, const void* w,
@@ -120,12 +127,10 @@ int moe_grouped_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dty
   if (!aligned16(X) || !aligned16(w) || !aligned16(s) || !aligned4(offsets) || !aligned4(rows) || !aligned16(Y) ||
       !aligned16(workspace))
     return INT8MM_E_ALIGN;
-  const GroupedLayout L = grouped_layout(M, K, weight_format, max_outliers);
+  const GroupedLayout L = grouped_layout(M, K, P, E, N, weight_format, max_outliers);
   if (workspace_bytes < L.total) return INT8MM_E_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  const i8mm::GroupTile tile = i8mm::pick_group_tile(P, E, weight_format == 0);
-  const int tiles_most = int(i8mm::group_tiles_most(P, E, i8mm::group_tile_rows(tile)));
-  const i8mm::GroupShape shape{int(M), int(K), int(N), int(P), gated != 0, rows, offsets, int(E), tiles_most, Y};
+  i8mm::GroupShape shape{int(M), int(K), int(N), int(P), gated != 0, rows, offsets, int(E), L.tiles_most, nullptr, Y};
   if (weight_format == 0) {
     char* st = ws;
     int rc = int8_quantize_activations(X, M, K, threshold, max_outliers, st, workspace_bytes, stream);
@@ -144,15 +149,18 @@ int moe_grouped_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dty
     a.q.count = reinterpret_cast<const int32_t*>(st + at[4]);
     a.q.o_stride = int(at[5]);
     a.q.max_outliers = int(max_outliers);
-    return hip_status(i8mm::launch_int8_grouped(a, tile, stream));
+    return hip_status(i8mm::launch_int8_grouped(a, L.tile, stream));
   }
   uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
   uint8_t* scales = reinterpret_cast<uint8_t*>(ws + L.scales);
-  const i8mm::GroupQuantArgs q{X, ldx, int(M), int(K), codes, scales};
+  int4* table = reinterpret_cast<int4*>(ws + L.table);
+  const i8mm::GroupQuantArgs q{X, ldx, int(M), int(K), codes, scales, offsets, int(E), int(P),
+                               i8mm::group_tile_rows(L.tile), L.tiles_n, L.tiles_most, table};
   const hipError_t e = i8mm::launch_group_quantize(q, dtype, stream);
   if (e != hipSuccess) return INT8MM_E_HIP;
+  shape.table = table;
   const i8mm::MxGroupArgs a{shape, codes, scales, static_cast<const uint8_t*>(w), static_cast<const uint32_t*>(s)};
-  return hip_status(i8mm::launch_mx_grouped(a, tile, dtype, stream));
+  return hip_status(i8mm::launch_mx_grouped(a, L.tile, dtype, stream));
 }
 
 int moe_combine(const void* P, int64_t P_rows, int64_t D, int dtype, const int32_t* slots, const float* weights,

@@ -45,13 +45,20 @@ __device__ __forceinline__ void zero_tile(const GroupShape& g, const RowTile& ti
 }
 
 // The row tile and feature tile of this workgroup (false: there is none for it), in the order of
-// tile_of over the tiles that there are. Row tiles never cross a group's border; the rows behind
-// the last group are a group of their own, -1. Every wave works it out for itself: the groups' rows,
-// 64 groups at a time, their tiles and sums of these (a table made by a launch of its own costs 2.3
-// us, and looking it up as long a chain of loads). Offsets that do not ascend give some tiles, at
-// most g.tiles_most, with all rows in [0, P).
-template <class C>
+// group_order. With a table of it (g.table) that is one load; otherwise every wave works it out for
+// itself from the offsets, 64 groups at a time, which takes 2.4 us of a tile's start. Offsets that do
+// not ascend give some tiles, at most g.tiles_most, with all rows in [0, P).
+template <class C, bool TABLE>
 __device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, RowTile& tile, int& tn) {
+  if constexpr (TABLE) {
+    const int4 head = g.table[0], t = g.table[1 + blockIdx.x];  // on their way together
+    if (static_cast<int>(blockIdx.x) >= head.x) return false;
+    tile.group = t.x;
+    tile.first = t.y;
+    tile.rows = t.z;
+    tn = t.w;
+    return true;
+  }
   const int lane = threadIdx.x & 63, chunks = g.G / 64 + 1;  // of the G + 1 groups
   auto rows_of = [&](int e, int& first) {
     first = e <= g.G ? group_first(g.offsets, e, g.P) : g.P;
@@ -67,10 +74,7 @@ __device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, 
   const int chunk_upto = wave_prefix_sum(sums);
   const int tiles_m = min(__builtin_amdgcn_readlane(chunk_upto, 63), g.tiles_most), blocks = tiles_n * tiles_m;
   if (static_cast<int>(blockIdx.x) >= blocks) return false;
-  // each XCD (workgroup number mod 8) takes a contiguous run of the tiles
-  const int xcd = blockIdx.x & 7, extra = blocks & 7;
-  int at = static_cast<int>(blockIdx.x >> 3) + xcd * (blocks >> 3) + min(xcd, extra);
-  // the run goes through the groups, all features of one after the other
+  int at = group_order(blockIdx.x, blocks);
   const int chunk = __builtin_ctzll(__ballot(chunk_upto > at / tiles_n));
   at -= __builtin_amdgcn_readlane(chunk_upto - sums, chunk) * tiles_n;
   if (chunks > 1) {
@@ -79,17 +83,26 @@ __device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, 
   }
   const int e = __builtin_ctzll(__ballot(upto > at / tiles_n)), n = __builtin_amdgcn_readlane(rows, e);
   const int tiles = (n + C::TM - 1) / C::TM;
-  at -= (__builtin_amdgcn_readlane(upto, e) - tiles) * tiles_n;
-  const int band = at / (8 * tiles_n), in = at - band * 8 * tiles_n, high = min(tiles - 8 * band, 8);
-  const int tm = 8 * band + in % high;
-  tn = in / high;
+  int tm;
+  group_product(at - (__builtin_amdgcn_readlane(upto, e) - tiles) * tiles_n, tiles, tiles_n, tm, tn);
   tile.group = 64 * chunk + e < g.G ? 64 * chunk + e : -1;
   tile.first = __builtin_amdgcn_readlane(first, e) + tm * C::TM;
   tile.rows = min(n - tm * C::TM, C::TM);
   return true;
 }
 
-__device__ __forceinline__ float silu_up(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
+// silu(g) u = g u / (1 + exp(-g)), within 9 units of 2^-24 relative, by t = exp(-|g|) <= 1, so that
+// nothing overflows: g u / (1 + t), and g u t / (1 + t) for negative g. 64 of them per lane follow a
+// 256 x 256 tile: with expf and an IEEE quotient they took 7 of its 44 us at K = 4096. t is 2^p with
+// the rounding of p put back; the exponential and reciprocal instructions are within one unit in
+// the last place. |g| beyond 100 counts as 100 there (t is 0).
+__device__ __forceinline__ float silu_up(float g, float u) {
+  constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+  const float x = -fminf(fabsf(g), 100.0f);
+  const float p = x * kLog2e, low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -p));
+  const float e = __builtin_amdgcn_exp2f(p), t = __builtin_fmaf(e, low * kLn2, e);
+  return g * (g < 0.0f ? t : 1.0f) * __builtin_amdgcn_rcpf(1.0f + t) * u;
+}
 
 // Rounds the wave's part of the tile into its slice of the ring and stores whole row segments, 16
 // bytes per lane. 16 x 16 accumulator layout: lane l, register e holds row m = l % 16, feature

@@ -43,6 +43,10 @@ struct GroupQuantArgs {
   int M, K;
   uint8_t* codes;   // [M + 1][64 ceil(K / 128)]
   uint8_t* scales;  // [M + 1][16 ceil(K / 512)]: a dword per block of the unit, a byte per unit
+  // and, in workgroups of their own, the order of the products (group.hpp)
+  const int32_t* offsets;
+  int G, P, tile_rows, tiles_n, tiles_most;
+  int4* table;
 };
 hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t s);
 
@@ -55,6 +59,7 @@ struct GroupShape {
   const int32_t* offsets; // [G + 1]
   int G;
   int tiles_most;         // row tiles that there can be
+  const int4* table;      // null, or the order of the products (group.hpp)
   void* Y;                // [P][gated ? N / 2 : N]
 };
 struct MxGroupArgs : GroupShape {
@@ -68,6 +73,7 @@ struct Int8GroupArgs : GroupShape {
 // Tile shapes (features x rows): 256 x 256, 128 x 128, 128 x 64.
 enum class GroupTile { L, S, T };
 int group_tile_rows(GroupTile t);
+int group_tile_features(GroupTile t);  // of the weight, gate and up counted
 GroupTile pick_group_tile(int64_t P, int64_t groups, bool int8);
 hipError_t launch_mx_grouped(const MxGroupArgs& a, GroupTile t, int type, hipStream_t s);
 hipError_t launch_int8_grouped(const Int8GroupArgs& a, GroupTile t, hipStream_t s);

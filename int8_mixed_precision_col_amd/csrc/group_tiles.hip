@@ -5,6 +5,7 @@
 namespace i8mm {
 
 int group_tile_rows(GroupTile t) { return t == GroupTile::S ? 128 : t == GroupTile::T ? 64 : 256; }
+int group_tile_features(GroupTile t) { return t == GroupTile::L ? 256 : 128; }
 
 // By the mean rows of a group: few rows are bound by the weights' bytes, which smaller tiles (more
 // of them at once) bring in faster, and pad less; many rows by the slabs that come into LDS per

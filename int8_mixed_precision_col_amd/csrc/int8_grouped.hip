@@ -87,7 +87,7 @@ template <class C, bool GATED>
 __global__ __launch_bounds__(C::NT) void k_int8_grouped(Int8GroupArgs g, int tiles_n) {
   RowTile tile;
   int tn;
-  if (!group_tile_of<C>(g, tiles_n, tile, tn)) return;
+  if (!group_tile_of<C, false>(g, tiles_n, tile, tn)) return;
   const int n0 = tn * (GATED ? C::TN / 2 : C::TN);
   if (tile.group < 0) {
     zero_tile<C, GATED>(g, tile, n0);

@@ -9,13 +9,19 @@ namespace i8mm {
 
 // Rows of X, one after the other, so that the GEMM can take any of them: 64 bytes of codes per
 // slab, and 16 bytes of scales per quad (dword b: block b of each unit, byte u: unit u). Lane l of
-// a wave holds row l / 16 of four, elements 8 (l % 16) .. + 7 of each unit of a quad.
+// a wave holds row l / 16 of four, elements 8 (l % 16) .. + 7 of each unit of a quad. The first
+// `parts` workgroups make the table of the products' order meanwhile.
 template <class T>
-__global__ __launch_bounds__(256) void k_group_quantize(GroupQuantArgs a) {
+__global__ __launch_bounds__(256) void k_group_quantize(GroupQuantArgs a, int parts) {
+  if (static_cast<int>(blockIdx.x) < parts) {
+    make_group_order<256>(a.offsets, a.G, a.P, a.tile_rows, a.tiles_n, a.tiles_most, a.table, blockIdx.x, parts);
+    return;
+  }
   const int lane = threadIdx.x & 63, r = 4 * (threadIdx.x >> 6) + (lane >> 4), c = lane & 15;
   const int quads = mx_quads(a.K), ks = mx_ks(a.K);
-  const int64_t grp = blockIdx.x / quads;
-  const int q = blockIdx.x - static_cast<int>(grp) * quads;
+  const int block = blockIdx.x - parts;
+  const int64_t grp = block / quads;
+  const int q = block - static_cast<int>(grp) * quads;
   const int64_t row = grp * 16 + r;
   const uint16_t* src = static_cast<const uint16_t*>(a.X) + row * a.ldx;
   v4u x[4];
@@ -39,9 +45,12 @@ __global__ __launch_bounds__(256) void k_group_quantize(GroupQuantArgs a) {
 }
 
 hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(a.M / 16 + 1) * mx_quads(a.K);
-  if (type == kMxF16) hipLaunchKernelGGL(k_group_quantize<F16>, dim3(blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_group_quantize<B16>, dim3(blocks), dim3(256), 0, s, a);
+  // an entry or two of the table per thread, as far as 64 workgroups go
+  const int64_t entries = static_cast<int64_t>(a.tiles_n) * a.tiles_most;
+  const int parts = static_cast<int>(entries < 64 * 256 ? (entries + 255) / 256 : 64);
+  const unsigned blocks = static_cast<unsigned>(a.M / 16 + 1) * mx_quads(a.K) + parts;
+  if (type == kMxF16) hipLaunchKernelGGL(k_group_quantize<F16>, dim3(blocks), dim3(256), 0, s, a, parts);
+  else hipLaunchKernelGGL(k_group_quantize<B16>, dim3(blocks), dim3(256), 0, s, a, parts);
   return hipGetLastError();
 }
 
@@ -51,7 +60,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n
   typedef MxBlock<C, true> Block;
   RowTile tile;
   int tn;
-  if (!group_tile_of<C>(g, tiles_n, tile, tn)) return;
+  if (!group_tile_of<C, true>(g, tiles_n, tile, tn)) return;
   const int n0 = tn * (GATED ? C::TN / 2 : C::TN);
   if (tile.group < 0) {
     zero_tile<C, GATED>(g, tile, n0);
