@@ -91,17 +91,12 @@ __device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, 
   return true;
 }
 
-// silu(g) u = g u / (1 + exp(-g)), within 9 units of 2^-24 relative, by t = exp(-|g|) <= 1, so that
-// nothing overflows: g u / (1 + t), and g u t / (1 + t) for negative g. 64 of them per lane follow a
-// 256 x 256 tile: with expf and an IEEE quotient they took 7 of its 44 us at K = 4096. t is 2^p with
-// the rounding of p put back; the exponential and reciprocal instructions are within one unit in
-// the last place. |g| beyond 100 counts as 100 there (t is 0).
+// silu(g) u = g u / (1 + exp(-g)), within |g| + 7 units of 2^-24 relative: exp as 2^p, p rounded, by
+// the exponential and reciprocal instructions (each within one unit in the last place). Where exp is
+// above 2^126 the result is 0 (it is below 2^-119 u). 64 of them per lane follow a 256 x 256 tile: with
+// expf and an IEEE quotient they took 7 of its 44 us at K = 4096, so 3.
 __device__ __forceinline__ float silu_up(float g, float u) {
-  constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
-  const float x = -fminf(fabsf(g), 100.0f);
-  const float p = x * kLog2e, low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -p));
-  const float e = __builtin_amdgcn_exp2f(p), t = __builtin_fmaf(e, low * kLn2, e);
-  return g * (g < 0.0f ? t : 1.0f) * __builtin_amdgcn_rcpf(1.0f + t) * u;
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
 // Rounds the wave's part of the tile into its slice of the ring and stores whole row segments, 16
