@@ -139,5 +139,11 @@ __device__ __forceinline__ void store_tile(const GroupShape& g, const RowTile& t
 using GroupL = GemmCfg<256, 256, 64, 2, 4, 4>;
 using GroupS = GemmCfg<128, 128, 64, 2, 4, 4>;
 using GroupT = GemmCfg<128, 64, 64, 2, 2, 4>;
+// MX4 takes a tile of at most 128 rows by this one where others have 256: all waves on these rows, and
+// a quarter less to bring per slab (768 tokens, 8 of 64 experts of 4096 x 1280 109 -> 105 us). With
+// int8 both in one kernel spill.
+struct GroupH : GemmCfg<256, 128, 64, 2, 4, 4> {
+  typedef GroupL Ring;
+};
 
 }  // namespace i8mm

@@ -70,11 +70,11 @@ struct MxGroupArgs : GroupShape {
 struct Int8GroupArgs : GroupShape {
   GemmArgs q;             // Xq, a_x, Xo, o_stride, idx, count, max_outliers of X; Wq, a_w of all groups
 };
-// Tile shapes (features x rows): 256 x 256, 128 x 128, 128 x 64.
+// Tile shapes (features x rows): 256 x 256, 128 x 128 (int8 only), 128 x 64.
 enum class GroupTile { L, S, T };
 int group_tile_rows(GroupTile t);
 int group_tile_features(GroupTile t);  // of the weight, gate and up counted
-GroupTile pick_group_tile(int64_t P, int64_t groups, bool int8);
+GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t K, bool int8);
 hipError_t launch_mx_grouped(const MxGroupArgs& a, GroupTile t, int type, hipStream_t s);
 hipError_t launch_int8_grouped(const Int8GroupArgs& a, GroupTile t, hipStream_t s);
 

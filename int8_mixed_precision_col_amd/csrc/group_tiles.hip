@@ -9,16 +9,19 @@ int group_tile_features(GroupTile t) { return t == GroupTile::L ? 256 : 128; }
 
 // By the mean rows of a group: few rows are bound by the weights' bytes, which smaller tiles (more
 // of them at once) bring in faster, and pad less; many rows by the slabs that come into LDS per
-// product, fewest in the largest tiles. Measured (us per call in a graph, X's quantization
-// included, 128 x 64 / 128 x 128 / 256 x 256), MX4: mean 3 rows of 64 groups, K x N 2048 x 1536 22.4
-// / 25.0 / 37.4; 32 rows, 4096 x 2560 85 / 91 / 108; 128 rows 134 / 132 / 133, of 2048 x 1536 55 / 58 /
-// 60; 512 rows, 4096 x 2560 369 / 343 / 305, of 8 groups, 4096 x 8192 157 / 142 / 131. int8: 23 rows of
-// 10 groups, 1040 x 528 22.6 / 23.0 / 33; 64 rows of 64, 2048 x 1536 78 / 75 / 99; 256 rows of 16 54 / 45 /
-// 57; 512 rows of 64 237 / 214 / 195.
-GroupTile pick_group_tile(int64_t P, int64_t groups, bool int8) {
+// product, fewest in the largest tiles. Measured, us per call in a graph, X's quantization included,
+// with tiles of 64 / 128 / 256 rows.
+// MX4, 64 experts, K x N 4096 x 2560, mean rows 48 86 / 91 / 94, 64 95 / 97 / 98, 96 112 / 108 / 105, 128
+// 130 / 126 / 114, 256 203 / 183 / 153; of 2048 x 1536, 64 37 / 38 / 41, 128 50 / 50 / 49; of 1280 x 4096, 64
+// 67 / 68 / 69, 128 100 / 93 / 85; 8 experts of 4096 x 8192, 32 41 / 41 / 37, 128 61 / 59 / 66, 256 90 / 85 /
+// 76. A short K leaves a large tile mostly its start and end: 768 x 2048, 128 31 / 32 / 36, 256 69 / 63 / 58.
+// (128 rows are best nowhere by more than 10%, and left out.)
+// int8, 64 experts of 2048 x 1536, 16 55 / 63 / 83, 32 64 / 66 / 82, 64 73 / 69 / 84, 128 91 / 90 / 89, 256 132 /
+// 120 / 128, 512 237 / 214 / 195; 8 experts of 4096 x 4096, 128 69 / 68 / 71, 256 94 / 87 / 78.
+GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t K, bool int8) {
   const int64_t rows = P / (groups < P ? groups : P);
-  if (rows <= (int8 ? 48 : 128)) return GroupTile::T;
-  return rows <= 256 ? GroupTile::S : GroupTile::L;
+  if (int8) return rows <= 48 ? GroupTile::T : rows <= 256 ? GroupTile::S : GroupTile::L;
+  return rows <= (K <= 1024 ? 160 : 72) ? GroupTile::T : GroupTile::L;
 }
 
 }  // namespace i8mm

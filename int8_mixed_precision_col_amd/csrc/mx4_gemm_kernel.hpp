@@ -11,9 +11,13 @@ namespace i8mm {
 #define I8MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
 template <class C>
-__device__ __forceinline__ char* scale_buf() {
+__device__ __forceinline__ char* ring_scales() {
   __shared__ __attribute__((aligned(1024))) char buf[(C::TN + C::TM) / 16 * 256];
   return buf;
+}
+template <class C>
+__device__ __forceinline__ char* scale_buf() {
+  return ring_scales<typename C::Ring>();
 }
 
 // One workgroup's walk over the slabs of a tile. ROWS: the activations are held row by row, 64

@@ -55,17 +55,9 @@ hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t 
 }
 
 template <class C, class T, bool GATED>
-__global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n) {
+__device__ __forceinline__ void mx_group_tile(const MxGroupArgs& g, const RowTile& tile, int n0) {
   static_assert(C::STAGES == 4, "a quad of slabs is one turn of the ring");
   typedef MxBlock<C, true> Block;
-  RowTile tile;
-  int tn;
-  if (!group_tile_of<C, true>(g, tiles_n, tile, tn)) return;
-  const int n0 = tn * (GATED ? C::TN / 2 : C::TN);
-  if (tile.group < 0) {
-    zero_tile<C, GATED>(g, tile, n0);
-    return;
-  }
   Block b;
   const int tid = threadIdx.x, vw = tid >> 6;
   b.lane = tid & 63;
@@ -150,6 +142,25 @@ __global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n
   });
 }
 
+template <class C, class T, bool GATED>
+__global__ __launch_bounds__(C::NT) void k_mx_grouped(MxGroupArgs g, int tiles_n) {
+  RowTile tile;
+  int tn;
+  if (!group_tile_of<C, true>(g, tiles_n, tile, tn)) return;
+  const int n0 = tn * (GATED ? C::TN / 2 : C::TN);
+  if (tile.group < 0) {
+    zero_tile<C, GATED>(g, tile, n0);
+    return;
+  }
+  if constexpr (C::TM == 256) {
+    if (tile.rows <= GroupH::TM) {
+      mx_group_tile<GroupH, T, GATED>(g, tile, n0);
+      return;
+    }
+  }
+  mx_group_tile<C, T, GATED>(g, tile, n0);
+}
+
 template <class C, bool GATED>
 static hipError_t run(const MxGroupArgs& g, int type, hipStream_t s) {
   constexpr int OUT = GATED ? C::TN / 2 : C::TN;
@@ -167,7 +178,6 @@ static hipError_t run(const MxGroupArgs& g, int type, hipStream_t s) {
 
 hipError_t launch_mx_grouped(const MxGroupArgs& g, GroupTile t, int type, hipStream_t s) {
   if (t == GroupTile::L) return run<GroupL>(g, type, s);
-  if (t == GroupTile::S) return run<GroupS>(g, type, s);
   return run<GroupT>(g, type, s);
 }
 
