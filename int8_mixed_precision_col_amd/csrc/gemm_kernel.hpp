@@ -57,7 +57,6 @@ struct GemmCfg {
   static_assert(AI * 1024 * NW == A_BYTES && BI * 1024 * NW == B_BYTES, "tile / wave mismatch");
   static_assert(BK == 64 && WTN % 32 == 0 && WTM % 32 == 0, "shape");
   static_assert(STAGES >= 2 && STAGES <= 4, "stages");
-  typedef GemmCfg Ring;  // whose LDS ring it runs on (a smaller tile may use a larger one's)
 };
 
 // XOR swizzle of the 16-byte chunk index within an LDS row. For the fragment reads
@@ -131,13 +130,9 @@ __device__ __forceinline__ void wait_and_barrier() {
 // stage a DMA writes and a fragment read reads (a single array indexed by stage makes
 // it wait for every outstanding DMA before each read).
 template <class C, int S>
-__device__ __forceinline__ char* ring_stage() {
+__device__ __forceinline__ char* stage_buf() {
   __shared__ __attribute__((aligned(1024))) char buf[C::STAGE];
   return buf;
-}
-template <class C, int S>
-__device__ __forceinline__ char* stage_buf() {
-  return ring_stage<typename C::Ring, S>();
 }
 
 // The LDS slice of wave w for staging its fp16 output sub-tile (WTM rows of WTN halves):

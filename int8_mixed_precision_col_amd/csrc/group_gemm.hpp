@@ -13,6 +13,23 @@
 
 namespace i8mm {
 
+// 256 x 256 and 128 x 128 (features x rows) on 8 waves, 128 x 64 on 4; 4-stage rings.
+using GroupL = GemmCfg<256, 256, 64, 2, 4, 4>;
+using GroupS = GemmCfg<128, 128, 64, 2, 4, 4>;
+using GroupT = GemmCfg<128, 64, 64, 2, 2, 4>;
+// What MX4 takes a tile of at most 128 rows by where others have 256, on their ring: all waves on these
+// rows, and a quarter less to bring per slab (768 tokens, 8 of 64 experts of 4096 x 1280 109 -> 105
+// us). With int8 both in one kernel spill.
+using GroupH = GemmCfg<256, 128, 64, 2, 4, 4>;
+template <>
+__device__ __forceinline__ char* stage_buf<GroupH, 0>() { return stage_buf<GroupL, 0>(); }
+template <>
+__device__ __forceinline__ char* stage_buf<GroupH, 1>() { return stage_buf<GroupL, 1>(); }
+template <>
+__device__ __forceinline__ char* stage_buf<GroupH, 2>() { return stage_buf<GroupL, 2>(); }
+template <>
+__device__ __forceinline__ char* stage_buf<GroupH, 3>() { return stage_buf<GroupL, 3>(); }
+
 // A tile's group (-1: rows behind the last group's), its first row and its rows, 1 .. TM.
 struct RowTile {
   int group, first, rows;
@@ -134,16 +151,5 @@ __device__ __forceinline__ void store_tile(const GroupShape& g, const RowTile& t
       *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.Y) + static_cast<size_t>(tile.first + m) * N + n) = v;
   }
 }
-
-// 256 x 256 and 128 x 128 (features x rows) on 8 waves, 128 x 64 on 4; 4-stage rings.
-using GroupL = GemmCfg<256, 256, 64, 2, 4, 4>;
-using GroupS = GemmCfg<128, 128, 64, 2, 4, 4>;
-using GroupT = GemmCfg<128, 64, 64, 2, 2, 4>;
-// MX4 takes a tile of at most 128 rows by this one where others have 256: all waves on these rows, and
-// a quarter less to bring per slab (768 tokens, 8 of 64 experts of 4096 x 1280 109 -> 105 us). With
-// int8 both in one kernel spill.
-struct GroupH : GemmCfg<256, 128, 64, 2, 4, 4> {
-  typedef GroupL Ring;
-};
 
 }  // namespace i8mm

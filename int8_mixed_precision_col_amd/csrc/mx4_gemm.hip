@@ -68,7 +68,7 @@ __global__ __launch_bounds__(C::NT) void k_mx_gemm(MxGemmArgs g, int tiles_m, in
   static_assert(C::STAGES == 4, "a quad of slabs is one turn of the ring");
   int tn, tm;
   tile_of(blockIdx.x, gridDim.x, tiles_m, group_m, tn, tm);
-  MxBlock<C, false> b;
+  MxBlock<C, false> b{};
   const int tid = threadIdx.x, vw = tid >> 6;
   b.lane = tid & 63;
   b.wave = __builtin_amdgcn_readfirstlane(vw);

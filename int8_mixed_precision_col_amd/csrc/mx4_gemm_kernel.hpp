@@ -11,13 +11,9 @@ namespace i8mm {
 #define I8MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
 template <class C>
-__device__ __forceinline__ char* ring_scales() {
+__device__ __forceinline__ char* scale_buf() {
   __shared__ __attribute__((aligned(1024))) char buf[(C::TN + C::TM) / 16 * 256];
   return buf;
-}
-template <class C>
-__device__ __forceinline__ char* scale_buf() {
-  return ring_scales<typename C::Ring>();
 }
 
 // One workgroup's walk over the slabs of a tile. ROWS: the activations are held row by row, 64
@@ -43,12 +39,12 @@ struct MxBlock {
   // layout's padding scales of both sides, 2^-254 together, and add nothing in fp32.
   template <int S>
   __device__ __forceinline__ void issue_one(int kt, int q) {
-    const size_t slab = static_cast<size_t>(min(kt, ks - 1));
+    const size_t step = static_cast<size_t>(min(kt, ks - 1)) * kUnitBytes;
     char* base = stage_buf<C, S>();
     if (q < C::AI)
-      dma16<0>(a_base + slab * kUnitBytes + a_off[q], I8MM_LDS(base + (q * C::NW + wave) * 1024));
+      dma16<0>(a_base + step + a_off[q], I8MM_LDS(base + (q * C::NW + wave) * 1024));
     else
-      dma16<0>(b_base + slab * (ROWS ? kUnitK : kUnitBytes) + b_off[q - C::AI],
+      dma16<0>(b_base + (ROWS ? step / kUnitRows : step) + b_off[q - C::AI],
                I8MM_LDS(base + C::A_BYTES + ((q - C::AI) * C::NW + wave) * 1024));
   }
   template <int S>

@@ -7,6 +7,9 @@
 
 namespace i8mm {
 
+template <>
+__device__ __forceinline__ char* scale_buf<GroupH>() { return scale_buf<GroupL>(); }
+
 // Rows of X, one after the other, so that the GEMM can take any of them: 64 bytes of codes per
 // slab, and 16 bytes of scales per quad (dword b: block b of each unit, byte u: unit u). Lane l of
 // a wave holds row l / 16 of four, elements 8 (l % 16) .. + 7 of each unit of a quad. The first
