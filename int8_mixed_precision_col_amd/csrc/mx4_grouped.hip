@@ -78,7 +78,7 @@ __device__ __forceinline__ void mx_group_tile(const MxGroupArgs& g, const RowTil
 #pragma unroll
   for (int i = 0; i < C::AI; ++i) {
     const int p = (i * C::NW + b.wave) * 64 + b.lane, r = p / C::CPR, c = (p % C::CPR) ^ swz<C::CPR>(r);
-    b.a_off[i] = static_cast<unsigned>(weight_group<GATED>(r >> 4, n0, g.N) * b.ks * kUnitBytes + (r & 15) * kUnitK + c * 16);
+    b.a_off[i] = static_cast<unsigned>(weight_group<GATED>(r >> 4, n0, g.N)) * (b.ks * kUnitBytes) + (r & 15) * kUnitK + c * 16;
   }
 #pragma unroll
   for (int i = 0; i < C::BI; ++i) {
@@ -91,7 +91,7 @@ __device__ __forceinline__ void mx_group_tile(const MxGroupArgs& g, const RowTil
     const int sw = b.wave % Block::SI, xw = sw - C::TN / 64;
     if (xw < 0) {
       b.s_base = reinterpret_cast<const uint8_t*>(g.Ws) + first_group * b.quads * 256;
-      b.s_off = static_cast<unsigned>(weight_group<GATED>(4 * sw + (b.lane >> 4), n0, g.N) * b.quads * 256 + 16 * (b.lane & 15));
+      b.s_off = static_cast<unsigned>(weight_group<GATED>(4 * sw + (b.lane >> 4), n0, g.N)) * (b.quads * 256) + 16 * (b.lane & 15);
       b.s_step = 256;
     } else {
       b.s_base = g.Xs;

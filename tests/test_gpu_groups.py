@@ -164,6 +164,35 @@ def test_grouped_each_tile_shape(E, n, fmt):
     check_grouped(x, weight, values, fmt, sizes, rows, P, False)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+@pytest.mark.parametrize("edge", [64, 128, 256])
+def test_grouped_groups_at_the_edges_of_tiles(edge, fmt, gated):
+    """Groups of a tile's rows, one less and one more, and twice that, beside empty ones, with means
+    that take each tile shape; features past a whole tile."""
+    announce(f"grouped at {edge} rows {fmt} gated={gated}")
+    sizes = [edge, 0, edge - 1, edge + 1, 2 * edge, 2 * edge - 1, 0, 2 * edge + 1]
+    x, (weight, values) = activations(60, 528, F16, edge), weights_of(8, 288, 528, fmt, F16, edge)
+    P = sum(sizes)
+    check_grouped(x, weight, values, fmt, sizes, np.arange(P) % 60, P, gated)
+    off = np.full(P, -1)               # no row at all
+    assert int(torch.count_nonzero(moe.grouped_matmul(x, weight, i32(offsets_of(sizes)), i32(off), gated))) == 0
+
+
+def test_grouped_one_experts_weight_beyond_2_31_bytes():
+    N, K = 139264, 32768
+    announce(f"grouped mx4 with experts of {N} x {K}")
+    w, x = (torch.randn((32, K), generator=gen(80)) * 0.05).half(), activations(5, K, F16, 81)
+    tail = mx4.prepare_weight(w.cuda(), 1)
+    codes = torch.zeros((N // 16, K // 128, 16, 64), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((N // 16, K // 512, 64, 4), dtype=torch.uint8, device="cuda")
+    codes[-2:], scales[-2:] = tail
+    y = moe.grouped_matmul(x, (codes, scales), i32([0, 5]))
+    want = ref.grouped_mx4(f64(x), mx4_oracle.mx4_round(f64(w))[None], [0, 5], None, 5, False)
+    close(y[:, -32:], *want)
+    assert int(torch.count_nonzero(y[:, :-32])) == 0
+
+
 @pytest.mark.parametrize("fmt", ["mx4", "int8"])
 def test_grouped_rows_out_of_range_are_zeros_and_offsets_stay_inside(fmt):
     announce(f"grouped, rows and offsets out of range, {fmt}")
@@ -328,6 +357,46 @@ def test_lora_wide_ranges_in_fp16(M):
     t["A"] = (t["A"].float() * 256).half()
     t["B"] = (t["B"].float() / 4096).half()
     close(lora.apply(**t), *want_lora(t))
+
+
+def test_lora_of_rows_that_are_not_finite():
+    announce("lora, rows with NaN and infinities")
+    for M in (6, 90):
+        t = lora_case(M, 272, 144, 16, 3, F16, M, False)
+        t["ids"].fill_(1)
+        want = lora.apply(**t)
+        t["X"][2, 5], t["X"][4, 271] = float("nan"), float("inf")
+        got = lora.apply(**t)
+        bad = torch.zeros(M, dtype=torch.bool)
+        bad[2] = bad[4] = True
+        assert bool(torch.isnan(got[bad.cuda()]).all()) and torch.equal(got[~bad.cuda()], want[~bad.cuda()])
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+def test_lora_whole_batch_of_one_adapter_and_of_none(dtype):
+    announce(f"lora, one adapter and none, {dtype}")
+    for M in (33, 64, 640):
+        t = lora_case(M, 528, 272, 32, 2, dtype, M, False)
+        t["ids"].fill_(1)
+        close(lora.apply(**t), *want_lora(t))
+        t["ids"].fill_(-1)
+        assert torch.equal(lora.apply(**t), t["Y"])
+
+
+def test_lora_many_rows_and_offsets_beyond_32_bits():
+    """Over 4 GB of X and of Y: the last rows are right, and rows far apart share a tile."""
+    M, K, N = 140000, 16384, 16400
+    announce(f"lora M={M} K={K} N={N}")
+    Y, X = (torch.zeros((M, w), dtype=B16, device="cuda") for w in (N, K))
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    pick = [0, 1, M // 2, M - 2, M - 1]
+    small = lora_case(5, K, N, 16, 2, B16, 7, False)
+    X[pick], Y[pick] = small["X"], small["Y"]
+    small["ids"] = torch.tensor([1, 0, 1, 0, 1], dtype=torch.int32, device="cuda")
+    ids[pick] = small["ids"]
+    got = lora.apply(Y, X, small["A"], small["B"], ids, scales=small["scales"], out=Y)
+    close(got[pick], *want_lora(small))
+    assert int(torch.count_nonzero(got)) <= 5 * N
 
 
 # ---- streams, graphs, large operands ----
