@@ -115,21 +115,21 @@ struct LoraTile {
 __device__ __forceinline__ bool lora_tile(const LoraArgs& a, int b, int* row_of, LoraTile& t) {
   const int tid = threadIdx.x, lane = tid & 63;
   if (a.M <= kLoraFew) {
-    // every wave finds the rows whose id no earlier row has: the b-th of them leads tile b
-    const int id0 = lane < a.M ? a.ids[lane] : -2;
-    const int id = lane >= a.M ? -2 : id0 >= 0 && id0 < a.S ? id0 : -1;
-    unsigned long long mine = 0, leaders = 0;
-    for (int m = 0; m < a.M; ++m) {
-      const unsigned long long same = __ballot(id == __builtin_amdgcn_readlane(id, m));
-      if (__builtin_ctzll(same) == m) {
-        if (__builtin_popcountll(leaders) == b) {
-          mine = same;
-          t.adapter = __builtin_amdgcn_readlane(id, m);
-        }
-        leaders |= 1ull << m;
-      }
+    // every wave finds each row's rows of equal id, by a ballot per bit of its number; the b-th row
+    // that no such row is in front of leads tile b
+    const int id = a.ids[min(lane, a.M - 1)], g = id >= 0 && id < a.S ? id : a.S;
+    unsigned long long same = __ballot(lane < a.M);
+    for (int bit = 0; bit < 32 - __builtin_clz(a.S); ++bit) {
+      const unsigned long long set = __ballot(g >> bit & 1);
+      same &= g >> bit & 1 ? set : ~set;
     }
-    if (mine == 0) return false;
+    const unsigned long long leaders = __ballot(lane < a.M && __builtin_ctzll(same) == lane);
+    if (b >= __builtin_popcountll(leaders)) return false;
+    const int who = __builtin_ctzll(__ballot((leaders >> lane & 1) && __builtin_popcountll(leaders & ((1ull << lane) - 1ull)) == b));
+    const unsigned long long mine = static_cast<unsigned long long>(static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(same), who))) |
+                                    static_cast<unsigned long long>(static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(same >> 32), who))) << 32;
+    const int adapter = __builtin_amdgcn_readlane(g, who);
+    t.adapter = adapter < a.S ? adapter : -1;
     t.rows = __builtin_popcountll(mine);
     if (tid < 64 && (mine >> lane & 1)) row_of[__builtin_popcountll(mine & ((1ull << lane) - 1ull))] = lane;
   } else {
@@ -463,11 +463,12 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
   typedef LoraStaged<T, KS> Staged;
   typedef typename Staged::v8e v8e;
   constexpr int LR = 32 * KS + 8;  // padded row of V in LDS
+  typedef typename T::elem Parts[2][kLoraRows][LR];
   __shared__ int row_of[kLoraRows];
-  __shared__ __attribute__((aligned(16))) typename T::elem v[2][kLoraRows][LR];
   __shared__ float row_scale[kLoraRows];
   __shared__ __attribute__((aligned(1024))) char buf0[Staged::BYTES];
-  __shared__ __attribute__((aligned(1024))) char buf1[Staged::BYTES];
+  __shared__ __attribute__((aligned(1024))) char buf1[sizeof(Parts) > Staged::BYTES ? sizeof(Parts) : Staged::BYTES];
+  Parts& v = *reinterpret_cast<Parts*>(buf1);  // until it is in registers
   LoraTile tile;
   if (!lora_tile(a, blockIdx.x, row_of, tile)) return;
   const int n0 = blockIdx.y * span, n1 = min(n0 + span, a.N);
@@ -498,6 +499,7 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
   lora_gather_v<T, KS, 64 * kStagedWaves, kLoraSplits>(a, tile, row_of, v, row_scale);
   wait_and_barrier<0>();
   if (16 * wave >= tile.rows) {  // no rows: only its share of B
+    lds_barrier();
     for (int n = n0; n < n1; n += 256) {
       if (n > n0) wait_and_barrier<0>();
       st.bring(buf1, n + 128);
@@ -517,6 +519,7 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
   float sc[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sc[e] = row_scale[min(16 * wave + 4 * st.lq + e, tile.rows - 1)];
+  lds_barrier();  // every wave has its V: the second buffer is free
   auto step = [&](const char* buf, char* other, v4u (&y)[4], int n) {
     st.bring(other, n + 128);
     asm volatile("" ::: "memory");  // what is asked for from here on comes after B's share: the next wait counts on it
