@@ -50,7 +50,7 @@ struct GroupedLayout {
 };
 GroupedLayout grouped_layout(int64_t M, int64_t K, int64_t P, int64_t E, int64_t N, int format, int64_t max_outliers) {
   GroupedLayout L;
-  L.tile = i8mm::pick_group_tile(P, E, K, format == 0);
+  L.tile = i8mm::pick_group_tile(P, E, N, K, format == 0);
   const int64_t features = i8mm::group_tile_features(L.tile);
   L.tiles_n = int((N + features - 1) / features);
   L.tiles_most = int(i8mm::group_tiles_most(P, E, i8mm::group_tile_rows(L.tile)));

@@ -74,7 +74,7 @@ struct Int8GroupArgs : GroupShape {
 enum class GroupTile { L, S, T };
 int group_tile_rows(GroupTile t);
 int group_tile_features(GroupTile t);  // of the weight, gate and up counted
-GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t K, bool int8);
+GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t N, int64_t K, bool int8);
 hipError_t launch_mx_grouped(const MxGroupArgs& a, GroupTile t, int type, hipStream_t s);
 hipError_t launch_int8_grouped(const Int8GroupArgs& a, GroupTile t, hipStream_t s);
 

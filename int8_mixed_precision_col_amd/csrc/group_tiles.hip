@@ -18,10 +18,16 @@ int group_tile_features(GroupTile t) { return t == GroupTile::L ? 256 : 128; }
 // (128 rows are best nowhere by more than 10%, and left out.)
 // int8, 64 experts of 2048 x 1536, 16 55 / 63 / 83, 32 64 / 66 / 82, 64 73 / 69 / 84, 128 91 / 90 / 89, 256 132 /
 // 120 / 128, 512 237 / 214 / 195; 8 experts of 4096 x 4096, 128 69 / 68 / 71, 256 94 / 87 / 78.
-GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t K, bool int8) {
-  const int64_t rows = P / (groups < P ? groups : P);
-  if (int8) return rows <= 48 ? GroupTile::T : rows <= 256 ? GroupTile::S : GroupTile::L;
-  return rows <= (K <= 1024 ? 160 : 72) ? GroupTile::T : GroupTile::L;
+// With few tiles in all, CUs stay idle for the whole time of a large one: 64 / 256 rows, MX4, 27 tiles
+// of 256 rows (10 experts of 1040 x 528) 8.8 / 16.3, 128 (16 of 2048 x 2048) 19 / 23, 160 (4 of 4096 x 4096) 44 /
+// 37, 192 (16 of 2048 x 2048) 27 / 26; int8, 64 / 128 rows, 256 tiles of 128 (16 of 2048 x 2048) 32 / 35, 384 40 / 39.
+GroupTile pick_group_tile(int64_t P, int64_t groups, int64_t N, int64_t K, bool int8) {
+  const int64_t used = groups < P ? groups : P, rows = P / used;
+  // tiles of f features x r rows, half of one more per group
+  auto tiles = [&](int f, int r) { return (N + f - 1) / f * (P / r + used / 2); };
+  if (rows > (int8 ? 256 : K <= 1024 ? 160 : 72) && tiles(256, 256) >= 160) return GroupTile::L;
+  if (int8 && rows > 48 && tiles(128, 128) >= 320) return GroupTile::S;
+  return GroupTile::T;
 }
 
 }  // namespace i8mm

@@ -166,17 +166,33 @@ def test_grouped_each_tile_shape(E, n, fmt):
 
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("fmt", ["mx4", "int8"])
-@pytest.mark.parametrize("edge", [64, 128, 256])
-def test_grouped_groups_at_the_edges_of_tiles(edge, fmt, gated):
-    """Groups of a tile's rows, one less and one more, and twice that, beside empty ones, with means
-    that take each tile shape; features past a whole tile."""
-    announce(f"grouped at {edge} rows {fmt} gated={gated}")
+@pytest.mark.parametrize("edge,N", [(64, 288), (128, 288), (64, 5152), (128, 5152), (256, 5152)])
+def test_grouped_groups_at_the_edges_of_tiles(edge, N, fmt, gated):
+    """Groups of a tile's rows, one less and one more, and twice that, beside empty ones; features past a
+    whole tile, and enough of them that the means take each tile shape."""
+    announce(f"grouped at {edge} rows N={N} {fmt} gated={gated}")
     sizes = [edge, 0, edge - 1, edge + 1, 2 * edge, 2 * edge - 1, 0, 2 * edge + 1]
-    x, (weight, values) = activations(60, 528, F16, edge), weights_of(8, 288, 528, fmt, F16, edge)
+    x, (weight, values) = activations(60, 272, F16, edge), weights_of(8, N, 272, fmt, F16, edge)
     P = sum(sizes)
     check_grouped(x, weight, values, fmt, sizes, np.arange(P) % 60, P, gated)
     off = np.full(P, -1)               # no row at all
     assert int(torch.count_nonzero(moe.grouped_matmul(x, weight, i32(offsets_of(sizes)), i32(off), gated))) == 0
+
+
+@pytest.mark.parametrize("fmt,dtype", [("mx4", F16), ("mx4", B16), ("int8", F16)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("sizes,T,K,N", [([0, 700, 0, 3, 128, 801, 1], 333, 272, 8224), ([300, 0, 5, 92], 50, 1040, 16416),
+                                         ([400, 129, 600], 77, 144, 10272)])
+def test_grouped_large_tiles(sizes, T, K, N, gated, fmt, dtype):
+    """Enough rows and features for tiles of 256 and 128 rows: partial ones, empty groups, rows behind
+    the last group."""
+    announce(f"grouped {sizes} T={T} K={K} N={N} gated={gated} {fmt} {dtype}")
+    x, (weight, values) = activations(T, K, dtype, T + K), weights_of(len(sizes), N, K, fmt, dtype, K + N)
+    n = sum(sizes)
+    rows = np.full(n + 300, -1)
+    rows[:n] = torch.randint(0, T, (n,), generator=gen(n)).numpy()
+    y = check_grouped(x, weight, values, fmt, sizes, rows, n + 300, gated)
+    assert torch.equal(y, moe.grouped_matmul(x, weight, i32(offsets_of(sizes)), i32(rows), gated))
 
 
 def test_grouped_one_experts_weight_beyond_2_31_bytes():
