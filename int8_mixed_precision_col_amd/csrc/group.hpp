@@ -107,4 +107,107 @@ __device__ __forceinline__ void make_group_order(const int* offsets, int G, int 
   }
 }
 
+// The same with tiles of different costs: a last tile of at most `half` rows of a group is
+// kHalfTileCost / kTileCost of the others. The XCDs' runs are of equal cost rather than number, and
+// each takes the groups of the costliest tiles first, so that its last ones are short. A workgroup per
+// group, or several groups to one (part of parts); workgroups number up to 8 of the longest
+// run, entries past a run's end have no rows. Runs too long for `capacity` entries (a multiple of
+// 8), which would take costs far apart, are cut by number.
+constexpr int kTileCost = 16, kHalfTileCost = 9;
+template <int NT>
+__device__ __forceinline__ void make_balanced_order(const int* offsets, int G, int P, int rows, int half, int tiles_n,
+                                                    int most, int capacity, int4* table, int part, int parts) {
+  __shared__ GroupTilesBefore first, cost;  // before a group: tiles, and their cost
+  __shared__ int bound[9];                  // the runs, in products
+  __shared__ int part_sums[NT / 64];
+  const int tid = threadIdx.x;
+  count_group_tiles<NT>(offsets, G, P, rows, first);
+  for (int g = tid; g <= G + 1; g += NT) first[g] = min(first[g], most);  // more come only of offsets that do not ascend
+  __syncthreads();
+  // halves before a group, then the cost
+  {
+    const int per = (G + NT) / NT;
+    auto is_half = [&](int g) {
+      const int n = (g < G ? group_first(offsets, g + 1, P) : P) - group_first(offsets, g, P), rest = n % rows;
+      return n > 0 && rest > 0 && rest <= half ? 1 : 0;
+    };
+    int sum = 0;
+    for (int g = tid * per; g < min((tid + 1) * per, G + 1); ++g) sum += is_half(g);
+    int upto = wave_prefix_sum(sum);
+    if ((tid & 63) == 63) part_sums[tid >> 6] = upto;
+    __syncthreads();
+    for (int w = 0; w < tid >> 6; ++w) upto += part_sums[w];
+    int at = upto - sum;
+    for (int g = tid * per; g < min((tid + 1) * per, G + 1); ++g) {
+      cost[g] = kTileCost * first[g] - (kTileCost - kHalfTileCost) * at;
+      at += is_half(g);
+      if (g == G) cost[G + 1] = kTileCost * first[G + 1] - (kTileCost - kHalfTileCost) * at;
+    }
+    __syncthreads();
+  }
+  const int all = tiles_n * first[G + 1];
+  if (tid < 9) {
+    const int64_t target = static_cast<int64_t>(cost[G + 1]) * tiles_n * tid / 8;
+    int lo = 0, hi = G;  // the last group that starts at or before the target
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(cost[mid]) * tiles_n <= target) lo = mid;
+      else hi = mid - 1;
+    }
+    const int64_t in = target - static_cast<int64_t>(cost[lo]) * tiles_n;
+    const int c = cost[lo + 1] - cost[lo], n = first[lo + 1] - first[lo];
+    bound[tid] = tid == 8 ? all : min(first[lo] * tiles_n + (c > 0 ? static_cast<int>(in * n / c) : 0), all);
+  }
+  __syncthreads();
+  int longest = 0;
+  bool ascending = true;
+  for (int x = 0; x < 8; ++x) {
+    longest = max(longest, bound[x + 1] - bound[x]);
+    ascending = ascending && bound[x + 1] >= bound[x] && bound[x] >= 0;
+  }
+  __syncthreads();
+  if (8 * longest > capacity || !ascending) {
+    if (tid < 9) bound[tid] = static_cast<int>(static_cast<int64_t>(all) * tid / 8);
+    longest = (all + 7) / 8;
+    __syncthreads();
+  }
+  if (part == 0) {
+    if (tid == 0) table[0] = make_int4(8 * longest, 0, 0, 0);
+    for (int e = tid; e < 8 * longest; e += NT)
+      if (e / 8 >= bound[(e & 7) + 1] - bound[e & 7]) table[1 + e] = make_int4(0, 0, 0, 0);
+  }
+  // a group's products in run x, [from, to)
+  auto from = [&](int g, int x) { return max(first[g] * tiles_n, bound[x]); };
+  auto to = [&](int g, int x) { return min(first[g + 1] * tiles_n, bound[x + 1]); };
+  for (int g = part; g <= G; g += parts) {
+    const int tiles = first[g + 1] - first[g], c = cost[g + 1] - cost[g];
+    for (int x = 0; x < 8; ++x) {
+      const int p0 = from(g, x), p1 = to(g, x);
+      if (p0 >= p1) continue;
+      // the products of the run's groups that come first
+      int before = 0;
+      for (int h = tid; h <= G; h += NT) {
+        const int n = to(h, x) - from(h, x);
+        if (n <= 0) continue;
+        const int64_t mine = static_cast<int64_t>(c) * (first[h + 1] - first[h]);
+        const int64_t its = static_cast<int64_t>(cost[h + 1] - cost[h]) * tiles;
+        if (its > mine || (its == mine && h < g)) before += n;
+      }
+      const int sum = __builtin_amdgcn_readlane(wave_prefix_sum(before), 63);
+      __syncthreads();
+      if ((tid & 63) == 0) part_sums[tid >> 6] = sum;
+      __syncthreads();
+      before = 0;
+      for (int w = 0; w < NT / 64; ++w) before += part_sums[w];
+      for (int p = p0 + tid; p < p1; p += NT) {
+        int tm, tn;
+        group_product(p - first[g] * tiles_n, tiles, tiles_n, tm, tn);
+        int4 t = group_tile(offsets, G, P, g, tm, rows);
+        t.w = tn;
+        table[1 + 8 * (before + p - p0) + x] = t;
+      }
+    }
+  }
+}
+
 }  // namespace i8mm

@@ -45,7 +45,7 @@ bool bad_grouped(int64_t M, int64_t K, int64_t P, int64_t E, int64_t N, int form
 // What X is quantized to and, MX4, the order of the products.
 struct GroupedLayout {
   i8mm::GroupTile tile;
-  int tiles_n, tiles_most;
+  int tiles_n, tiles_most, capacity;
   size_t scales = 0, table = 0, total = 0;
 };
 GroupedLayout grouped_layout(int64_t M, int64_t K, int64_t P, int64_t E, int64_t N, int format, int64_t max_outliers) {
@@ -54,12 +54,13 @@ GroupedLayout grouped_layout(int64_t M, int64_t K, int64_t P, int64_t E, int64_t
   const int64_t features = i8mm::group_tile_features(L.tile);
   L.tiles_n = int((N + features - 1) / features);
   L.tiles_most = int(i8mm::group_tiles_most(P, E, i8mm::group_tile_rows(L.tile)));
+  L.capacity = (L.tiles_n * L.tiles_most + 7) / 8 * 8;  // eight equal runs
   if (format == 0) {
     L.total = round256(int8_quant_state_bytes(M, K, max_outliers));
   } else {
     L.scales = round256(size_t(M + 1) * i8mm::mx_ks(K) * i8mm::kUnitK);
     L.table = L.scales + round256(size_t(M + 1) * i8mm::mx_quads(K) * 16);
-    L.total = L.table + round256((1 + size_t(L.tiles_n) * L.tiles_most) * sizeof(int4));
+    L.total = L.table + round256((1 + size_t(L.capacity)) * sizeof(int4));
   }
   return L;
 }
@@ -155,11 +156,12 @@ int moe_grouped_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dty
   uint8_t* scales = reinterpret_cast<uint8_t*>(ws + L.scales);
   int4* table = reinterpret_cast<int4*>(ws + L.table);
   const i8mm::GroupQuantArgs q{X, ldx, int(M), int(K), codes, scales, offsets, int(E), int(P),
-                               i8mm::group_tile_rows(L.tile), L.tiles_n, L.tiles_most, table};
+                               i8mm::group_tile_rows(L.tile), L.tiles_n, L.tiles_most, L.capacity, table};
   const hipError_t e = i8mm::launch_group_quantize(q, dtype, stream);
   if (e != hipSuccess) return INT8MM_E_HIP;
   shape.table = table;
-  const i8mm::MxGroupArgs a{shape, codes, scales, static_cast<const uint8_t*>(w), static_cast<const uint32_t*>(s)};
+  const i8mm::MxGroupArgs a{shape, codes, scales, static_cast<const uint8_t*>(w), static_cast<const uint32_t*>(s),
+                             L.capacity};
   return hip_status(i8mm::launch_mx_grouped(a, L.tile, dtype, stream));
 }
 

@@ -69,7 +69,7 @@ template <class C, bool TABLE>
 __device__ __forceinline__ bool group_tile_of(const GroupShape& g, int tiles_n, RowTile& tile, int& tn) {
   if constexpr (TABLE) {
     const int4 head = g.table[0], t = g.table[1 + blockIdx.x];  // on their way together
-    if (static_cast<int>(blockIdx.x) >= head.x) return false;
+    if (static_cast<int>(blockIdx.x) >= head.x || t.z <= 0) return false;
     tile.group = t.x;
     tile.first = t.y;
     tile.rows = t.z;

@@ -45,7 +45,7 @@ struct GroupQuantArgs {
   uint8_t* scales;  // [M + 1][16 ceil(K / 512)]: a dword per block of the unit, a byte per unit
   // and, in workgroups of their own, the order of the products (group.hpp)
   const int32_t* offsets;
-  int G, P, tile_rows, tiles_n, tiles_most;
+  int G, P, tile_rows, tiles_n, tiles_most, capacity;
   int4* table;
 };
 hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t s);
@@ -66,6 +66,7 @@ struct MxGroupArgs : GroupShape {
   const uint8_t *Xc, *Xs;  // GroupQuantArgs
   const uint8_t* Wc;
   const uint32_t* Ws;
+  int capacity;           // of the order's table, in workgroups
 };
 struct Int8GroupArgs : GroupShape {
   GemmArgs q;             // Xq, a_x, Xo, o_stride, idx, count, max_outliers of X; Wq, a_w of all groups

@@ -17,7 +17,11 @@ __device__ __forceinline__ char* scale_buf<GroupH>() { return scale_buf<GroupL>(
 template <class T>
 __global__ __launch_bounds__(256) void k_group_quantize(GroupQuantArgs a, int parts) {
   if (static_cast<int>(blockIdx.x) < parts) {
-    make_group_order<256>(a.offsets, a.G, a.P, a.tile_rows, a.tiles_n, a.tiles_most, a.table, blockIdx.x, parts);
+    if (a.tile_rows == GroupL::TM)
+      make_balanced_order<256>(a.offsets, a.G, a.P, GroupL::TM, GroupH::TM, a.tiles_n, a.tiles_most, a.capacity, a.table,
+                               blockIdx.x, parts);
+    else
+      make_group_order<256>(a.offsets, a.G, a.P, a.tile_rows, a.tiles_n, a.tiles_most, a.table, blockIdx.x, parts);
     return;
   }
   const int lane = threadIdx.x & 63, r = 4 * (threadIdx.x >> 6) + (lane >> 4), c = lane & 15;
@@ -48,9 +52,9 @@ __global__ __launch_bounds__(256) void k_group_quantize(GroupQuantArgs a, int pa
 }
 
 hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t s) {
-  // an entry or two of the table per thread, as far as 64 workgroups go
-  const int64_t entries = static_cast<int64_t>(a.tiles_n) * a.tiles_most;
-  const int parts = static_cast<int>(entries < 64 * 256 ? (entries + 255) / 256 : 64);
+  // a group per workgroup, or an entry or two of the table per thread, as far as 64 or 256 go
+  const int parts = a.tile_rows == GroupL::TM ? (a.G + 1 < 256 ? a.G + 1 : 256)
+                                              : (a.capacity < 64 * 256 ? (a.capacity + 255) / 256 : 64);
   const unsigned blocks = static_cast<unsigned>(a.M / 16 + 1) * mx_quads(a.K) + parts;
   if (type == kMxF16) hipLaunchKernelGGL(k_group_quantize<F16>, dim3(blocks), dim3(256), 0, s, a, parts);
   else hipLaunchKernelGGL(k_group_quantize<B16>, dim3(blocks), dim3(256), 0, s, a, parts);
@@ -168,7 +172,7 @@ template <class C, bool GATED>
 static hipError_t run(const MxGroupArgs& g, int type, hipStream_t s) {
   constexpr int OUT = GATED ? C::TN / 2 : C::TN;
   const int tiles_n = ((GATED ? g.N / 2 : g.N) + OUT - 1) / OUT;
-  const dim3 grid(static_cast<unsigned>(tiles_n) * g.tiles_most);
+  const dim3 grid(g.capacity);
   if (type == kMxF16) hipLaunchKernelGGL((k_mx_grouped<C, F16, GATED>), grid, dim3(C::NT), 0, s, g, tiles_n);
   else hipLaunchKernelGGL((k_mx_grouped<C, B16, GATED>), grid, dim3(C::NT), 0, s, g, tiles_n);
   return hipGetLastError();
