@@ -109,103 +109,93 @@ __device__ __forceinline__ void make_group_order(const int* offsets, int G, int 
 
 // The same with tiles of different costs: a last tile of at most `half` rows of a group is
 // kHalfTileCost / kTileCost of the others. The XCDs' runs are of equal cost rather than number, and
-// each takes the groups of the costliest tiles first, so that its last ones are short. A workgroup per
-// group, or several groups to one (part of parts); workgroups number up to 8 of the longest
-// run, entries past a run's end have no rows. Runs too long for `capacity` entries (a multiple of
-// 8), which would take costs far apart, are cut by number.
+// each takes the groups of the costliest tiles first, so that its last ones are short. Workgroups
+// number up to 8 of the longest run, entries past a run's end have no rows. Runs too long for
+// `capacity` entries (a multiple of 8), which would take costs far apart, are cut by number.
+// 32768 pairs, 64 experts of 4096 x 1280: the gate and up product 240.6 -> 234.1 us; costs of 7, 8,
+// 11 and 13 in place of 9 come out at 240, 236, 237 and 234.
 constexpr int kTileCost = 16, kHalfTileCost = 9;
 template <int NT>
 __device__ __forceinline__ void make_balanced_order(const int* offsets, int G, int P, int rows, int half, int tiles_n,
                                                     int most, int capacity, int4* table, int part, int parts) {
-  __shared__ GroupTilesBefore first, cost;  // before a group: tiles, and their cost
-  __shared__ int bound[9];                  // the runs, in products
-  __shared__ int part_sums[NT / 64];
-  const int tid = threadIdx.x;
-  count_group_tiles<NT>(offsets, G, P, rows, first);
-  for (int g = tid; g <= G + 1; g += NT) first[g] = min(first[g], most);  // more come only of offsets that do not ascend
+  __shared__ GroupTilesBefore start, first, cost;  // of a group: its first row; tiles and their cost before it
+  __shared__ int bound[9];                         // the runs, in products
+  __shared__ int2 sums[NT / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int per = (G + NT) / NT, g0 = tid * per, g1 = min(g0 + per, G + 1);  // consecutive groups of a thread
+  for (int g = g0; g < g1; ++g) start[g] = group_first(offsets, g, P);
+  if (tid == 0) start[G + 1] = P;
+  if (tid < 9) bound[tid] = 0;
   __syncthreads();
-  // halves before a group, then the cost
-  {
-    const int per = (G + NT) / NT;
-    auto is_half = [&](int g) {
-      const int n = (g < G ? group_first(offsets, g + 1, P) : P) - group_first(offsets, g, P), rest = n % rows;
-      return n > 0 && rest > 0 && rest <= half ? 1 : 0;
-    };
-    int sum = 0;
-    for (int g = tid * per; g < min((tid + 1) * per, G + 1); ++g) sum += is_half(g);
-    int upto = wave_prefix_sum(sum);
-    if ((tid & 63) == 63) part_sums[tid >> 6] = upto;
-    __syncthreads();
-    for (int w = 0; w < tid >> 6; ++w) upto += part_sums[w];
-    int at = upto - sum;
-    for (int g = tid * per; g < min((tid + 1) * per, G + 1); ++g) {
-      cost[g] = kTileCost * first[g] - (kTileCost - kHalfTileCost) * at;
-      at += is_half(g);
-      if (g == G) cost[G + 1] = kTileCost * first[G + 1] - (kTileCost - kHalfTileCost) * at;
-    }
-    __syncthreads();
+  auto tiles_of = [&](int g) { return (max(start[g + 1] - start[g], 0) + rows - 1) / rows; };
+  auto halves_of = [&](int g) {
+    const int n = max(start[g + 1] - start[g], 0), rest = n % rows;
+    return rest > 0 && rest <= half ? 1 : 0;
+  };
+  int tiles = 0, halves = 0;
+  for (int g = g0; g < g1; ++g) tiles += tiles_of(g), halves += halves_of(g);
+  int2 upto = make_int2(wave_prefix_sum(tiles), wave_prefix_sum(halves));
+  if (lane == 63) sums[wave] = upto;
+  __syncthreads();
+  int2 total = make_int2(0, 0);
+  for (int w = 0; w < NT / 64; ++w) {
+    if (w == wave) upto.x += total.x, upto.y += total.y;
+    total.x += sums[w].x, total.y += sums[w].y;
   }
-  const int all = tiles_n * first[G + 1];
-  if (tid < 9) {
-    const int64_t target = static_cast<int64_t>(cost[G + 1]) * tiles_n * tid / 8;
-    int lo = 0, hi = G;  // the last group that starts at or before the target
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(cost[mid]) * tiles_n <= target) lo = mid;
-      else hi = mid - 1;
+  const bool ascending = total.x <= most;  // more come only of offsets that do not ascend
+  const int all_tiles = min(total.x, most), all = tiles_n * all_tiles;
+  const int64_t all_cost = static_cast<int64_t>(kTileCost * all_tiles - (kTileCost - kHalfTileCost) * total.y) * tiles_n;
+  {
+    int at = upto.x - tiles, at_half = upto.y - halves;
+    for (int g = g0; g < g1; ++g) {
+      const int n = tiles_of(g), c = kTileCost * n - (kTileCost - kHalfTileCost) * halves_of(g);
+      first[g] = min(at, most);
+      cost[g] = kTileCost * at - (kTileCost - kHalfTileCost) * at_half;
+      if (g == G) first[G + 1] = min(at + n, most), cost[G + 1] = cost[g] + c;
+      // the runs that begin in this group; their ends may be a product off by the float's rounding
+      const int64_t from = static_cast<int64_t>(cost[g]) * tiles_n, to = from + static_cast<int64_t>(c) * tiles_n;
+      if (ascending && n > 0)
+        for (int x = 1; x < 8; ++x) {
+          const int64_t target = all_cost * x >> 3;
+          if (from <= target && target < to)
+            bound[x] = tiles_n * at + min(static_cast<int>(static_cast<float>(target - from) * n / c), tiles_n * n);
+        }
+      at += n;
+      at_half += halves_of(g);
     }
-    const int64_t in = target - static_cast<int64_t>(cost[lo]) * tiles_n;
-    const int c = cost[lo + 1] - cost[lo], n = first[lo + 1] - first[lo];
-    bound[tid] = tid == 8 ? all : min(first[lo] * tiles_n + (c > 0 ? static_cast<int>(in * n / c) : 0), all);
+    if (tid == 0) bound[8] = all;
   }
   __syncthreads();
   int longest = 0;
-  bool ascending = true;
-  for (int x = 0; x < 8; ++x) {
-    longest = max(longest, bound[x + 1] - bound[x]);
-    ascending = ascending && bound[x + 1] >= bound[x] && bound[x] >= 0;
-  }
-  __syncthreads();
-  if (8 * longest > capacity || !ascending) {
-    if (tid < 9) bound[tid] = static_cast<int>(static_cast<int64_t>(all) * tid / 8);
-    longest = (all + 7) / 8;
-    __syncthreads();
-  }
-  if (part == 0) {
+  for (int x = 0; x < 8; ++x) longest = max(longest, bound[x + 1] - bound[x]);
+  const bool equal = !ascending || 8 * longest > capacity;
+  if (equal) longest = (all + 7) / 8;
+  auto run = [&](int x) { return equal ? static_cast<int>(static_cast<int64_t>(all) * x >> 3) : bound[x]; };
+  if (part == parts - 1) {
     if (tid == 0) table[0] = make_int4(8 * longest, 0, 0, 0);
-    for (int e = tid; e < 8 * longest; e += NT)
-      if (e / 8 >= bound[(e & 7) + 1] - bound[e & 7]) table[1 + e] = make_int4(0, 0, 0, 0);
+    for (int x = wave; x < 8; x += NT / 64)
+      for (int i = run(x + 1) - run(x) + lane; i < longest; i += 64) table[1 + 8 * i + x] = make_int4(0, 0, 0, 0);
   }
-  // a group's products in run x, [from, to)
-  auto from = [&](int g, int x) { return max(first[g] * tiles_n, bound[x]); };
-  auto to = [&](int g, int x) { return min(first[g + 1] * tiles_n, bound[x + 1]); };
-  for (int g = part; g <= G; g += parts) {
-    const int tiles = first[g + 1] - first[g], c = cost[g + 1] - cost[g];
-    for (int x = 0; x < 8; ++x) {
-      const int p0 = from(g, x), p1 = to(g, x);
-      if (p0 >= p1) continue;
-      // the products of the run's groups that come first
-      int before = 0;
-      for (int h = tid; h <= G; h += NT) {
-        const int n = to(h, x) - from(h, x);
-        if (n <= 0) continue;
-        const int64_t mine = static_cast<int64_t>(c) * (first[h + 1] - first[h]);
-        const int64_t its = static_cast<int64_t>(cost[h + 1] - cost[h]) * tiles;
-        if (its > mine || (its == mine && h < g)) before += n;
-      }
-      const int sum = __builtin_amdgcn_readlane(wave_prefix_sum(before), 63);
-      __syncthreads();
-      if ((tid & 63) == 0) part_sums[tid >> 6] = sum;
-      __syncthreads();
-      before = 0;
-      for (int w = 0; w < NT / 64; ++w) before += part_sums[w];
-      for (int p = p0 + tid; p < p1; p += NT) {
-        int tm, tn;
-        group_product(p - first[g] * tiles_n, tiles, tiles_n, tm, tn);
-        int4 t = group_tile(offsets, G, P, g, tm, rows);
-        t.w = tn;
-        table[1 + 8 * (before + p - p0) + x] = t;
-      }
+  // a wave per group and run
+  for (int item = part * (NT / 64) + wave; item < 8 * (G + 1); item += parts * (NT / 64)) {
+    const int g = item >> 3, x = item & 7, run0 = run(x), run1 = run(x + 1);
+    const int p0 = max(first[g] * tiles_n, run0), p1 = min(first[g + 1] * tiles_n, run1);
+    if (p0 >= p1) continue;
+    const int n = first[g + 1] - first[g], c = cost[g + 1] - cost[g];
+    int before = 0;  // the products of the run's groups that come first
+    for (int h = lane; h <= G; h += 64) {
+      const int products = min(first[h + 1] * tiles_n, run1) - max(first[h] * tiles_n, run0);
+      const int64_t mine = static_cast<int64_t>(c) * (first[h + 1] - first[h]);
+      const int64_t its = static_cast<int64_t>(cost[h + 1] - cost[h]) * n;
+      if (products > 0 && (its > mine || (its == mine && h < g))) before += products;
+    }
+    before = __builtin_amdgcn_readlane(wave_prefix_sum(before), 63);
+    const int row0 = start[g], end = start[g + 1];
+    for (int p = p0 + lane; p < p1; p += 64) {
+      int tm, tn;
+      group_product(p - first[g] * tiles_n, n, tiles_n, tm, tn);
+      const int row = row0 + tm * rows;
+      table[1 + 8 * (before + p - p0) + x] = make_int4(g < G ? g : -1, row, min(rows, end - row), tn);
     }
   }
 }

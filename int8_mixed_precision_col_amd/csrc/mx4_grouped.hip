@@ -5,6 +5,8 @@
 #include "mx4_gemm_kernel.hpp"
 #include "mx4_launch.hpp"
 
+#include <algorithm>
+
 namespace i8mm {
 
 template <>
@@ -52,9 +54,8 @@ __global__ __launch_bounds__(256) void k_group_quantize(GroupQuantArgs a, int pa
 }
 
 hipError_t launch_group_quantize(const GroupQuantArgs& a, int type, hipStream_t s) {
-  // a group per workgroup, or an entry or two of the table per thread, as far as 64 or 256 go
-  const int parts = a.tile_rows == GroupL::TM ? (a.G + 1 < 256 ? a.G + 1 : 256)
-                                              : (a.capacity < 64 * 256 ? (a.capacity + 255) / 256 : 64);
+  // a wave per group and run, or an entry of the table per thread, as far as 64 workgroups go
+  const int parts = std::min(a.tile_rows == GroupL::TM ? 2 * (a.G + 1) : (a.capacity + 255) / 256, 64);
   const unsigned blocks = static_cast<unsigned>(a.M / 16 + 1) * mx_quads(a.K) + parts;
   if (type == kMxF16) hipLaunchKernelGGL(k_group_quantize<F16>, dim3(blocks), dim3(256), 0, s, a, parts);
   else hipLaunchKernelGGL(k_group_quantize<B16>, dim3(blocks), dim3(256), 0, s, a, parts);
