@@ -108,13 +108,21 @@ __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int mo
   make_group_tiles<kOrderThreads>(first, a.S, a.M, kLoraRows, most, a.table);
 }
 
-// The tile of workgroup column b: its adapter (-1: none) and its rows, in LDS. false: no such tile.
+// A workgroup's tile, of a grid of as many tiles as there may be times parts: the tile's adapter (-1: none)
+// and its rows, in LDS, and the part. false: none. RUNS, beyond kLoraFew rows: each XCD (workgroup
+// number mod 8) takes a contiguous run of the tiles with all their parts, so that its L2 holds few
+// adapters and a tile's V comes from memory once. The run's bounds cost a load of the table's head
+// before the tile's: the staged expand gains by it (3333 x 4096 x 11008 of rank 64, 64.7 -> 61.0 us in
+// all), the shrink loses (61.5).
 struct LoraTile {
-  int adapter, rows;
+  int adapter, rows, part;
 };
-__device__ __forceinline__ bool lora_tile(const LoraArgs& a, int b, int* row_of, LoraTile& t) {
+template <bool RUNS = false>
+__device__ __forceinline__ bool lora_tile(const LoraArgs& a, int* row_of, LoraTile& t) {
   const int tid = threadIdx.x, lane = tid & 63;
-  if (a.M <= kLoraFew) {
+  int b = blockIdx.x;
+  t.part = blockIdx.y;
+  if (!RUNS && a.M <= kLoraFew) {
     // every wave finds each row's rows of equal id, by a ballot per bit of its number; the b-th row
     // that no such row is in front of leads tile b
     const int id = a.ids[min(lane, a.M - 1)], g = id >= 0 && id < a.S ? id : a.S;
@@ -133,8 +141,18 @@ __device__ __forceinline__ bool lora_tile(const LoraArgs& a, int b, int* row_of,
     t.rows = __builtin_popcountll(mine);
     if (tid < 64 && (mine >> lane & 1)) row_of[__builtin_popcountll(mine & ((1ull << lane) - 1ull))] = lane;
   } else {
-    const int4 head = a.table[0], e = a.table[1 + b];  // on their way together
-    if (b >= head.x) return false;
+    int4 head = a.table[0], e;
+    if constexpr (RUNS) {
+      const int workgroups = head.x * gridDim.y, number = blockIdx.x + gridDim.x * blockIdx.y;
+      if (number >= workgroups) return false;
+      const int at = group_order(number, workgroups);
+      b = at / static_cast<int>(gridDim.y);
+      t.part = at - b * gridDim.y;
+      e = a.table[1 + b];
+    } else {
+      e = a.table[1 + b];  // with the head on its way too
+      if (b >= head.x) return false;
+    }
     t.adapter = e.x;
     t.rows = e.z;
     if (tid < e.z) row_of[tid] = a.order[e.y + tid];
@@ -160,7 +178,7 @@ __device__ __forceinline__ void lora_shrink(const LoraArgs& a, const LoraTile& t
                                             float (&red)[kLoraWaves][kLoraRows][36]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int steps = (a.K + 63) / 64, split = blockIdx.y, splits = gridDim.y;
+  const int steps = (a.K + 63) / 64, split = tile.part, splits = gridDim.y;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * split / splits);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits);
   const uint16_t *x[J], *w[RB];
@@ -229,7 +247,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_shrink(LoraArgs a) {
   __shared__ int row_of[kLoraRows];
   __shared__ __attribute__((aligned(16))) float red[kLoraWaves][kLoraRows][36];
   LoraTile tile;
-  if (!lora_tile(a, blockIdx.x, row_of, tile) || tile.adapter < 0) return;
+  if (!lora_tile(a, row_of, tile) || tile.adapter < 0) return;
   const int rank = lora_rank(a, tile.adapter);
   if (tile.rows <= 16) lora_shrink<T, RB, 1>(a, tile, rank, row_of, red);
   else if (tile.rows <= 32) lora_shrink<T, RB, 2>(a, tile, rank, row_of, red);
@@ -402,8 +420,8 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_expand(LoraArgs a, int
   __shared__ __attribute__((aligned(16))) typename T::elem v[2][kLoraRows][LR];
   __shared__ float row_scale[kLoraRows];
   LoraTile tile;
-  if (!lora_tile(a, blockIdx.x, row_of, tile)) return;
-  const int n0 = blockIdx.y * span, n1 = min(n0 + span, a.N);
+  if (!lora_tile(a, row_of, tile)) return;
+  const int n0 = tile.part * span, n1 = min(n0 + span, a.N);
   const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
   if (rank == 0) {
     lora_copy_rows<64 * kLoraWaves>(a, tile, row_of, n0, n1);
@@ -470,8 +488,8 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
   __shared__ __attribute__((aligned(1024))) char buf1[sizeof(Parts) > Staged::BYTES ? sizeof(Parts) : Staged::BYTES];
   Parts& v = *reinterpret_cast<Parts*>(buf1);  // until it is in registers
   LoraTile tile;
-  if (!lora_tile(a, blockIdx.x, row_of, tile)) return;
-  const int n0 = blockIdx.y * span, n1 = min(n0 + span, a.N);
+  if (!lora_tile<true>(a, row_of, tile)) return;
+  const int n0 = tile.part * span, n1 = min(n0 + span, a.N);
   const int rank = tile.adapter < 0 ? 0 : lora_rank(a, tile.adapter);
   if (rank == 0) {
     lora_copy_rows<64 * kStagedWaves>(a, tile, row_of, n0, n1);
@@ -591,10 +609,11 @@ static hipError_t lora(const LoraArgs& a, hipStream_t s) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // features per workgroup: as many workgroups as the GPU holds, two to three per CU
+  // features per workgroup: as many workgroups as the GPU holds, of the staged expand three per CU up to
+  // rank 64, then two (3000 x 8192 x 10240, rank 128: 768 workgroups 98.2 us, 512 87.8)
   const bool few = a.M <= kLoraFew;
   const int round = few ? 32 * kLoraWaves : 128;
-  const int64_t per = (few ? 512 : 768) / tiles < 1 ? 1 : (few ? 512 : 768) / tiles;
+  const int64_t room = few || a.R > 64 ? 512 : 768, per = room / tiles < 1 ? 1 : room / tiles;
   const int span = static_cast<int>(((a.N + per - 1) / per + round - 1) / round * round);
   const dim3 expand(tiles, (a.N + span - 1) / span);
   if (!few) {
