@@ -22,10 +22,7 @@ namespace i8mm {
 
 constexpr int kLoraFew = 64;  // rows that each workgroup orders by itself
 constexpr int kLoraWaves = 8;
-// Parts of K at most, their sums loaded together: of few rows, where workgroups are few, and of many
-// (us per call with 2 / 4 / 8: 8 x 4096 x 4096 of rank 16 8.5 / 7.5 / 7.1, 3333 x 4096 x 11008 of rank 64
-// 70.8 / 64.7 / 70.9).
-constexpr int kLoraFewSplits = 8, kLoraSplits = 4;
+constexpr int kLoraSplits = 8;  // parts of K at most
 
 // ---- rows by adapter ----
 
@@ -366,7 +363,7 @@ struct LoraExpand {
   }
 };
 
-// V of the tile's rows: LPR lanes to a row, 4 ranks each; the parts of K together.
+// V of the tile's rows: LPR lanes to a row, 4 ranks each; the parts of K, up to SPLITS, together.
 template <class T, int KS, int THREADS, int SPLITS, int LR>
 __device__ __forceinline__ void lora_gather_v(const LoraArgs& a, const LoraTile& tile, const int* row_of,
                                               typename T::elem (&v)[2][kLoraRows][LR], float* row_scale) {
@@ -430,7 +427,7 @@ __device__ __forceinline__ void lora_expand(const LoraArgs& a, const LoraTile& t
   int n = n0 + 32 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   typename LoraExpand<T, KS, J>::Operands x, y;
   e.load(x, n);
-  lora_gather_v<T, KS, 64 * kLoraWaves, kLoraFewSplits>(a, tile, row_of, v, row_scale);
+  lora_gather_v<T, KS, 64 * kLoraWaves, kLoraSplits>(a, tile, row_of, v, row_scale);
   lds_barrier();
   for (; n < n1; n += 2 * step) {
     e.load(y, n + step);
@@ -504,7 +501,8 @@ struct LoraStaged {
   }
 };
 
-template <class T, int KS>
+// SPLITS: parts of K at most.
+template <class T, int KS, int SPLITS>
 __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraArgs a, int span) {
   typedef LoraStaged<T, KS> Staged;
   typedef typename Staged::v8e v8e;
@@ -542,7 +540,7 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
   v4u y0[4], y1[4];
   load_y(y0, n0);
   load_y(y1, n0 + 128);
-  lora_gather_v<T, KS, 64 * kStagedWaves, kLoraSplits>(a, tile, row_of, v, row_scale);
+  lora_gather_v<T, KS, 64 * kStagedWaves, SPLITS>(a, tile, row_of, v, row_scale);
   wait_and_barrier<0>();
   if (16 * wave >= tile.rows) {  // no rows: only its share of B
     lds_barrier();
@@ -608,11 +606,23 @@ static int64_t lora_tiles(int64_t M, int64_t S) {
   return group_tiles_most(M, S, kLoraRows);
 }
 
+// Parts of K: a workgroup of the first product per CU, two of few rows; every workgroup of the second
+// reads each part. us in all with 3 / 4 / 6 of them: 3333 x 4096 x 11008, rank 64, 59 tiles 62.2 / 60.2 /
+// 62.7; 4096 x 4096 x 4096, rank 16, 72 tiles 33.1 / 35.8 / 34.1; 2048, rank 128, 36 tiles 47.3 / 43.6 / 41.4.
 int lora_splits(int64_t M, int64_t K, int64_t S) {
-  const int64_t by_tiles = 512 / lora_tiles(M, S), by_k = K / (64 * kLoraWaves);
+  const int64_t by_tiles = (M <= kLoraFew ? 512 : 264) / lora_tiles(M, S), by_k = K / (64 * kLoraWaves);
   const int64_t n = by_tiles < by_k ? by_tiles : by_k;
-  const int64_t most = M <= kLoraFew ? kLoraFewSplits : kLoraSplits;
-  return static_cast<int>(n < 1 ? 1 : n > most ? most : n);
+  return static_cast<int>(n < 1 ? 1 : n > kLoraSplits ? kLoraSplits : n);
+}
+
+template <class T, int SPLITS>
+static void expand_staged(const LoraArgs& a, dim3 expand, int span, hipStream_t s) {
+  switch ((a.R + 31) / 32) {
+    case 1: hipLaunchKernelGGL((k_lora_expand_staged<T, 1, SPLITS>), expand, dim3(64 * kStagedWaves), 0, s, a, span); break;
+    case 2: hipLaunchKernelGGL((k_lora_expand_staged<T, 2, SPLITS>), expand, dim3(64 * kStagedWaves), 0, s, a, span); break;
+    case 3: hipLaunchKernelGGL((k_lora_expand_staged<T, 3, SPLITS>), expand, dim3(64 * kStagedWaves), 0, s, a, span); break;
+    default: hipLaunchKernelGGL((k_lora_expand_staged<T, 4, SPLITS>), expand, dim3(64 * kStagedWaves), 0, s, a, span); break;
+  }
 }
 
 template <class T>
@@ -645,13 +655,8 @@ static hipError_t lora(const LoraArgs& a, hipStream_t s) {
   const int span = static_cast<int>(((a.N + per - 1) / per + round - 1) / round * round);
   const dim3 expand(tiles, (a.N + span - 1) / span);
   if (!few) {
-    const dim3 staged(64 * kStagedWaves);
-    switch ((a.R + 31) / 32) {
-      case 1: hipLaunchKernelGGL((k_lora_expand_staged<T, 1>), expand, staged, 0, s, a, span); break;
-      case 2: hipLaunchKernelGGL((k_lora_expand_staged<T, 2>), expand, staged, 0, s, a, span); break;
-      case 3: hipLaunchKernelGGL((k_lora_expand_staged<T, 3>), expand, staged, 0, s, a, span); break;
-      default: hipLaunchKernelGGL((k_lora_expand_staged<T, 4>), expand, staged, 0, s, a, span); break;
-    }
+    if (a.splits <= kLoraSplits / 2) expand_staged<T, kLoraSplits / 2>(a, expand, span, s);
+    else expand_staged<T, kLoraSplits>(a, expand, span, s);
     return hipGetLastError();
   }
   switch ((a.R + 31) / 32) {
