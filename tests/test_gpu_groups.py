@@ -347,6 +347,23 @@ def test_lora(M, K, N, R, S, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("ranked", [False, True])
+@pytest.mark.parametrize("M,K,N,R,S", [
+    (65, 4112, 272, 8, 1), (200, 4608, 1040, 72, 2), (300, 4112, 528, 128, 3),     # K in 8 parts
+    (700, 2576, 272, 24, 9),                                                       # in 5, tiles for each XCD
+    (1500, 1040, 144, 104, 40), (2100, 1552, 272, 64, 6), (4000, 2064, 144, 24, 100),  # in 2, 3 and 1
+])
+def test_lora_many_rows_in_parts(M, K, N, R, S, dtype, ranked):
+    """Beyond 64 rows: K in few and in many parts, one step of a wave and several, a last step past K's
+    end, tiles that do not divide by the XCDs."""
+    announce(f"lora {M} x {K} x {N} rank {R} of {S} {dtype} ranked={ranked}")
+    t = lora_case(M, K, N, R, S, dtype, M + R, ranked)
+    y = lora.apply(**t)
+    close(y, *want_lora(t))
+    assert torch.equal(y, lora.apply(**t))
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
 @pytest.mark.parametrize("M", [1, 40, 150])
 def test_lora_strided_and_ids_out_of_range(M, dtype):
     announce(f"lora strided M={M} {dtype}")
