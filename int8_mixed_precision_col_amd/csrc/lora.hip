@@ -29,7 +29,8 @@ constexpr int kLoraSplits = 8;  // parts of K at most
 // Counting sort of ids into S adapters and, last, the rows without one; stable. 16 waves each take
 // a stretch of the rows, 64 at a time: lanes of equal group find each other by a ballot per bit of
 // the group's number, so no order depends on atomics. Counts, their sums, places; then the table of
-// tiles.
+// tiles. Up to 4096 rows a wave's groups stay in registers from the counts to
+// the places (3333 x 4096 x 11008 60.9 -> 59.5 us in all, 256 x 4096 x 4096 16.5 -> 16.1).
 constexpr int kOrderWaves = 16, kOrderThreads = 64 * kOrderWaves;
 constexpr int kOrderBatch = 4;  // chunks of 64 rows whose ids are asked for together
 __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int most) {
@@ -43,29 +44,34 @@ __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int mo
   const int bits = 32 - __builtin_clz(a.S);
   for (int g = lane; g < G; g += 64) next[g] = 0;
   wave_lds_fence();
-  auto each_chunk = [&](auto use) {
-    for (int c0 = m0; c0 < m1; c0 += 64 * kOrderBatch) {
-      int id[kOrderBatch];
+  int group[kOrderBatch];
+  unsigned long long same[kOrderBatch];  // the lanes of a chunk whose row is in this one's group
+  auto find = [&](int c0) {
+    int id[kOrderBatch];
 #pragma unroll
-      for (int i = 0; i < kOrderBatch; ++i) id[i] = a.ids[min(c0 + 64 * i + lane, a.M - 1)];
+    for (int i = 0; i < kOrderBatch; ++i) id[i] = a.ids[min(c0 + 64 * i + lane, a.M - 1)];
 #pragma unroll
-      for (int i = 0; i < kOrderBatch; ++i) {
-        const int m = c0 + 64 * i + lane;
-        if (m - lane >= m1) break;
-        const int g = id[i] >= 0 && id[i] < a.S ? id[i] : a.S;
-        unsigned long long same = __ballot(m < m1);
-        for (int b = 0; b < bits; ++b) {
-          const unsigned long long set = __ballot(g >> b & 1);
-          same &= g >> b & 1 ? set : ~set;
-        }
-        if (m < m1) use(m, g, same, __builtin_popcountll(same & ((1ull << lane) - 1ull)));
-        wave_lds_fence();
+    for (int i = 0; i < kOrderBatch; ++i) {
+      if (c0 + 64 * i >= m1) break;
+      const int g = id[i] >= 0 && id[i] < a.S ? id[i] : a.S;
+      group[i] = g;
+      same[i] = __ballot(c0 + 64 * i + lane < m1);
+      for (int b = 0; b < bits; ++b) {
+        const unsigned long long set = __ballot(g >> b & 1);
+        same[i] &= g >> b & 1 ? set : ~set;
       }
     }
   };
-  each_chunk([&](int, int g, unsigned long long same, int rank) {
-    if (rank == 0) next[g] += __builtin_popcountll(same);
-  });
+  auto rank = [&](int i) { return __builtin_popcountll(same[i] & ((1ull << lane) - 1ull)); };
+  for (int c0 = m0; c0 < m1; c0 += 64 * kOrderBatch) {
+    find(c0);
+#pragma unroll
+    for (int i = 0; i < kOrderBatch; ++i) {
+      if (c0 + 64 * i >= m1) break;
+      if (c0 + 64 * i + lane < m1 && rank(i) == 0) next[group[i]] += __builtin_popcountll(same[i]);
+      wave_lds_fence();
+    }
+  }
   __syncthreads();
   // exclusive sums: over the groups (a thread has one or two, G <= 1025), within one over the waves
   int run = 0;
@@ -95,11 +101,20 @@ __global__ __launch_bounds__(kOrderThreads) void k_lora_order(LoraArgs a, int mo
     __syncthreads();
   }
   if (tid == 0) first[G] = a.M;
-  each_chunk([&](int m, int g, unsigned long long same, int rank) {
-    const int at = next[g];
-    a.order[at + rank] = m;
-    if (rank == 0) next[g] = at + __builtin_popcountll(same);
-  });
+  for (int c0 = m0; c0 < m1; c0 += 64 * kOrderBatch) {
+    if (per > kOrderBatch) find(c0);  // one batch is still known
+#pragma unroll
+    for (int i = 0; i < kOrderBatch; ++i) {
+      const int m = c0 + 64 * i + lane;
+      if (m - lane >= m1) break;
+      if (m < m1) {
+        const int at = next[group[i]];
+        a.order[at + rank(i)] = m;
+        if (rank(i) == 0) next[group[i]] = at + __builtin_popcountll(same[i]);
+      }
+      wave_lds_fence();
+    }
+  }
   __syncthreads();
   // the rows without an adapter are the table's group -1
   make_group_tiles<kOrderThreads>(first, a.S, a.M, kLoraRows, most, a.table);

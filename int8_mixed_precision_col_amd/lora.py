@@ -29,8 +29,8 @@ def apply(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, id
     """out [M, N] = Y + scales[a] (X A_a^T) B_a^T with a = ids[m] for each row m, in X's type (fp16
     or bf16); rows whose id is no adapter (say -1) keep Y.
 
-    Y [M, N] is the shared projection of X [M, K] (rows contiguous, any row stride of a multiple
-    of 8). A [S, R, K] and B [S, N, R] hold S adapters of R ranks (a multiple of 8, at most 128);
+    Y [M, N] is the shared projection of X [M, K] (K and N multiples of 16, rows contiguous, any
+    row stride of a multiple of 8). A [S, R, K] and B [S, N, R] hold S adapters of R ranks (a multiple of 8, at most 128);
     ids int32 [M] in any order; scales fp32 [S]; ranks int32 [S]: an adapter's own rank, what A
     and B hold beyond it is not looked at. out=Y adds in place.
     """
