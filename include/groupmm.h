@@ -75,7 +75,7 @@ int moe_grouped_matmul(const void* X, int64_t M, int64_t K, int64_t ldx, int dty
  * Y[t] = sum over j of weights[t, j] P[slots[t, j]], summed in fp32 in the order of j, rounded
  * once; a slot outside 0 .. P_rows - 1 adds nothing.
  *   P             [P_rows, D] contiguous, dtype MX4_F16 or MX4_BF16; D a multiple of 16.
- *   slots, weights  int32 and fp32 [T, top_k], 1 <= top_k <= 16.
+ *   slots, weights  int32 and fp32 [T, top_k], 1 <= T <= 2^24, 1 <= top_k <= 16; P_rows up to 2^28.
  *   Y             out, [T, D] contiguous, dtype.
  */
 int moe_combine(const void* P, int64_t P_rows, int64_t D, int dtype, const int32_t* slots, const float* weights,

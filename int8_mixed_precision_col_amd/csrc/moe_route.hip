@@ -343,9 +343,9 @@ template <class T, int K>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
   typedef typename T::elem v8e __attribute__((ext_vector_type(8)));
   const int per = a.D / 8;
-  const int64_t t = blockIdx.x;
+  const int64_t t = blockIdx.x + static_cast<int64_t>(gridDim.x) * blockIdx.z;
   const int c = blockIdx.y * 256 + threadIdx.x;
-  if (c >= per) return;
+  if (c >= per || t >= a.T) return;
   float sum[8] = {};
   for (int j0 = 0; j0 < a.k; j0 += K) {
     v4u x[K];
@@ -374,7 +374,9 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
 
 template <class T>
 static hipError_t combine(const CombineArgs& a, hipStream_t s) {
-  const dim3 grid(a.T, (a.D / 8 + 255) / 256);
+  // a launch has less than 2^32 threads in x: more tokens than that lie side by side in z
+  const unsigned sides = a.T < 1 << 24 ? 1 : 2;
+  const dim3 grid((a.T + sides - 1) / sides, (a.D / 8 + 255) / 256, sides);
   if (a.k <= 1) hipLaunchKernelGGL((k_combine<T, 1>), grid, dim3(256), 0, s, a);
   else if (a.k <= 2) hipLaunchKernelGGL((k_combine<T, 2>), grid, dim3(256), 0, s, a);
   else if (a.k <= 4) hipLaunchKernelGGL((k_combine<T, 4>), grid, dim3(256), 0, s, a);

@@ -274,6 +274,19 @@ def test_combine(T, k, D, dtype):
     close(y, *ref.combine(f64(p), slots.numpy(), w.double().numpy()))
 
 
+@pytest.mark.parametrize("T", [(1 << 24) - 1, 1 << 24])
+def test_combine_of_as_many_tokens_as_there_may_be(T):
+    announce(f"combine T={T}")
+    p = torch.randn((1000, 16), generator=gen(4)).half().cuda()
+    slots = (torch.arange(T, dtype=torch.int32, device="cuda") * 7 % 1003).view(T, 1)   # 1000 .. 1002: no row
+    w = torch.ones((T, 1), device="cuda")
+    y = moe.combine(p, slots, w)
+    want = torch.cat((p, torch.zeros((3, 16), dtype=F16, device="cuda")))
+    for part in range(0, T, 1 << 22):
+        at = slots[part:part + (1 << 22), 0].long()
+        assert torch.equal(y[part:part + (1 << 22)], want[at])
+
+
 # ---- the layer ----
 
 @pytest.mark.parametrize("fmt,dtype", [("mx4", F16), ("mx4", B16), ("int8", F16)])
