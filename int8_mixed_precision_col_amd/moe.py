@@ -104,11 +104,18 @@ def _route_workspace_bytes(T: int, E: int) -> int:
     return int(groups.lib().moe_route_workspace_bytes(T, E))
 
 
+def _outliers(K: int, max_outliers: int | None) -> int:
+    """How many outlier columns a call makes room for."""
+    most = min(K, 8192)
+    return most if max_outliers is None else min(max_outliers, most)
+
+
 @functools.lru_cache(maxsize=1024)
-def grouped_workspace_bytes(M: int, K: int, P: int, E: int, N: int, weight_format: int, max_outliers: int = 256) -> int:
+def grouped_workspace_bytes(M: int, K: int, P: int, E: int, N: int, weight_format: int,
+                            max_outliers: int | None = None) -> int:
     """What ``grouped_matmul`` needs for X [M, K], P rows of the product and E experts of N features
-    (0 on bad shapes); weight_format 0: int8, 1: MX4."""
-    return int(groups.lib().moe_grouped_workspace_bytes(M, K, P, E, N, weight_format, max_outliers))
+    (0 on bad shapes); weight_format 0: int8, 1: MX4; max_outliers as given to the call."""
+    return int(groups.lib().moe_grouped_workspace_bytes(M, K, P, E, N, weight_format, _outliers(K, max_outliers)))
 
 
 def route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> Routing:
@@ -172,8 +179,7 @@ def grouped_matmul(X: torch.Tensor, weight: tuple, offsets: torch.Tensor, rows: 
         out = X.new_empty((P, width))
     else:
         _need_shape(out, X.dtype, (P, width), X.device, "out")
-    most = min(K, 8192)
-    max_outliers = most if max_outliers is None else min(max_outliers, most)
+    max_outliers = _outliers(K, max_outliers)
     nbytes = grouped_workspace_bytes(M, K, P, E, N, fmt, max_outliers)
     if nbytes == 0:
         raise ValueError(f"bad shape for grouped_matmul: M={M} K={K} P={P} E={E} N={N} max_outliers={max_outliers}")

@@ -247,6 +247,20 @@ def test_grouped_int8_without_and_with_many_outliers():
     assert bool(torch.isnan(y[:80]).all()) and int(torch.count_nonzero(y[80:])) == 0
 
 
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+@pytest.mark.parametrize("E,n,N,K,gated", [(3, 90, 96, 528, False), (64, 500, 64, 144, True), (3, 1500, 10272, 272, False)])
+def test_grouped_in_a_workspace_of_the_callers(E, n, N, K, gated, fmt):
+    """Exactly as large as the helper says, filled with anything, nothing written around it."""
+    announce(f"grouped in a workspace, E={E} rows={n} N={N} K={K} {fmt}")
+    x, (weight, _) = activations(40, K, F16, n), weights_of(E, N, K, fmt, F16, E)
+    off, rows = i32(np.arange(E + 1) * n // E), i32(np.arange(n) % 40)
+    need = moe.grouped_workspace_bytes(40, K, n, E, N, int(fmt == "mx4"))
+    guard = torch.full((need + 512,), 0xa5, dtype=torch.uint8, device="cuda")
+    y = moe.grouped_matmul(x, weight, off, rows, gated, workspace=guard[256:256 + need])
+    assert torch.equal(y, moe.grouped_matmul(x, weight, off, rows, gated))
+    assert bool((guard[:256] == 0xa5).all()) and bool((guard[256 + need:] == 0xa5).all())
+
+
 @pytest.mark.parametrize("dtype", [F16, B16])
 def test_grouped_strided_rows(dtype):
     announce(f"grouped mx4, strided X {dtype}")
@@ -391,6 +405,17 @@ def test_lora_strided_and_ids_out_of_range(M, dtype):
     got = lora.apply(**{**t, "X": xb[:, 64:336], "Y": yb[:, 8:152]}, out=ob[:, 16:160])
     assert torch.equal(got, want)
     assert bool(torch.isnan(ob[:, :16]).all()) and bool(torch.isnan(ob[:, 160:]).all())
+
+
+@pytest.mark.parametrize("M,K,R,S", [(1, 16, 8, 1), (9, 1040, 24, 3), (64, 528, 128, 7), (65, 4112, 72, 2), (700, 272, 40, 20)])
+def test_lora_in_a_workspace_of_the_callers(M, K, R, S):
+    """Exactly as large as the helper says, filled with anything, nothing written around it."""
+    announce(f"lora in a workspace, M={M} K={K} R={R} S={S}")
+    t = lora_case(M, K, 144, R, S, B16, M, True)
+    need = lora.workspace_bytes(M, K, S, R)
+    guard = torch.full((need + 512,), 0xa5, dtype=torch.uint8, device="cuda")
+    assert torch.equal(lora.apply(**t, workspace=guard[256:256 + need]), lora.apply(**t))
+    assert bool((guard[:256] == 0xa5).all()) and bool((guard[256 + need:] == 0xa5).all())
 
 
 @pytest.mark.parametrize("M", [5, 100])

@@ -59,6 +59,21 @@ def test_good_calls_reach_the_library(calls):
     assert [c[0] for c in calls[-4:]] == ["moe_route", "moe_grouped_matmul", "moe_grouped_matmul", "moe_combine"]
 
 
+@pytest.mark.parametrize("K", [64, 144, 2048, 16384])
+@pytest.mark.parametrize("most", [None, 0, 40, 256, 1 << 20])
+@pytest.mark.parametrize("weights", ["int8", "mx4"])
+def test_the_size_helper_sizes_the_call(calls, weights, most, K):
+    """The helper's size is what the library asks for with the outlier columns that the call tells it."""
+    w = int8_pair(96, K) if weights == "int8" else pair(96, K)
+    args = {} if most is None else {"max_outliers": most}
+    fmt = int(weights == "mx4")
+    need = moe.grouped_workspace_bytes(5, K, 11, 3, 32, fmt, **args)
+    t = grouped_args(X=f16(5, K), weight=w, **args)
+    assert moe.grouped_matmul(**t, workspace=torch.zeros(need, dtype=torch.uint8)).shape == (11, 32)
+    told = calls[-1][1]
+    assert told[18] == need == groups.lib().moe_grouped_workspace_bytes(5, K, 11, 3, 32, fmt, told[15])
+
+
 @pytest.mark.parametrize("logits,k", [
     (torch.zeros(4, 8, dtype=torch.float64), 2), (torch.zeros(8), 1), (torch.zeros(8, 4).T, 2), (torch.zeros(4, 8), 0),
     (torch.zeros(4, 8), 9), (torch.zeros(4, 20), 17), (torch.zeros(0, 8), 2), (torch.zeros(4, 0), 1), (torch.zeros(2, 513), 2)])
