@@ -220,6 +220,9 @@ def moe_prompt(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tupl
     weights (MX4, or int8 with fp16 outlier columns, threshold and max_outliers as in
     ``grouped_matmul``), and the hidden values and each expert's outputs are rounded to X's type
     between the launches, where ``moe_layer`` keeps both in 16 bits or more."""
+    T = mx4._need_rows(X, "X")[0]
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[0] != T:
+        raise ValueError(f"logits must be a 2-D fp16, bf16 or fp32 tensor with {T} rows")
     r = route(logits, top_k, renormalize)
     h = grouped_matmul(X, gate_up, r.offsets, r.rows, True, threshold, max_outliers)
     p = grouped_matmul(h, down, r.offsets, None, False, threshold, max_outliers)

@@ -127,6 +127,13 @@ def test_lora_refused(calls, kw):
     assert calls == []
 
 
+@pytest.mark.parametrize("logits", [torch.zeros(19, 4), torch.zeros(21, 4), torch.zeros(0, 4), torch.zeros(20), None])
+def test_prompt_of_other_tokens_than_the_logits_refused(calls, logits):
+    with pytest.raises(ValueError):
+        moe.moe_prompt(f16(20, 64), logits, pair(4 * 64, 64), pair(4 * 64, 32), 2)
+    assert calls == []
+
+
 def test_cpu_tensors_are_refused_by_every_call(monkeypatch):
     launched = []
     monkeypatch.setattr(mx4, "_launch", lambda name, t, *args: launched.append(name))
