@@ -1,8 +1,9 @@
 /*
  * groupmm.h - C ABI of libint8mm.so, continued: products whose rows have weights of their
- * own, on MI355X (gfx950). A mixture-of-experts layer for any number of tokens (routing,
+ * own, on MI355X (gfx950). A mixture-of-experts layer for many tokens (routing,
  * products grouped by expert, the weighted sum back to tokens), and low-rank adapters of
- * many requests beside a shared projection.
+ * many requests beside a shared projection. The limits are those of mx4mm.h: at most
+ * 2^24 rows of any operand but moe_combine's P.
  *
  * Conventions are those of int8mm.h and mx4mm.h: device pointers owned by the caller, no
  * overlap unless a call says so; matrices, weights and workspaces 16-byte aligned, vectors of
@@ -51,8 +52,8 @@ int moe_route(const void* logits, int64_t T, int64_t E, int logits_dtype, int64_
  *                 X; more than max_outliers of them fill Y with NaN); X is fp16 and contiguous.
  *                 1: MX4, as mx4_matmul (X is quantized in the call); threshold and
  *                 max_outliers are not looked at.
- *   X             [M, K], row stride ldx, dtype MX4_F16 or MX4_BF16; less than 2^33 elements
- *                 with MX4 weights.
+ *   X             [M, K], row stride ldx, dtype MX4_F16 or MX4_BF16; M and P at most 2^24; less
+ *                 than 2^33 elements of X and of one expert's weight with MX4 weights.
  *   w, s          one prepared weight of E * N output features over K.
  *   offsets       int32 [E + 1], ascending from 0; 1 <= E <= 1024. Offsets that do not ascend,
  *                 or lie outside 0 .. P, give rows of Y that mean nothing.

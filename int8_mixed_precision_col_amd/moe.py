@@ -2,7 +2,7 @@
 ``tile_weight``) or MX4 (``mx4.prepare_weight`` / ``tile_weight``).
 
 For a few tokens ``moe_layer`` (include/mx4mm.h): routing, gate and up products, SiLU, down
-product and the weighted sum over experts in two launches. For any number of tokens
+product and the weighted sum over experts in two launches. For few or many tokens
 ``moe_prompt`` and its parts (include/groupmm.h): ``route``, ``grouped_matmul`` and ``combine``.
 """
 
@@ -118,10 +118,8 @@ def grouped_workspace_bytes(M: int, K: int, P: int, E: int, N: int, weight_forma
     return int(groups.lib().moe_grouped_workspace_bytes(M, K, P, E, N, weight_format, _outliers(K, max_outliers)))
 
 
-def route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> Routing:
-    """Routing of T tokens from their router logits [T, E] (fp16, bf16 or fp32; -inf: the expert is
-    off; E <= 512, top_k <= 16): lists as in ``moe_layer``, and the pairs of token and expert in
-    order of expert and then token. The same inputs give the same order."""
+def _need_logits(logits: torch.Tensor, top_k: int) -> tuple[int, int]:
+    """(T, E) of what ``route`` takes."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in mx4.DTYPES or logits.dim() != 2:
         raise ValueError("logits must be a 2-D fp16, bf16 or fp32 tensor")
     T, E = logits.shape
@@ -129,6 +127,31 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> Routing
         _need_shape(logits, logits.dtype, (T, E), logits.device, "logits")
     if not (1 <= top_k <= min(E, 16) and 1 <= T <= 1 << 24 and E <= 512):
         raise ValueError(f"bad shape for route: T={T} E={E} top_k={top_k}")
+    return T, E
+
+
+def _need_experts(weight: tuple, M: int, K: int, P: int, E: int, gated: bool, max_outliers: int | None,
+                  X: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """(weight format, features per expert, bytes of workspace) of a product of [M, K] in X's type."""
+    fmt, features = _rows(weight, name)
+    step = 32 if gated else 16
+    if features % (step * E):
+        raise ValueError(f"{name} has {features} output features: not E = {E} times a multiple of {step}")
+    N = features // E
+    if not fmt and X.dtype is not torch.float16:
+        raise ValueError("int8 weights take contiguous fp16 X")
+    _need_pair(weight, fmt, features, K, X, name)
+    nbytes = grouped_workspace_bytes(M, K, P, E, N, fmt, max_outliers)
+    if nbytes == 0:
+        raise ValueError(f"bad shape for a grouped product: M={M} K={K} P={P} E={E} N={N} max_outliers={max_outliers}")
+    return fmt, N, nbytes
+
+
+def route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> Routing:
+    """Routing of T tokens from their router logits [T, E] (fp16, bf16 or fp32; -inf: the expert is
+    off; E <= 512, top_k <= 16): lists as in ``moe_layer``, and the pairs of token and expert in
+    order of expert and then token. The same inputs give the same order."""
+    T, E = _need_logits(logits, top_k)
     nbytes = _route_workspace_bytes(T, E)
     i32 = torch.int32
     r = Routing(logits.new_empty((T, top_k), dtype=i32), logits.new_empty((T, top_k), dtype=torch.float32),
@@ -166,27 +189,18 @@ def grouped_matmul(X: torch.Tensor, weight: tuple, offsets: torch.Tensor, rows: 
             raise ValueError("rows must be an int32 tensor [P]")
         P = rows.shape[0]
         groups.need_vector(rows, torch.int32, (P,), X, "rows")
-    fmt, features = _rows(weight, "weight")
-    step = 32 if gated else 16
-    if features % (step * E):
-        raise ValueError(f"weight has {features} output features: not E = {E} times a multiple of {step}")
-    N = features // E
-    if not fmt and (X.dtype is not torch.float16 or ld != K):
+    fmt, N, nbytes = _need_experts(weight, M, K, P, E, gated, max_outliers, X, "weight")
+    if not fmt and ld != K:
         raise ValueError("int8 weights take contiguous fp16 X")
-    _need_pair(weight, fmt, features, K, X, "weight")
     width = N // 2 if gated else N
     if out is None:
         out = X.new_empty((P, width))
     else:
         _need_shape(out, X.dtype, (P, width), X.device, "out")
-    max_outliers = _outliers(K, max_outliers)
-    nbytes = grouped_workspace_bytes(M, K, P, E, N, fmt, max_outliers)
-    if nbytes == 0:
-        raise ValueError(f"bad shape for grouped_matmul: M={M} K={K} P={P} E={E} N={N} max_outliers={max_outliers}")
     workspace = mx4._scratch(workspace, nbytes, X)
     groups.launch("moe_grouped_matmul", X, X.data_ptr(), M, K, ld, dt, fmt, weight[0].data_ptr(), weight[1].data_ptr(),
                   E, N, offsets.data_ptr(), 0 if rows is None else rows.data_ptr(), P, int(gated), float(threshold),
-                  max_outliers, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+                  _outliers(K, max_outliers), out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -215,14 +229,27 @@ def combine(P: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
 def moe_prompt(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tuple, top_k: int,
                renormalize: bool = True, threshold: float = 6.0, max_outliers: int | None = None,
                out: torch.Tensor | None = None):
-    """(Y [T, D], ids, weights) as ``moe_layer``, for any number of tokens: ``route``, the gated
+    """(Y [T, D], ids, weights) as ``moe_layer``, for few or many tokens: ``route``, the gated
     product of gate_up, the product of down and ``combine``. The activations are quantized like the
     weights (MX4, or int8 with fp16 outlier columns, threshold and max_outliers as in
     ``grouped_matmul``), and the hidden values and each expert's outputs are rounded to X's type
-    between the launches, where ``moe_layer`` keeps both in 16 bits or more."""
-    T = mx4._need_rows(X, "X")[0]
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[0] != T:
-        raise ValueError(f"logits must be a 2-D fp16, bf16 or fp32 tensor with {T} rows")
+    between the launches, where ``moe_layer`` keeps both in 16 bits or more.
+
+    T * top_k is at most 2^24; with MX4 weights X and the hidden values [T * top_k, I], their rows
+    padded to 128 elements, have less than 2^33. Shapes that do not fit are refused before the first
+    launch.
+    """
+    M, D, ld, _ = mx4._need_rows(X, "X")
+    T, E = _need_logits(logits, top_k)
+    if T != M or logits.get_device() != X.get_device():
+        raise ValueError(f"logits must be [{M}, E] on {X.device}, got {tuple(logits.shape)} on {logits.device}")
+    P = T * top_k
+    fmt, N, _ = _need_experts(gate_up, T, D, P, E, True, max_outliers, X, "gate_up")
+    if not fmt and ld != D:
+        raise ValueError("int8 weights take contiguous fp16 X")
+    features = _need_experts(down, P, N // 2, P, E, False, max_outliers, X, "down")[1]
+    if out is not None:
+        _need_shape(out, X.dtype, (T, features), X.device, "out")
     r = route(logits, top_k, renormalize)
     h = grouped_matmul(X, gate_up, r.offsets, r.rows, True, threshold, max_outliers)
     p = grouped_matmul(h, down, r.offsets, None, False, threshold, max_outliers)

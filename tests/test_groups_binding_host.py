@@ -134,6 +134,31 @@ def test_prompt_of_other_tokens_than_the_logits_refused(calls, logits):
     assert calls == []
 
 
+@pytest.mark.parametrize("T,D,E,gate_up,down,k,kw", [
+    (20, 64, 4, pair(4 * 64, 64), pair(4 * 64, 160), 2, {}), (20, 64, 4, pair(4 * 64, 64), pair(4 * 64 + 16, 32), 2, {}),
+    (20, 64, 4, pair(4 * 48, 64), pair(4 * 64, 32), 2, {}), (20, 64, 4, pair(4 * 64, 192), pair(4 * 64, 32), 2, {}),
+    (20, 64, 4, pair(4 * 64, 64), (pair(4 * 64, 32)[0], pair(16, 32)[1]), 2, {}), (20, 64, 4, pair(4 * 64, 64), (None, None), 2, {}),
+    (20, 64, 4, pair(4 * 64, 64), pair(4 * 64, 32), 5, {}), (20, 64, 4, pair(4 * 64, 64), pair(4 * 64, 32), 0, {}),
+    (20, 64, 4, pair(4 * 64, 64), pair(4 * 64, 32), 2, dict(out=f16(19, 64))),
+    (20, 64, 4, pair(4 * 64, 64), pair(4 * 64, 32), 2, dict(out=f16(20, 64).bfloat16())),
+    (20, 64, 4, int8_pair(4 * 64, 64), int8_pair(4 * 64, 32), 2, dict(max_outliers=-1)),
+    (600000, 16, 1, pair(2 * 14336, 16), pair(16, 14336), 1, {}),     # the hidden values are 2^33 elements
+    ((1 << 21) + 1, 16, 8, pair(8 * 32, 16), pair(8 * 16, 16), 8, {}),    # more than 2^24 rows
+])
+def test_prompt_is_refused_before_its_first_launch(calls, T, D, E, gate_up, down, k, kw):
+    with pytest.raises(ValueError):
+        moe.moe_prompt(f16(T, D), torch.zeros(T, E), gate_up, down, k, **kw)
+    assert calls == []
+
+
+def test_prompt_over_int8_refuses_bf16_and_strided_rows_before_its_first_launch(calls):
+    w = int8_pair(4 * 64, 64), int8_pair(4 * 64, 32)
+    for x in (f16(20, 64).bfloat16(), f16(20, 128)[:, :64]):
+        with pytest.raises(ValueError):
+            moe.moe_prompt(x, torch.zeros(20, 4), *w, 2)
+        assert calls == []
+
+
 def test_cpu_tensors_are_refused_by_every_call(monkeypatch):
     launched = []
     monkeypatch.setattr(mx4, "_launch", lambda name, t, *args: launched.append(name))
