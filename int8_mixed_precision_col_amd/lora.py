@@ -33,7 +33,12 @@ def apply(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, id
     row stride of a multiple of 8). A [S, R, K] and B [S, N, R] hold S adapters of R ranks (a multiple of 8, at most 128);
     ids int32 [M] in any order; scales fp32 [S]; ranks int32 [S]: an adapter's own rank, what A
     and B hold beyond it is not looked at. out=Y adds in place.
+
+    For inference: there is no backward, so a call that autograd would have to record (one of its
+    tensors requires a gradient, outside torch.no_grad() and inference_mode()) is refused.
     """
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (Y, X, A, B, scales, out)):
+        raise ValueError("lora.apply has no backward: call it under torch.no_grad(), or with detached tensors")
     M, K, ldx, dt = mx4._need_rows(X, "X")
     my, N, ldy, dty = mx4._need_rows(Y, "Y")
     if my != M or dty != dt or Y.get_device() != X.get_device():

@@ -134,6 +134,20 @@ def test_prompt_of_other_tokens_than_the_logits_refused(calls, logits):
     assert calls == []
 
 
+@pytest.mark.parametrize("name", ["Y", "X", "A", "B", "scales", "out"])
+def test_lora_that_autograd_would_have_to_record_refused(calls, name):
+    t = lora_args(out=f16(5, 48))
+    t[name] = t[name].clone().requires_grad_()
+    with pytest.raises(ValueError, match="no backward"):
+        lora.apply(**t)
+    assert calls == []
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            assert lora.apply(**t).shape == (5, 48)
+    t[name] = t[name].detach()
+    assert lora.apply(**t).shape == (5, 48) and len(calls) == 3
+
+
 @pytest.mark.parametrize("T,D,E,gate_up,down,k,kw", [
     (20, 64, 4, pair(4 * 64, 64), pair(4 * 64, 160), 2, {}), (20, 64, 4, pair(4 * 64, 64), pair(4 * 64 + 16, 32), 2, {}),
     (20, 64, 4, pair(4 * 48, 64), pair(4 * 64, 32), 2, {}), (20, 64, 4, pair(4 * 64, 192), pair(4 * 64, 32), 2, {}),
