@@ -85,9 +85,10 @@ int moe_combine(const void* P, int64_t P_rows, int64_t D, int dtype, const int32
 /*
  * Low-rank adapters beside a shared projection: with a = ids[m],
  *   out[m] = Y[m] + scales[a] B_a (A_a X[m]),
- * fp32 sums (A X enters the second product with 16 significant bits in bf16 and 22 in fp16), one
- * rounding; rows whose id is outside 0 .. S - 1 have no adapter and keep Y[m]. A row of X with an
- * infinity or a NaN gives NaNs.
+ * fp32 sums, one rounding. The sums A X enter the second product whole in bf16, and in fp16 within
+ * 2^-23 of each or 2^-39 of their row's largest, whichever is more. Rows whose id is outside
+ * 0 .. S - 1 have no adapter and keep Y[m]. An infinity or a NaN in a row of X, or in what an
+ * adapter's ranks hold, gives NaNs wherever it enters, also against zeros.
  *   Y, X, out     [M, N], [M, K], [M, N], row strides ldy, ldx, ldo, dtype MX4_F16 or MX4_BF16.
  *                 out may be Y (then ldo = ldy): the adapters are added in place.
  *   A, B          [S, R, K] and [S, N, R] contiguous, dtype; 1 <= S <= 1024, R a multiple of 8,

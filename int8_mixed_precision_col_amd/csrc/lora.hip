@@ -6,9 +6,13 @@
 // what bounds them is reading X, Y and the adapters and writing out. k_lora_shrink: V = A X over
 // a part of K for a tile of up to 64 rows of one adapter, fp32 sums to scratch (parts of K as
 // few as fill the chip). k_lora_expand: the tile's V, summed over the parts, against a range of
-// features. V enters the matrix instructions as two parts, its rounding to the type and what that left
-// (bf16 16 bits together, fp16 22 under a power of two per row that keeps both in range); the
-// output's own rounding is to 8 and 11 bits.
+// features. V enters the matrix instructions as parts of the type, each the rounding of what those
+// before it left: in bf16 three, all 24 bits of an fp32 sum; in fp16 two, within 2^-23 of a value, or
+// 2^-39 of its row's largest where that is more (a power of two per row brings the largest to
+// 2^14 .. 2^15, and fp16 ends at 2^-24). Where an adapter nearly cancels its projection those bits are
+// what is left. The third part's cost, us in a graph: rank 16 to 64 none to 2% (4096 x 8192 x 8192 of
+// rank 32 65.5 -> 65.6, 256 x 4096 x 4096 of 16 16.1 -> 16.4), rank 96 and 128 1 to 4% (2048 x 4096 x
+// 14336 59.0 -> 61.0, 3000 x 8192 x 10240 84 -> 86).
 //
 // Rows in order: up to 64 rows every workgroup orders for itself by comparing the ids (no launch);
 // beyond, one workgroup sorts them first (k_lora_order).
@@ -23,6 +27,8 @@ namespace i8mm {
 constexpr int kLoraFew = 64;  // rows that each workgroup orders by itself
 constexpr int kLoraWaves = 8;
 constexpr int kLoraSplits = 8;  // parts of K at most
+template <class T>
+constexpr int kLoraParts = T::bf ? 3 : 2;  // of V's values
 
 // ---- rows by adapter ----
 
@@ -342,7 +348,7 @@ struct LoraExpand {
                                                   min(32 * s + 8 * lq, a.R - 8));
   }
   template <int LR>
-  __device__ __forceinline__ void multiply(Operands& o, int n, const typename T::elem (&v)[2][kLoraRows][LR],
+  __device__ __forceinline__ void multiply(Operands& o, int n, const typename T::elem (&v)[kLoraParts<T>][kLoraRows][LR],
                                            const float* row_scale) const {
     if (rank < 32 * KS) {  // ranks past this adapter's may hold anything
 #pragma unroll
@@ -363,7 +369,7 @@ struct LoraExpand {
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < kLoraParts<T>; ++p) {
           const v4u x = *reinterpret_cast<const v4u*>(&v[p][r][32 * s + 8 * lq]);
           acc[0] = T::mfma(o.b[0][s], x, acc[0]);
           acc[1] = T::mfma(o.b[1][s], x, acc[1]);
@@ -378,11 +384,21 @@ struct LoraExpand {
   }
 };
 
-// V of the tile's rows: LPR lanes to a row, 4 ranks each; the parts of K, up to SPLITS, together.
-template <class T, int KS, int THREADS, int SPLITS, int LR>
-__device__ __forceinline__ void lora_gather_v(const LoraArgs& a, const LoraTile& tile, const int* row_of,
-                                              typename T::elem (&v)[2][kLoraRows][LR], float* row_scale) {
-  typedef typename T::elem v4e __attribute__((ext_vector_type(4)));
+// f as a sum of kLoraParts<T> values of the type.
+template <class T>
+__device__ __forceinline__ void lora_parts(float f, typename T::elem (&part)[kLoraParts<T>]) {
+#pragma unroll
+  for (int p = 0; p < kLoraParts<T>; ++p) {
+    part[p] = T::round(f);
+    f -= static_cast<float>(part[p]);
+  }
+}
+
+// V of the tile's rows: LPR lanes to a row, 4 ranks each; the parts of K, up to SPLITS, together. put(r,
+// c, f): ranks c .. c + 3 of row r of the tile.
+template <class T, int KS, int THREADS, int SPLITS, class F>
+__device__ __forceinline__ void lora_gather_v(const LoraArgs& a, const LoraTile& tile, const int* row_of, float* row_scale,
+                                              F put) {
   constexpr int LPR = KS == 1 ? 8 : KS == 2 ? 16 : 32, RPP = THREADS / LPR;
   const int c = 4 * (threadIdx.x % LPR), R16 = (a.R + 15) & ~15;
   for (int r = threadIdx.x / LPR; r < tile.rows; r += RPP) {
@@ -405,17 +421,7 @@ __device__ __forceinline__ void lora_gather_v(const LoraArgs& a, const LoraTile&
       up = ldexpf(1.0f, min(max(e, -126), 126));
       down = ldexpf(1.0f, -min(max(e, -126), 126));
     }
-    v4e hi, lo;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float f = sum[e] * up;
-      hi[e] = T::round(f);
-      lo[e] = T::round(f - static_cast<float>(hi[e]));
-    }
-    if (c < 32 * KS) {
-      *reinterpret_cast<v4e*>(&v[0][r][c]) = hi;
-      *reinterpret_cast<v4e*>(&v[1][r][c]) = lo;
-    }
+    if (c < 32 * KS) put(r, c, sum * up);
     if (c == 0) row_scale[r] = down * (a.scales ? a.scales[tile.adapter] : 1.0f);
   }
 }
@@ -436,13 +442,26 @@ __device__ __forceinline__ void lora_copy_rows(const LoraArgs& a, const LoraTile
 // A workgroup takes a tile's rows and `span` features.
 template <class T, int KS, int J, int LR>
 __device__ __forceinline__ void lora_expand(const LoraArgs& a, const LoraTile& tile, int rank, const int* row_of,
-                                            typename T::elem (&v)[2][kLoraRows][LR], float* row_scale, int n0, int n1) {
+                                            typename T::elem (&v)[kLoraParts<T>][kLoraRows][LR], float* row_scale, int n0,
+                                            int n1) {
+  typedef typename T::elem v4e __attribute__((ext_vector_type(4)));
   constexpr int step = 32 * kLoraWaves;
   const LoraExpand<T, KS, J> e(a, tile, rank, row_of, n1);
   int n = n0 + 32 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   typename LoraExpand<T, KS, J>::Operands x, y;
   e.load(x, n);
-  lora_gather_v<T, KS, 64 * kLoraWaves, kLoraSplits>(a, tile, row_of, v, row_scale);
+  lora_gather_v<T, KS, 64 * kLoraWaves, kLoraSplits>(a, tile, row_of, row_scale, [&](int r, int c, v4f f) {
+    v4e part[kLoraParts<T>];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      typename T::elem of[kLoraParts<T>];
+      lora_parts<T>(f[e], of);
+#pragma unroll
+      for (int p = 0; p < kLoraParts<T>; ++p) part[p][e] = of[p];
+    }
+#pragma unroll
+    for (int p = 0; p < kLoraParts<T>; ++p) *reinterpret_cast<v4e*>(&v[p][r][c]) = part[p];
+  });
   lds_barrier();
   for (; n < n1; n += 2 * step) {
     e.load(y, n + step);
@@ -455,9 +474,9 @@ __device__ __forceinline__ void lora_expand(const LoraArgs& a, const LoraTile& t
 
 template <class T, int KS>
 __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_expand(LoraArgs a, int span) {
-  constexpr int LR = 32 * KS + 8;  // padded row of V in LDS
+  constexpr int LR = 32 * KS + 8;  // padded row of a part of V in LDS
   __shared__ int row_of[kLoraRows];
-  __shared__ __attribute__((aligned(16))) typename T::elem v[2][kLoraRows][LR];
+  __shared__ __attribute__((aligned(16))) typename T::elem v[kLoraParts<T>][kLoraRows][LR];
   __shared__ float row_scale[kLoraRows];
   LoraTile tile;
   if (!lora_tile(a, row_of, tile)) return;
@@ -473,7 +492,8 @@ __global__ __launch_bounds__(64 * kLoraWaves) void k_lora_expand(LoraArgs a, int
 }
 
 // For more than kLoraFew rows. A tile's rows share B: each of four waves has 16 of the rows,
-// with their V in registers, and B comes 128 features at a time through LDS (two buffers, filled by
+// with their V's parts in registers (V itself comes through LDS in fp32: the parts of rank 128 would leave
+// room for one workgroup per CU), and B comes 128 features at a time through LDS (two buffers, filled by
 // DMA), read by all four. Of eight blocks of 16 of its rows, block h has the features 8 c + h, so that
 // a lane has 8 consecutive features of four rows and 16 lanes together 256 contiguous bytes of a row.
 // Y is asked for two steps ahead, and nothing is under a condition, as above.
@@ -516,18 +536,19 @@ struct LoraStaged {
   }
 };
 
-// SPLITS: parts of K at most.
+// SPLITS: parts of K at most. The bound on registers, three workgroups per CU up to rank 64, then two, also
+// keeps the accumulators out of the other register file, which costs moves (rank 64 in bf16 took 201 of
+// 168 without it).
 template <class T, int KS, int SPLITS>
-__global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraArgs a, int span) {
+__global__ __launch_bounds__(64 * kStagedWaves, KS <= 2 ? 3 : 2) void k_lora_expand_staged(LoraArgs a, int span) {
   typedef LoraStaged<T, KS> Staged;
   typedef typename Staged::v8e v8e;
-  constexpr int LR = 32 * KS + 8;  // padded row of V in LDS
-  typedef typename T::elem Parts[2][kLoraRows][LR];
+  typedef float V[kLoraRows][32 * KS + 4];  // padded rows
   __shared__ int row_of[kLoraRows];
   __shared__ float row_scale[kLoraRows];
   __shared__ __attribute__((aligned(1024))) char buf0[Staged::BYTES];
-  __shared__ __attribute__((aligned(1024))) char buf1[sizeof(Parts) > Staged::BYTES ? sizeof(Parts) : Staged::BYTES];
-  Parts& v = *reinterpret_cast<Parts*>(buf1);  // until it is in registers
+  __shared__ __attribute__((aligned(1024))) char buf1[sizeof(V) > Staged::BYTES ? sizeof(V) : Staged::BYTES];
+  V& v = *reinterpret_cast<V*>(buf1);  // until it is in registers
   LoraTile tile;
   if (!lora_tile<true>(a, row_of, tile)) return;
   const int n0 = tile.part * span, n1 = min(n0 + span, a.N);
@@ -555,7 +576,8 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
   v4u y0[4], y1[4];
   load_y(y0, n0);
   load_y(y1, n0 + 128);
-  lora_gather_v<T, KS, 64 * kStagedWaves, SPLITS>(a, tile, row_of, v, row_scale);
+  lora_gather_v<T, KS, 64 * kStagedWaves, SPLITS>(a, tile, row_of, row_scale,
+                                                  [&](int r, int c, v4f f) { *reinterpret_cast<v4f*>(&v[r][c]) = f; });
   wait_and_barrier<0>();
   if (16 * wave >= tile.rows) {  // no rows: only its share of B
     lds_barrier();
@@ -569,12 +591,22 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
     __builtin_amdgcn_s_waitcnt(0);
     return;
   }
-  v4u x[2][KS];
+  v4u x[kLoraParts<T>][KS];
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
+  for (int s = 0; s < KS; ++s) {
+    const float* f = &v[min(16 * wave + st.l16, tile.rows - 1)][32 * s + 8 * st.lq];
+    const v4f half[2] = {*reinterpret_cast<const v4f*>(f), *reinterpret_cast<const v4f*>(f + 4)};
+    v8e part[kLoraParts<T>];
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-      x[p][s] = *reinterpret_cast<const v4u*>(&v[p][min(16 * wave + st.l16, tile.rows - 1)][32 * s + 8 * st.lq]);
+    for (int e = 0; e < 8; ++e) {
+      typename T::elem of[kLoraParts<T>];
+      lora_parts<T>(half[e >> 2][e & 3], of);
+#pragma unroll
+      for (int p = 0; p < kLoraParts<T>; ++p) part[p][e] = of[p];
+    }
+#pragma unroll
+    for (int p = 0; p < kLoraParts<T>; ++p) x[p][s] = __builtin_bit_cast(v4u, part[p]);
+  }
   float sc[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sc[e] = row_scale[min(16 * wave + 4 * st.lq + e, tile.rows - 1)];
@@ -590,8 +622,8 @@ __global__ __launch_bounds__(64 * kStagedWaves) void k_lora_expand_staged(LoraAr
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
         const v4u b = st.piece(buf, h, s);
-        acc[h] = T::mfma(x[0][s], b, acc[h]);
-        acc[h] = T::mfma(x[1][s], b, acc[h]);
+#pragma unroll
+        for (int p = 0; p < kLoraParts<T>; ++p) acc[h] = T::mfma(x[p][s], b, acc[h]);
       }
     v8e out[4];
 #pragma unroll

@@ -391,6 +391,52 @@ def test_lora_many_rows_in_parts(M, K, N, R, S, dtype, ranked):
 
 
 @pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("M,R,S,ranked", [(1, 8, 1, False), (9, 24, 2, True), (30, 48, 1, False), (64, 128, 3, True),
+                                          (65, 16, 2, False), (200, 56, 3, True), (130, 88, 1, True), (700, 128, 4, False)])
+def test_lora_keeps_all_of_a_sum(M, R, S, ranked, dtype):
+    """V of 24 bits whose first nine cancel between two ranks: whole numbers below 2^24 all along (V, its parts, and
+    the sums of one rank less another), so bf16 has one rounding, the output's. Two fp16 parts leave out at most
+    one unit of a number below 2^24 (11 bits, and 11 of the 12 of what they leave), so 1 each of two ranks."""
+    announce(f"lora of 24-bit sums M={M} R={R} S={S} {dtype} ranked={ranked}")
+    g, K, N = gen(M + R), 48, 80
+    whole = lambda lo, hi, *shape: torch.randint(lo, hi + 1, shape, generator=g)  # noqa: E731
+    X, A = whole(-127, 127, M, K), whole(0, 1, S, R, K) * 2 - 1
+    X[:, 0] = (whole(64, 126, M) << 7) * (whole(0, 1, M) * 2 - 1)
+    A[:, :, 0], A[:, :, 1] = 1 << 10, whole(-127, 127, S, R)   # V: 64 .. 126 times 2^17, and up to 173 * 127 beside it
+    ranks = whole(2, R, S) if ranked else torch.full((S,), R)
+    B = torch.zeros((S, N, R), dtype=torch.int64)
+    for a in range(S):
+        for n in range(N):
+            i, j = torch.randperm(int(ranks[a]), generator=g)[:2].tolist()
+            B[a, n, i], B[a, n, j] = 1, -1
+    Y, ids = whole(-64, 64, M, N), whole(0, S - 1, M)
+    V = torch.einsum("mk,mrk->mr", X, A[ids])
+    assert int(V.abs().min()) > 1 << 22 and int(V.abs().max()) < 1 << 24
+    want = (Y + torch.einsum("mr,mnr->mn", V, B[ids])).double().numpy()
+    t = [v.to(dtype) for v in (Y, X, A, B)]
+    assert all(torch.equal(a.long(), b) for a, b in zip(t, (Y, X, A, B)))
+    got = lora.apply(*(v.cuda() for v in t), ids.int().cuda(), ranks=ranks.int().cuda() if ranked else None)
+    close(got, want, np.full(want.shape, 2.0 if dtype == F16 else 0.0))
+
+
+@pytest.mark.parametrize("M", [3, 90])
+def test_lora_small_values_beside_a_large_one_in_fp16(M):
+    """A value of V far below its row's largest is off by at most 2^-39 of the largest."""
+    announce(f"lora, V from 2^-10 to 2^30, M={M}")
+    X, A, B = torch.zeros((M, 16)), torch.zeros((1, 16, 16)), torch.zeros((1, 32, 16))
+    X[:, 0], X[:, 1] = 2.0 ** 15, (1024 + torch.arange(M) % 1024) * 2.0 ** -15
+    A[0, 0, 0] = 2.0 ** 15
+    small = torch.arange(1, 16)
+    A[0, small, 1] = torch.exp2(5.0 - small)            # V: 2^30, and 11 bits from 1 down to 2^-14
+    B[0, small, small] = 1.0
+    got = lora.apply(torch.zeros((M, 32), dtype=F16, device="cuda"), X.half().cuda(), A.half().cuda(), B.half().cuda(),
+                     torch.zeros(M, dtype=torch.int32, device="cuda"))
+    want = (X.double() @ A[0].double().T) @ B[0].double().T
+    assert float(want.max()) < 2 and float(want[:, 1:16].min()) > 0
+    close(got, want.numpy(), np.full(want.shape, 2.0 ** -9))
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
 @pytest.mark.parametrize("M", [1, 40, 150])
 def test_lora_strided_and_ids_out_of_range(M, dtype):
     announce(f"lora strided M={M} {dtype}")
