@@ -30,6 +30,12 @@ def close(y, want, bound):
     assert worst <= 1, worst
 
 
+def nearest(x, dtype):
+    """Values of the type nearest to float64 x (below its largest)."""
+    last = np.maximum(np.frexp(x)[1] - (11 if dtype == F16 else 8), -24 if dtype == F16 else -133)
+    return np.ldexp(np.round(np.ldexp(x, -last)), last)
+
+
 def gen(seed):
     return torch.Generator().manual_seed(seed)
 
@@ -245,6 +251,43 @@ def test_grouped_int8_without_and_with_many_outliers():
     x = activations(40, 528, F16, 9, 40)
     y = moe.grouped_matmul(x, weight, i32([0, 30, 30, 80]), i32(rows), max_outliers=8)
     assert bool(torch.isnan(y[:80]).all()) and int(torch.count_nonzero(y[80:])) == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, B16])
+@pytest.mark.parametrize("M", [5, 300])
+def test_gated_epilogue_at_every_size_of_the_gate(M, dtype):
+    """silu(gate) up of gates and ups that are exact: eight powers of two, each in a block of its own. The result
+    is within 1.23 |gate| + 7 units of 2^-24 and one rounding, or 0 where exp is above 2^126. exp is 2^p with p =
+    -gate log2(e): p's rounding is up to 1 unit of p and the fp32 constant is off by 0.224 units, and an error of p
+    is |gate| times as many units of exp; then the exponential instruction 2, 1 + exp 1, the reciprocal
+    instruction 2, two products 2. Between -20 and -60 the ups are as large as it takes for every bit to count."""
+    I, g = 16384, gen(M)
+    announce(f"gated epilogue, {M} rows of {I} features {dtype}")
+    mantissa = lambda: torch.randint(128, 256, (I,), generator=g).double()  # noqa: E731
+    kind = torch.arange(I) % 4                          # large and negative twice, ordinary, far out
+    size = torch.where(kind < 2, 20 + 40 * torch.rand(I, generator=g).double(),
+                       torch.where(kind == 2, 8 * torch.rand(I, generator=g).double() + 0.01, 60 + 400 * torch.rand(I, generator=g).double()))
+    gate = mantissa() * torch.exp2(torch.floor(torch.log2(size)) - 7)
+    gate = torch.where((kind < 2) | (torch.rand(I, generator=g) < 0.5), -gate, gate)
+    silu = gate / (1 + torch.exp(-gate))
+    lift = torch.where(kind < 2, -torch.floor(torch.log2(silu.abs())), 0.0) + torch.randint(-6, 7, (I,), generator=g)
+    up = mantissa() * torch.exp2(lift - 7)
+    w = torch.zeros((2 * I, 8, 32), dtype=torch.float64)
+    for half, v in ((0, gate), (I, up)):
+        whole = (v.abs() / torch.exp2(torch.floor(torch.log2(v.abs())) - 7)).long()
+        for b in range(8):
+            w[half:half + I, b, 0] = (whole >> b & 1) * torch.exp2(torch.floor(torch.log2(v.abs())) - 7 + b) * torch.sign(v)
+    x = torch.zeros((M, 8, 32), dtype=dtype)
+    x[:, :, 0] = 1
+    weight = mx4.prepare_weight(w.view(2 * I, 256).to(B16).cuda(), 1)
+    y = moe.grouped_matmul(x.view(M, 256).cuda(), weight, i32([0, M]), gated=True)
+    want = (silu * up).numpy()[None]
+    gone = (gate < -126 * np.log(2) + 1e-4).numpy()     # the reciprocal instruction has no result below 2^-126: 0
+    bound = np.abs(want) * np.where(gone, 1, (1.23 * gate.abs().numpy() + 7.01) * ref.U)
+    close(y[:1], want, bound)
+    got = f64(y[:1])                                    # and no other value than the two ends' roundings allow
+    assert ((nearest(want - bound, dtype) <= got) & (got <= nearest(want + bound, dtype))).all()
+    assert torch.equal(y, y[:1].expand(M, I))
 
 
 @pytest.mark.parametrize("fmt", ["mx4", "int8"])
