@@ -229,6 +229,42 @@ def test_grouped_rows_out_of_range_are_zeros_and_offsets_stay_inside(fmt):
         assert bool((guard[512:] == 3.0).all())
 
 
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+@pytest.mark.parametrize("E,P,N", [(3, 1500, 10272), (8, 1600, 5152), (300, 2000, 64)])
+def test_grouped_offsets_that_mean_nothing_stay_inside_at_each_tile_shape(E, P, N, fmt):
+    """Tiles of 256 and, int8, of 128 rows; groups over several chunks of 64: descending, overlapping and far offsets
+    write nothing around Y or the workspace, and the next call is right."""
+    announce(f"grouped, bad offsets, E={E} P={P} N={N} {fmt}")
+    x, (weight, values) = activations(50, 272, F16, E), weights_of(E, N, 272, fmt, F16, P)
+    rows, g = i32(np.arange(P) % 50), gen(E)
+    need = moe.grouped_workspace_bytes(50, 272, P, E, N, int(fmt == "mx4"))
+    guard, work = torch.full((P * N + 512,), 3.0, dtype=F16, device="cuda"), torch.full((need + 512,), 0xa5, dtype=torch.uint8, device="cuda")
+    y, ws = guard[256:256 + P * N].view(P, N), work[256:256 + need]
+    far = [-(1 << 31), (1 << 31) - 1, 1 << 30, -1]
+    for bad in (np.linspace(P, 0, E + 1).astype(int), np.arange(E + 1) % 2 * P, np.arange(1, E + 2) % 2 * P,
+                torch.randint(-P, 2 * P, (E + 1,), generator=g).numpy(), np.resize(far, E + 1), np.full(E + 1, P)):
+        moe.grouped_matmul(x, weight, i32(bad), rows, out=y, workspace=ws)
+        torch.cuda.synchronize()
+        for t in (guard, work):
+            assert bool((t[:256] == t[0]).all()) and bool((t[-256:] == t[0]).all())
+        assert float(guard[0]) == 3.0 and int(work[0]) == 0xa5
+    offsets = np.sort(np.concatenate(([0], torch.randint(0, P, (E,), generator=g).numpy())))
+    moe.grouped_matmul(x, weight, i32(offsets), rows, out=y, workspace=ws)
+    close(y, *want_grouped(x, values, fmt, offsets, np.arange(P) % 50, P, False))
+
+
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,n", [(129, 700), (500, 300), (1024, 2300)])
+def test_grouped_over_hundreds_of_experts(E, n, gated, fmt):
+    announce(f"grouped over {E} experts, {n} rows, gated={gated} {fmt}")
+    x, (weight, values) = activations(70, 144, F16, n), weights_of(E, 32, 144, fmt, F16, E)
+    sizes = np.bincount(torch.randint(0, E, (n,), generator=gen(E)).numpy(), minlength=E)
+    sizes[: E // 3] = 0
+    P = int(sizes.sum())
+    check_grouped(x, weight, values, fmt, sizes, np.arange(P) * 7 % 70, P, gated)
+
+
 def test_grouped_nonfinite_rows_and_weights():
     announce("grouped mx4, non-finite blocks")
     x = activations(30, 272, F16, 5)
