@@ -37,8 +37,6 @@ def apply(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, id
     For inference: there is no backward, so a call that autograd would have to record (one of its
     tensors requires a gradient, outside torch.no_grad() and inference_mode()) is refused.
     """
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (Y, X, A, B, scales, out)):
-        raise ValueError("lora.apply has no backward: call it under torch.no_grad(), or with detached tensors")
     M, K, ldx, dt = mx4._need_rows(X, "X")
     my, N, ldy, dty = mx4._need_rows(Y, "Y")
     if my != M or dty != dt or Y.get_device() != X.get_device():
@@ -60,6 +58,9 @@ def apply(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, id
         if (mo, no, dto) != (M, N, dt) or out.get_device() != X.get_device():
             raise ValueError(f"out must be {X.dtype} [{M}, {N}] on {X.device}, got {out.dtype} {tuple(out.shape)} on "
                              f"{out.device}")
+    if ((Y.requires_grad or X.requires_grad or A.requires_grad or B.requires_grad or out.requires_grad
+         or (scales is not None and scales.requires_grad)) and torch.is_grad_enabled()):
+        raise ValueError("lora.apply has no backward: call it under torch.no_grad(), or with detached tensors")
     nbytes = workspace_bytes(M, K, S, R)
     if nbytes == 0:
         raise ValueError(f"bad shape for lora.apply: M={M} K={K} S={S} R={R}")

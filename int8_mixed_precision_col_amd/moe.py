@@ -147,6 +147,18 @@ def _need_experts(weight: tuple, M: int, K: int, P: int, E: int, gated: bool, ma
     return fmt, N, nbytes
 
 
+def _grouped(X: torch.Tensor, M: int, K: int, ld: int, dt: int, weight: tuple, experts: tuple, offsets: torch.Tensor,
+             E: int, rows: torch.Tensor | None, P: int, gated: bool, threshold: float, max_outliers: int | None,
+             workspace: torch.Tensor | None, out: torch.Tensor) -> torch.Tensor:
+    """The launch of ``grouped_matmul``, its arguments checked; experts as from ``_need_experts``."""
+    fmt, N, nbytes = experts
+    workspace = mx4._scratch(workspace, nbytes, X)
+    groups.launch("moe_grouped_matmul", X, X.data_ptr(), M, K, ld, dt, fmt, weight[0].data_ptr(),
+                  weight[1].data_ptr(), E, N, offsets.data_ptr(), 0 if rows is None else rows.data_ptr(), P, int(gated),
+                  float(threshold), _outliers(K, max_outliers), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
 def route(logits: torch.Tensor, top_k: int, renormalize: bool = True) -> Routing:
     """Routing of T tokens from their router logits [T, E] (fp16, bf16 or fp32; -inf: the expert is
     off; E <= 512, top_k <= 16): lists as in ``moe_layer``, and the pairs of token and expert in
@@ -189,19 +201,15 @@ def grouped_matmul(X: torch.Tensor, weight: tuple, offsets: torch.Tensor, rows: 
             raise ValueError("rows must be an int32 tensor [P]")
         P = rows.shape[0]
         groups.need_vector(rows, torch.int32, (P,), X, "rows")
-    fmt, N, nbytes = _need_experts(weight, M, K, P, E, gated, max_outliers, X, "weight")
-    if not fmt and ld != K:
+    experts = _need_experts(weight, M, K, P, E, gated, max_outliers, X, "weight")
+    if not experts[0] and ld != K:
         raise ValueError("int8 weights take contiguous fp16 X")
-    width = N // 2 if gated else N
+    width = experts[1] // 2 if gated else experts[1]
     if out is None:
         out = X.new_empty((P, width))
     else:
         _need_shape(out, X.dtype, (P, width), X.device, "out")
-    workspace = mx4._scratch(workspace, nbytes, X)
-    groups.launch("moe_grouped_matmul", X, X.data_ptr(), M, K, ld, dt, fmt, weight[0].data_ptr(), weight[1].data_ptr(),
-                  E, N, offsets.data_ptr(), 0 if rows is None else rows.data_ptr(), P, int(gated), float(threshold),
-                  _outliers(K, max_outliers), out.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return out
+    return _grouped(X, M, K, ld, dt, weight, experts, offsets, E, rows, P, gated, threshold, max_outliers, workspace, out)
 
 
 def combine(P: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
@@ -239,18 +247,21 @@ def moe_prompt(X: torch.Tensor, logits: torch.Tensor, gate_up: tuple, down: tupl
     padded to 128 elements, have less than 2^33. Shapes that do not fit are refused before the first
     launch.
     """
-    M, D, ld, _ = mx4._need_rows(X, "X")
+    M, D, ld, dt = mx4._need_rows(X, "X")
     T, E = _need_logits(logits, top_k)
     if T != M or logits.get_device() != X.get_device():
         raise ValueError(f"logits must be [{M}, E] on {X.device}, got {tuple(logits.shape)} on {logits.device}")
     P = T * top_k
-    fmt, N, _ = _need_experts(gate_up, T, D, P, E, True, max_outliers, X, "gate_up")
-    if not fmt and ld != D:
+    first = _need_experts(gate_up, T, D, P, E, True, max_outliers, X, "gate_up")
+    if not first[0] and ld != D:
         raise ValueError("int8 weights take contiguous fp16 X")
-    features = _need_experts(down, P, N // 2, P, E, False, max_outliers, X, "down")[1]
+    I = first[1] // 2
+    second = _need_experts(down, P, I, P, E, False, max_outliers, X, "down")
     if out is not None:
-        _need_shape(out, X.dtype, (T, features), X.device, "out")
+        _need_shape(out, X.dtype, (T, second[1]), X.device, "out")
     r = route(logits, top_k, renormalize)
-    h = grouped_matmul(X, gate_up, r.offsets, r.rows, True, threshold, max_outliers)
-    p = grouped_matmul(h, down, r.offsets, None, False, threshold, max_outliers)
+    h = _grouped(X, T, D, ld, dt, gate_up, first, r.offsets, E, r.rows, P, True, threshold, max_outliers, None,
+                 X.new_empty((P, I)))
+    p = _grouped(h, P, I, I, dt, down, second, r.offsets, E, None, P, False, threshold, max_outliers, None,
+                 X.new_empty((P, second[1])))
     return combine(p, r.slots, r.weights, out), r.ids, r.weights
