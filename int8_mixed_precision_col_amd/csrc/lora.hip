@@ -6,13 +6,13 @@
 // what bounds them is reading X, Y and the adapters and writing out. k_lora_shrink: V = A X over
 // a part of K for a tile of up to 64 rows of one adapter, fp32 sums to scratch (parts of K as
 // few as fill the chip). k_lora_expand: the tile's V, summed over the parts, against a range of
-// features. V enters the matrix instructions as parts of the type, each the rounding of what those
-// before it left: in bf16 three, all 24 bits of an fp32 sum; in fp16 two, within 2^-23 of a value, or
+// features. V enters the matrix instructions as parts of the type, each of what those before it
+// left: in bf16 three, all 24 bits of an fp32 sum; in fp16 two, within 2^-23 of a value, or
 // 2^-39 of its row's largest where that is more (a power of two per row brings the largest to
 // 2^14 .. 2^15, and fp16 ends at 2^-24). Where an adapter nearly cancels its projection those bits are
-// what is left. The third part's cost, us in a graph: rank 16 to 64 none to 2% (4096 x 8192 x 8192 of
-// rank 32 65.5 -> 65.6, 256 x 4096 x 4096 of 16 16.1 -> 16.4), rank 96 and 128 1 to 4% (2048 x 4096 x
-// 14336 59.0 -> 61.0, 3000 x 8192 x 10240 84 -> 86).
+// what is left. The third part's cost, us in a graph: up to rank 64 less than 2% (4096 x 8192 x 8192 of
+// rank 32 65.5 -> 65.6, 256 x 4096 x 4096 of 16 16.1 -> 16.4), at 96 and 128 up to 3% (2048 x 4096 x
+// 14336 59.0 -> 60.9, 3000 x 8192 x 10240 83.9 -> 85.6).
 //
 // Rows in order: up to 64 rows every workgroup orders for itself by comparing the ids (no launch);
 // beyond, one workgroup sorts them first (k_lora_order).
@@ -384,12 +384,16 @@ struct LoraExpand {
   }
 };
 
-// f as a sum of kLoraParts<T> values of the type.
+// f as a sum of kLoraParts<T> values of the type. bf16: 8 bits at a time, cut off rather than rounded, so
+// that the largest fp32 values do not become infinite.
 template <class T>
 __device__ __forceinline__ void lora_parts(float f, typename T::elem (&part)[kLoraParts<T>]) {
 #pragma unroll
   for (int p = 0; p < kLoraParts<T>; ++p) {
-    part[p] = T::round(f);
+    if constexpr (T::bf)
+      part[p] = __builtin_bit_cast(typename T::elem, static_cast<unsigned short>(__builtin_bit_cast(unsigned, f) >> 16));
+    else
+      part[p] = T::round(f);
     f -= static_cast<float>(part[p]);
   }
 }

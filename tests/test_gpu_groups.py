@@ -499,6 +499,20 @@ def test_lora_keeps_all_of_a_sum(M, R, S, ranked, dtype):
 
 
 @pytest.mark.parametrize("M", [3, 90])
+def test_lora_the_largest_sum_in_bf16(M):
+    """V of fp32's largest value, 2^128 - 2^104, whose rounding to 8 bits would be infinite: brought down by B
+    it is 2^108 - 2^84, which rounds to 2^108."""
+    announce(f"lora, V of 2^128 - 2^104, M={M}")
+    X = torch.zeros((M, 32), dtype=B16)
+    X[:, :24] = torch.exp2(127.0 - torch.arange(24)).to(B16)
+    A, B = torch.ones((1, 8, 32), dtype=B16), torch.zeros((1, 48, 8), dtype=B16)
+    B[0, :, 5] = 2.0 ** -20
+    got = lora.apply(torch.zeros((M, 48), dtype=B16, device="cuda"), X.cuda(), A.cuda(), B.cuda(),
+                     torch.zeros(M, dtype=torch.int32, device="cuda"))
+    assert bool((got == 2.0 ** 108).all())
+
+
+@pytest.mark.parametrize("M", [3, 90])
 def test_lora_small_values_beside_a_large_one_in_fp16(M):
     """A value of V far below its row's largest is off by at most 2^-39 of the largest."""
     announce(f"lora, V from 2^-10 to 2^30, M={M}")
