@@ -665,6 +665,53 @@ def test_graph_capture_and_replay(T, fmt):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_route_of_as_many_tokens_as_there_may_be():
+    T, E, k = 1 << 24, 3, 2
+    announce(f"route T={T}")
+    x = torch.randn((T, E), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    x[::5, 1] = -float("inf")
+    x[::35] = -float("inf")
+    r = moe.route(x, k)
+    top, ids = torch.sort(x, dim=1, descending=True, stable=True)
+    ids = torch.where(top > -float("inf"), ids, E)[:, :k].reshape(-1)
+    key, order = torch.sort(ids, stable=True)
+    n = int((key < E).sum())
+    assert torch.equal(r.ids.view(-1).long(), torch.where(ids < E, ids, -1))
+    assert torch.equal(r.offsets.long(), torch.searchsorted(key, torch.arange(E + 1, device="cuda")))
+    assert torch.equal(r.rows[:n].long(), order[:n] // k) and bool((r.rows[n:] == -1).all())
+    slots = torch.full((T * k,), -1, device="cuda")
+    slots[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(r.slots.view(-1).long(), slots)
+
+
+@pytest.mark.parametrize("fmt", ["mx4", "int8"])
+def test_grouped_of_as_many_rows_as_there_may_be(fmt):
+    """2^24 rows of Y, and as many of X: each as in a product of a few."""
+    P = 1 << 24
+    announce(f"grouped P={P} {fmt}")
+    x, (weight, values) = activations(8, 16, F16, 90, 0), weights_of(3, 16, 16, fmt, F16, 91)
+    small = torch.cat([moe.grouped_matmul(x, weight, i32([8 * (i > e) for i in range(4)])) for e in range(3)])
+    close(small, *want_grouped(x, values, fmt, [0, 8, 16, 24], np.arange(24) % 8, 24, False))
+    offsets = [0, 100, (1 << 23) + 1, P - 9]
+    at = torch.arange(P, device="cuda")
+    want = small[(at >= offsets[1]) * 8 + (at >= offsets[2]) * 8 + at % 8]
+    want[offsets[3]:] = 0
+    many = x.repeat(P // 8, 1)
+    for got in (moe.grouped_matmul(x, weight, i32(offsets), (at % 8).int()), moe.grouped_matmul(many, weight, i32(offsets))):
+        assert torch.equal(got, want)
+
+
+def test_lora_of_as_many_rows_as_there_may_be():
+    M = 1 << 24
+    announce(f"lora M={M}")
+    t = lora_case(4096, 16, 16, 8, 2, B16, 92, False)
+    want = lora.apply(**t)
+    close(want, *want_lora(t))
+    big = {n: v.repeat(M // 4096, *[1] * (v.dim() - 1)) if n in ("X", "Y", "ids") else v for n, v in t.items()}
+    got = lora.apply(**big)
+    assert torch.equal(got.view(-1, 4096, 16), want.expand(M // 4096, 4096, 16))
+
+
 def test_grouped_offsets_beyond_32_bits():
     """Over 4 GB of expert weights and over 4 GB of outputs: the last expert's rows are right."""
     E, N, K = 1024, 4112, 2048
