@@ -49,7 +49,8 @@ int moe_route(const void* logits, int64_t T, int64_t E, int logits_dtype, int64_
  * Products grouped by expert: row p of Y, offsets[e] <= p < offsets[e + 1], is the product of
  * row rows[p] of X with expert e's N rows of the weight.
  *   weight_format 0: int8, as int8_mixed_matmul (the outlier columns are those of the whole of
- *                 X; more than max_outliers of them fill Y with NaN); X is fp16 and contiguous.
+ *                 X; more than max_outliers of them fill the experts' rows with NaN); X is fp16
+ *                 and contiguous.
  *                 1: MX4, as mx4_matmul (X is quantized in the call); threshold and
  *                 max_outliers are not looked at.
  *   X             [M, K], row stride ldx, dtype MX4_F16 or MX4_BF16; M and P at most 2^24; less

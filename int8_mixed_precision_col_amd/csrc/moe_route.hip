@@ -160,8 +160,8 @@ __device__ __forceinline__ int route_tokens(const RouteArgs& a, int64_t t0, int 
   return id;
 }
 
-// Exclusive prefix sum of n <= kMoeMaxExperts + 1 counts in LDS, in place of thread i's count;
-// returns it, with the sum of all in `total`. All threads of the workgroup take part.
+// Exclusive prefix sum of the threads' counts v, with the sum of all in `total`. All threads of the
+// workgroup take part.
 __device__ __forceinline__ int block_exclusive(int v, int tid, int* wave_sums, int& total) {
   int upto = wave_prefix_sum(v);
   if ((tid & 63) == 63) wave_sums[tid >> 6] = upto;

@@ -186,9 +186,11 @@ def grouped_matmul(X: torch.Tensor, weight: tuple, offsets: torch.Tensor, rows: 
 
     MX4 weights: fp16 or bf16 X, rounded to MX4 as in ``mx4.matmul``. int8 weights: fp16 X,
     decomposed as in ``binding.mixed_matmul`` (outlier columns are those of the whole of X; more than
-    max_outliers of them, without one any number up to 8192, give NaN).
+    max_outliers of them, without one any number up to 8192, give NaN). The workspace has room for
+    max_outliers columns of X in fp16: give a smaller number where all of X is too much.
     offsets int32 [E + 1] ascending from 0 and rows int32 [P] are on the GPU and stay there
-    (``route`` makes both). Rows of Y behind offsets[E], and rows whose index is outside X, are zeros.
+    (``route`` makes both). Rows of Y behind offsets[E] are zeros, and a row
+    whose index is outside X counts as zeros.
     """
     M, K, ld, dt = mx4._need_rows(X, "X")
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
